@@ -22,6 +22,9 @@ QN_OK, QN_ERR_NULL, QN_ERR_SHAPE, QN_ERR_ALIGN = 0, -1, -2, -3
 QN_ERR_UNSUPPORTED, QN_ERR_WORKSPACE, QN_ERR_HIP = -4, -5, -6
 QN_F32, QN_BF16 = 0, 1
 QN_OP_FWD, QN_OP_BWD_DX, QN_OP_LORA_GRADS, QN_OP_BWD_DX_DROPOUT = 0, 1, 2, 3
+QN_OP_FP8_FWD, QN_OP_FP8_BWD_DX = 4, 5
+QN_STATE_F32, QN_STATE_8BIT = 0, 1
+FP8_BLOCK, STATE_BLOCK = 128, 256
 BLOCKSIZE, GROUP = 64, 256
 
 EXPORTS = ("qn_status_string", "nf4_codebook", "nf4_quantize", "dq_quantize_scales",
@@ -30,7 +33,10 @@ EXPORTS = ("qn_status_string", "nf4_codebook", "nf4_quantize", "dq_quantize_scal
            "qlora_linear_fwd_dropout", "qlora_linear_bwd_dx_dropout", "fp4_codebook",
            "fp4_quantize", "dq_quantize_scales_fp8", "qlora_linear_fwd_noalloc",
            "dq_quantize_scales_centred", "nf4_quantize_dq", "nf4_quantize_dq_batch",
-           "qn_hbm_read_probe")
+           "qn_hbm_read_probe", "fp8_quantize_blocks", "fp8_quantize_rows", "fp8_dequant",
+           "fp8_matmul", "fp8_linear_fwd", "fp8_linear_bwd_dx", "lora_adamw_table_bytes",
+           "lora_adamw_table", "lora_grad_norm_workspace_bytes", "lora_grad_norm",
+           "lora_adamw_multi_step")
 
 
 class QnError(RuntimeError):
@@ -46,6 +52,24 @@ class qn_weight(ctypes.Structure):
                 ("blocksize", ctypes.c_int32), ("group", ctypes.c_int32),
                 ("quant_type", ctypes.c_int32), ("scale_type", ctypes.c_int32),
                 ("offset", ctypes.c_void_p)]
+
+
+class qn_fp8_weight(ctypes.Structure):
+    _fields_ = [("codes", ctypes.c_void_p), ("scale", ctypes.c_void_p),
+                ("N", ctypes.c_int64), ("K", ctypes.c_int64)]
+
+
+class qn_adamw_tensor(ctypes.Structure):
+    _fields_ = [("p", ctypes.c_void_p), ("g", ctypes.c_void_p), ("m", ctypes.c_void_p),
+                ("v", ctypes.c_void_p), ("m_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("p_bf16", ctypes.c_void_p),
+                ("n", ctypes.c_int64)]
+
+
+class qn_adamw_plan(ctypes.Structure):
+    _fields_ = [("chunks", ctypes.c_int64), ("bytes", ctypes.c_int64),
+                ("tensors", ctypes.c_int32), ("grad_dtype", ctypes.c_int32),
+                ("state", ctypes.c_int32), ("reserved", ctypes.c_int32)]
 
 
 _lib = None
@@ -92,6 +116,21 @@ def load_library():
         "qlora_linear_bwd_dx_dropout": (ctypes.c_int, [wp, vp, i64, vp, vp, i32, f32, f32, u64, vp,
                                                        vp, vp, sz, vp]),
     }
+    fp, ap, pp = (ctypes.POINTER(c) for c in (qn_fp8_weight, qn_adamw_tensor, qn_adamw_plan))
+    lin = [fp, vp, i64, vp, vp, i32, f32, vp, vp, vp, sz, vp]
+    sig.update({
+        "fp8_quantize_blocks": (ctypes.c_int, [vp, i32, i64, i64, vp, vp, vp]),
+        "fp8_quantize_rows": (ctypes.c_int, [vp, i64, i64, vp, vp, vp]),
+        "fp8_dequant": (ctypes.c_int, [fp, i32, vp, vp]),
+        "fp8_matmul": (ctypes.c_int, [fp, vp, vp, i64, i32, vp, vp]),
+        "fp8_linear_fwd": (ctypes.c_int, lin),
+        "fp8_linear_bwd_dx": (ctypes.c_int, lin),
+        "lora_adamw_table_bytes": (sz, [ap, i32]),
+        "lora_adamw_table": (ctypes.c_int, [ap, i32, i32, i32, vp, sz, pp]),
+        "lora_grad_norm_workspace_bytes": (sz, [pp]),
+        "lora_grad_norm": (ctypes.c_int, [pp, vp, f32, vp, vp, sz, vp]),
+        "lora_adamw_multi_step": (ctypes.c_int, [pp, vp, vp, f32, f32, f32, f32, f32, i32, vp]),
+    })
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
         fn.restype = res
@@ -579,3 +618,268 @@ def lora_adamw_step(p, g, m, v, step, lr=2e-4, betas=(0.9, 0.999), eps=1e-8, wei
         _ptr(p), _ptr(g), _ptr(m), _ptr(v), _ptr(p_bf16), n, float(lr), float(betas[0]),
         float(betas[1]), float(eps), float(weight_decay), int(step), _stream(stream)))
     return p
+
+
+# --- block-scaled FP8 ------------------------------------------------------
+
+
+def _all_on(dev, *tensors):
+    """Every tensor given lies on dev; the calls below run there, whichever
+    device is current."""
+    for t in tensors:
+        if t is not None and t.device != dev:
+            raise ValueError(f"tensors on {t.device} and {dev}: all must be on one device")
+
+
+def _call(fn, dev, stream, *args):
+    """Call a library function on dev, on the given stream of dev or on its
+    current one."""
+    torch = _torch()
+    f = getattr(load_library(), fn)
+    if stream is not None and stream.device != dev:
+        raise ValueError(f"{fn}: the stream belongs to {stream.device}, the tensors to {dev}")
+    if torch.cuda.current_device() == dev.index:
+        s = torch.cuda.current_stream() if stream is None else stream
+        status = f(*args, s.cuda_stream)
+    else:
+        with torch.cuda.device(dev):
+            s = torch.cuda.current_stream() if stream is None else stream
+            status = f(*args, s.cuda_stream)
+    if status != QN_OK:
+        _check(fn, status)
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
+class Fp8Weight:
+    """Device tensors of an 8-bit weight W[N, K]: codes float8_e4m3fn[N, K]
+    and scale fp32[ceil(N/128), ceil(K/128)], one per 128 x 128 block."""
+
+    def __init__(self, codes, scale):
+        torch = _torch()
+        if codes.dim() != 2:
+            raise ValueError("codes: need a matrix [N, K]")
+        self.N, self.K = codes.shape
+        _dev(codes, torch.float8_e4m3fn, name="codes")
+        _dev(scale, torch.float32, -(-self.N // FP8_BLOCK) * -(-self.K // FP8_BLOCK), "scale")
+        _all_on(codes.device, scale)
+        self.codes, self.scale = codes, scale
+
+    def c_struct(self):
+        return qn_fp8_weight(self.codes.data_ptr(), self.scale.data_ptr(), self.N, self.K)
+
+
+def fp8_quantize_blocks(w, codes=None, scale=None, stream=None):
+    """E4M3 codes float8_e4m3fn[N, K] and the scale of each 128 x 128 block,
+    fp32[ceil(N/128), ceil(K/128)], of a fp32 or bf16 matrix."""
+    torch = _torch()
+    if w.dim() != 2 or w.dtype not in (torch.float32, torch.bfloat16):
+        raise ValueError("fp8_quantize_blocks: need a float32 or bfloat16 matrix")
+    _dev(w, w.dtype, name="w")
+    N, K = w.shape
+    nb, kb = -(-N // FP8_BLOCK), -(-K // FP8_BLOCK)
+    if codes is None:
+        codes = torch.empty((N, K), dtype=torch.float8_e4m3fn, device=w.device)
+    if scale is None:
+        scale = torch.empty((nb, kb), dtype=torch.float32, device=w.device)
+    _dev(codes, torch.float8_e4m3fn, N * K, "codes")
+    _dev(scale, torch.float32, nb * kb, "scale")
+    _all_on(w.device, codes, scale)
+    _call("fp8_quantize_blocks", w.device, stream, w.data_ptr(),
+          QN_F32 if w.dtype == torch.float32 else QN_BF16, N, K, codes.data_ptr(),
+          scale.data_ptr())
+    return codes, scale
+
+
+def fp8_quantize_weight(w, stream=None):
+    """The Fp8Weight of a fp32 or bf16 matrix [N, K] (fp8_quantize_blocks)."""
+    return Fp8Weight(*fp8_quantize_blocks(w, stream=stream))
+
+
+def fp8_quantize_rows(x, codes=None, scale=None, stream=None):
+    """E4M3 codes float8_e4m3fn[M, K] and scales fp32[ceil(K/128), M] of a
+    bf16 matrix, one scale per 128 columns of a row."""
+    torch = _torch()
+    if x.dim() != 2:
+        raise ValueError("x: need a matrix [M, K]")
+    M, K = x.shape
+    kb = -(-K // FP8_BLOCK)
+    _dev(x, torch.bfloat16, name="x")
+    if codes is None:
+        codes = torch.empty((M, K), dtype=torch.float8_e4m3fn, device=x.device)
+    if scale is None:
+        scale = torch.empty((kb, M), dtype=torch.float32, device=x.device)
+    _dev(codes, torch.float8_e4m3fn, M * K, "codes")
+    _dev(scale, torch.float32, kb * M, "scale")
+    _all_on(x.device, codes, scale)
+    _call("fp8_quantize_rows", x.device, stream, x.data_ptr(), M, K, codes.data_ptr(),
+          scale.data_ptr())
+    return codes, scale
+
+
+def fp8_dequant(fw, out_dtype=None, out=None, stream=None):
+    """Materialise an Fp8Weight as fp32 or bf16 [N, K]."""
+    torch = _torch()
+    out_dtype = out_dtype or torch.bfloat16
+    if out_dtype not in (torch.float32, torch.bfloat16):
+        raise ValueError("fp8_dequant: out_dtype must be float32 or bfloat16")
+    dev = fw.codes.device
+    if out is None:
+        out = torch.empty((fw.N, fw.K), dtype=out_dtype, device=dev)
+    _dev(out, out_dtype, fw.N * fw.K, "out")
+    _all_on(dev, out)
+    _call("fp8_dequant", dev, stream, ctypes.byref(fw.c_struct()),
+          QN_BF16 if out_dtype == torch.bfloat16 else QN_F32, out.data_ptr())
+    return out
+
+
+def fp8_matmul(fw, codes, scale, transposed=False, out=None, stream=None):
+    """x W^T (bf16[M, N]) of x [M, K] from fp8_quantize_rows, or with
+    transposed x W (bf16[M, K]) of x [M, N]."""
+    torch = _torch()
+    L, n = (fw.N, fw.K) if transposed else (fw.K, fw.N)
+    if codes.dim() != 2 or codes.shape[1] != L:
+        raise ValueError(f"codes: need [M, {L}]")
+    M = codes.shape[0]
+    _dev(codes, torch.float8_e4m3fn, name="codes")
+    _dev(scale, torch.float32, -(-L // FP8_BLOCK) * M, "scale")
+    if out is None:
+        out = torch.empty((M, n), dtype=torch.bfloat16, device=codes.device)
+    _dev(out, torch.bfloat16, M * n, "out")
+    _all_on(codes.device, fw.codes, scale, out)
+    _call("fp8_matmul", codes.device, stream, ctypes.byref(fw.c_struct()), codes.data_ptr(),
+          scale.data_ptr(), M, int(bool(transposed)), out.data_ptr())
+    return out
+
+
+def fp8_linear_fwd(fw, x, A, B, r, alpha, y=None, u_out=None, ws=None, stream=None):
+    """y = Q(x) W^T + (alpha/r) (x A^T) B^T on an Fp8Weight (bf16 in/out)."""
+    return _fp8_linear("fp8_linear_fwd", QN_OP_FP8_FWD, fw, x, fw.K, fw.N, A, B, r, alpha, y,
+                       u_out, ws, stream)
+
+
+def fp8_linear_bwd_dx(fw, dy, A, B, r, alpha, dx=None, t_out=None, ws=None, stream=None):
+    """dx = Q(dy) W + (alpha/r) (dy B) A on an Fp8Weight (bf16 in/out)."""
+    return _fp8_linear("fp8_linear_bwd_dx", QN_OP_FP8_BWD_DX, fw, dy, fw.N, fw.K, A, B, r, alpha,
+                       dx, t_out, ws, stream)
+
+
+def _fp8_linear(fn, op, fw, x, L, n, A, B, r, alpha, out, low, ws, stream):
+    torch = _torch()
+    bf16, dev = torch.bfloat16, x.device
+    M = x.shape[0]
+    _dev(x, bf16, M * L, "x" if op == QN_OP_FP8_FWD else "dy")
+    if r:
+        _dev(A, bf16, r * fw.K, "A")
+        _dev(B, bf16, fw.N * r, "B")
+    else:
+        A = B = None
+    if out is None:
+        out = torch.empty((M, n), dtype=bf16, device=dev)
+    _dev(out, bf16, M * n, "y" if op == QN_OP_FP8_FWD else "dx")
+    _dev(low, bf16, M * r, "u_out" if op == QN_OP_FP8_FWD else "t_out")
+    if ws is None:
+        ws = workspace(qn_workspace_bytes(op, M, fw.N, fw.K, r), dev)
+    _dev(ws, torch.uint8, name="ws")
+    _all_on(dev, fw.codes, A, B, out, low, ws)
+    _call(fn, dev, stream, ctypes.byref(fw.c_struct()), x.data_ptr(), M, _addr(A), _addr(B), r,
+          alpha, out.data_ptr(), _addr(low), ws.data_ptr(), ws.numel())
+    return out
+
+
+# --- AdamW over many matrices ----------------------------------------------
+
+
+class AdamwTable:
+    """The device table of lora_adamw_multi_step and lora_grad_norm over the
+    given matrices, which it keeps alive (their memory is updated in place)."""
+
+    def __init__(self, plan, table, device, tensors):
+        self.plan, self.table, self.device, self.tensors = plan, table, device, tensors
+
+
+def lora_adamw_table(ps, gs, ms, vs, m_scales=None, v_scales=None, p_bf16s=None):
+    """Table over matrices p (fp32) with gradients g (all fp32 or all bf16).
+
+    States: m and v fp32, or m float8_e4m3fn and v float8_e5m2 with
+    m_scales and v_scales fp32[ceil(n/256)] each (start all of them from
+    zeros).  p_bf16s, if given, holds bf16 tensors (or None) that receive the
+    new p.  Build it once; changed addresses or sizes need a new one."""
+    torch = _torch()
+    lib = load_library()
+    n = len(ps)
+    if not n:
+        raise ValueError("lora_adamw_table: no matrices")
+    eight = ms[0].dtype != torch.float32
+    none = [None] * n
+    if eight and (m_scales is None or v_scales is None):
+        raise ValueError("lora_adamw_table: 8-bit states need m_scales and v_scales")
+    if not eight:
+        m_scales = v_scales = none
+    p_bf16s = none if p_bf16s is None else p_bf16s
+    cols = [list(c) for c in (ps, gs, ms, vs, m_scales, v_scales, p_bf16s)]
+    if any(len(c) != n for c in cols):
+        raise ValueError("lora_adamw_table: lists of different lengths")
+    gt = gs[0].dtype
+    if gt not in (torch.float32, torch.bfloat16):
+        raise ValueError("lora_adamw_table: gradients must be float32 or bfloat16")
+    mt, vt = (torch.float8_e4m3fn, torch.float8_e5m2) if eight else (torch.float32,) * 2
+    dev = ps[0].device
+    arr = (qn_adamw_tensor * n)()
+    for i, row in enumerate(zip(*cols)):
+        k = row[0].numel()
+        blocks = -(-k // STATE_BLOCK)
+        for t, dt, size, name in zip(row, (torch.float32, gt, mt, vt, torch.float32,
+                                           torch.float32, torch.bfloat16),
+                                     (k, k, k, k, blocks, blocks, k),
+                                     ("p", "g", "m", "v", "m_scale", "v_scale", "p_bf16")):
+            if t is None and name in ("p", "g", "m", "v"):
+                raise ValueError(f"{name}: missing")
+            if t is None and eight and name in ("m_scale", "v_scale"):
+                raise ValueError(f"{name}: missing")
+            _dev(t, dt, size, name)
+        _all_on(dev, *row)
+        arr[i] = qn_adamw_tensor(*[_addr(t) for t in row], k)
+    size = lib.lora_adamw_table_bytes(arr, n)
+    host = torch.empty(max(size, 1), dtype=torch.uint8)
+    plan = qn_adamw_plan()
+    _check("lora_adamw_table", lib.lora_adamw_table(
+        arr, n, QN_F32 if gt == torch.float32 else QN_BF16,
+        QN_STATE_8BIT if eight else QN_STATE_F32, host.data_ptr(), size, ctypes.byref(plan)))
+    return AdamwTable(plan, host.to(dev), dev, cols)
+
+
+def lora_grad_norm_workspace_bytes(table):
+    return int(load_library().lora_grad_norm_workspace_bytes(ctypes.byref(table.plan)))
+
+
+def lora_grad_norm(table, max_norm, out=None, ws=None, stream=None):
+    """fp32[2]: the L2 norm of all gradients of a table and the coefficient
+    min(1, max_norm / (norm + 1e-6)) (NaN if the norm is not finite)."""
+    torch = _torch()
+    dev = table.device
+    if out is None:
+        out = torch.empty(2, dtype=torch.float32, device=dev)
+    _dev(out, torch.float32, 2, "out")
+    if ws is None:
+        ws = workspace(lora_grad_norm_workspace_bytes(table), dev)
+    _dev(ws, torch.uint8, name="ws")
+    _all_on(dev, out, ws)
+    _call("lora_grad_norm", dev, stream, ctypes.byref(table.plan), table.table.data_ptr(),
+          max_norm, out.data_ptr(), ws.data_ptr(), ws.numel())
+    return out
+
+
+def lora_adamw_multi_step(table, step, lr=2e-4, betas=(0.9, 0.999), eps=1e-8, weight_decay=0.0,
+                          grad_scale=None, stream=None):
+    """One in-place AdamW step on every matrix of a table.  grad_scale, a
+    device fp32[1] (lora_grad_norm's out[1:]), multiplies the gradients; a
+    step with one that is not finite does nothing."""
+    torch = _torch()
+    dev = table.device
+    _dev(grad_scale, torch.float32, 1, "grad_scale")
+    _all_on(dev, grad_scale)
+    _call("lora_adamw_multi_step", dev, stream, ctypes.byref(table.plan), table.table.data_ptr(),
+          _addr(grad_scale), lr, betas[0], betas[1], eps, weight_decay, step)

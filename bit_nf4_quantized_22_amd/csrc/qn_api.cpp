@@ -6,8 +6,10 @@
 
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
 #include <cstdint>
 #include <cstring>
+#include <vector>
 
 #include "qn_launch.h"
 #include "qn_tables.h"
@@ -246,6 +248,171 @@ int bwd_impl(const qn_weight* w, const qn_bf16* dy, int64_t M, const qn_bf16* A,
   return hip_status(qn::launch_dx_lora_dropout(base32, dx, ts, A, M, w->K, r, *drop_p, seed, s));
 }
 
+// --- block-scaled FP8 ---------------------------------------------------
+
+constexpr int64_t kFp8MaxDim = int64_t{1} << 23;  // 32-bit offsets within a tile
+
+int64_t blocks128(int64_t n) { return (n + 127) / 128; }
+
+int check_fp8_weight(const qn_fp8_weight* w, qn::Fp8View& v) {
+  if (!w || !w->codes || !w->scale) return QN_ERR_NULL;
+  if (w->N <= 0 || w->K <= 0 || w->N % 16 != 0 || w->K % 16 != 0 || w->N > kFp8MaxDim ||
+      w->K > kFp8MaxDim)
+    return QN_ERR_SHAPE;
+  if (!aligned(w->codes, 16) || !aligned(w->scale, 4)) return QN_ERR_ALIGN;
+  v = qn::Fp8View{w->codes, w->scale, w->N, w->K};
+  return QN_OK;
+}
+
+// Rows of a batch: every launch over M rows of n columns fits its grid.
+bool fp8_rows_ok(int64_t M, int64_t n) {
+  return M >= 0 && M <= INT32_MAX && M * blocks128(n) <= INT32_MAX;
+}
+
+// Workspace of a quantised batch [M, L] and its LoRA projection: codes, row
+// scales, partial sums of the projection, its bf16 scaled sum.
+struct Fp8Ws {
+  size_t scale, part, sum, total;
+};
+
+Fp8Ws fp8_ws(int64_t M, int64_t L, int32_t r) {
+  Fp8Ws f{};
+  if (M <= 0) return f;
+  const size_t m = static_cast<size_t>(M), l = static_cast<size_t>(L);
+  f.scale = round_up(m * l, 256);
+  f.part = f.scale + round_up(m * static_cast<size_t>(blocks128(L)) * 4, 256);
+  f.sum = f.part;
+  if (r > 0)
+    f.sum += round_up(m * static_cast<size_t>(r) * 4 *
+                          static_cast<size_t>(qn::fp8_project_slices(M, L)), 256);
+  f.total = f.sum + lora_bf16_bytes(M, r);
+  return f;
+}
+
+// Forward (bwd false: in = x [M, K], down = A, up = B) or backward to the
+// input (in = dy [M, N], down = B read in place, up = A).
+int fp8_linear(bool bwd, const qn_fp8_weight* w, const qn_bf16* in, int64_t M, const qn_bf16* A,
+               const qn_bf16* B, int32_t r, float alpha, qn_bf16* out, qn_bf16* low_out, void* ws,
+               size_t ws_bytes, void* stream) {
+  qn::Fp8View v;
+  int st = check_fp8_weight(w, v);
+  if (st != QN_OK) return st;
+  const int64_t L = bwd ? v.N : v.K;
+  if (r < 0 || !fp8_rows_ok(M, v.N) || !fp8_rows_ok(M, v.K)) return QN_ERR_SHAPE;
+  if (r > kMaxRank) return QN_ERR_UNSUPPORTED;
+  if (M == 0) return QN_OK;
+  if ((st = adapter_rank(r, A, B, r)) != QN_OK) return st;
+  if (!in || !out) return QN_ERR_NULL;
+  if (!aligned(in, 16) || !aligned(out, 16) || (r > 0 && (!aligned(A, 2) || !aligned(B, 2))) ||
+      !aligned(low_out, 2))
+    return QN_ERR_ALIGN;
+  const Fp8Ws f = fp8_ws(M, L, r);
+  if (!ws || ws_bytes < f.total) return QN_ERR_WORKSPACE;
+  if (!aligned(ws, 16)) return QN_ERR_ALIGN;
+  hipStream_t s = as_stream(stream);
+  (void)hipGetLastError();
+  uint8_t* codes = static_cast<uint8_t*>(ws);
+  float* scale = reinterpret_cast<float*>(codes + f.scale);
+  float* part = reinterpret_cast<float*>(codes + f.part);
+  uint16_t* sum = reinterpret_cast<uint16_t*>(codes + f.sum);
+  const float ls = r > 0 ? alpha / static_cast<float>(r) : 0.0f;
+  hipError_t e = r > 0 ? qn::launch_fp8_quantize_project(in, M, L, bwd ? B : A, r, bwd, codes,
+                                                         scale, part, s)
+                       : qn::launch_fp8_quantize_rows(in, M, L, codes, scale, s);
+  if (e != hipSuccess) return QN_ERR_HIP;
+  const int slices = r > 0 ? qn::fp8_project_slices(M, L) : 0;
+  if (!bwd && M <= qn::kFp8DecodeM)
+    return hip_status(qn::launch_fp8_decode(v, codes, scale, static_cast<int>(M), part, slices, B,
+                                            r, ls, out, r > 0 ? low_out : nullptr, s));
+  if (r > 0 &&
+      qn::launch_fp8_project_sum(part, slices, M * r, ls, sum, low_out, s) != hipSuccess)
+    return QN_ERR_HIP;
+  return hip_status(qn::launch_fp8_gemm(v, codes, scale, M, sum, bwd ? A : B, r, bwd, out, s));
+}
+
+bool adamw_hyper_ok(float lr, float beta1, float beta2, float eps, float weight_decay) {
+  return lr >= 0.0f && beta1 >= 0.0f && beta1 < 1.0f && beta2 >= 0.0f && beta2 < 1.0f &&
+         eps > 0.0f && weight_decay >= 0.0f;
+}
+
+// Chunks of the matrices of an AdamW table, -1 for sizes out of range;
+// `used` counts the matrices that have elements.
+int64_t adamw_chunks(const qn_adamw_tensor* t, int32_t count, int32_t& used) {
+  int64_t chunks = 0;
+  used = 0;
+  for (int32_t i = 0; i < count; ++i) {
+    if (t[i].n < 0) return -1;
+    if (t[i].n == 0) continue;
+    ++used;
+    chunks += (t[i].n - 1) / qn::kAdamChunk + 1;
+    if (chunks > INT32_MAX) return -1;
+  }
+  return chunks;
+}
+
+size_t adamw_table_size(int32_t used, int64_t chunks) {
+  return static_cast<size_t>(used) * sizeof(qn::AdamTensor) +
+         static_cast<size_t>(chunks) * sizeof(uint2);
+}
+
+// Whether memory that a step writes overlaps anything else of the table.
+bool adamw_overlaps(const qn_adamw_tensor* t, int32_t count, size_t grad_size, bool state8) {
+  struct Range {
+    uintptr_t lo, hi;
+    bool written;
+  };
+  std::vector<Range> all;
+  all.reserve(static_cast<size_t>(count) * 7);
+  for (int32_t i = 0; i < count; ++i) {
+    const size_t n = static_cast<size_t>(t[i].n);
+    if (n == 0) continue;
+    auto add = [&](const void* p, size_t bytes, bool written) {
+      const uintptr_t lo = reinterpret_cast<uintptr_t>(p);
+      if (p) all.push_back({lo, lo + bytes, written});
+    };
+    const size_t state = n * (state8 ? 1 : 4);
+    const size_t blocks = (n - 1) / qn::kAdamStateBlock + 1;
+    add(t[i].p, n * 4, true);
+    add(t[i].g, n * grad_size, false);
+    add(t[i].m, state, true);
+    add(t[i].v, state, true);
+    add(t[i].p_bf16, n * 2, true);
+    if (state8) {
+      add(t[i].m_scale, blocks * 4, true);
+      add(t[i].v_scale, blocks * 4, true);
+    }
+  }
+  std::sort(all.begin(), all.end(), [](const Range& a, const Range& b) { return a.lo < b.lo; });
+  uintptr_t any = 0, written = 0;  // furthest end so far, of all and of the written
+  for (const Range& r : all) {
+    if (r.lo < (r.written ? any : written)) return true;
+    any = std::max(any, r.hi);
+    if (r.written) written = std::max(written, r.hi);
+  }
+  return false;
+}
+
+int check_adamw_plan(const qn_adamw_plan* plan, const void* table) {
+  if (!plan) return QN_ERR_NULL;
+  if ((plan->grad_dtype != QN_F32 && plan->grad_dtype != QN_BF16) ||
+      (plan->state != QN_STATE_F32 && plan->state != QN_STATE_8BIT))
+    return QN_ERR_UNSUPPORTED;
+  if (plan->tensors < 0 || plan->chunks < plan->tensors || plan->chunks > INT32_MAX ||
+      plan->bytes != static_cast<int64_t>(adamw_table_size(plan->tensors, plan->chunks)))
+    return QN_ERR_SHAPE;
+  if (plan->chunks > 0 && !table) return QN_ERR_NULL;
+  if (!aligned(table, 16)) return QN_ERR_ALIGN;
+  return QN_OK;
+}
+
+const qn::AdamTensor* adamw_tensors(const void* table) {
+  return static_cast<const qn::AdamTensor*>(table);
+}
+
+const uint2* adamw_map(const qn_adamw_plan* plan, const void* table) {
+  return reinterpret_cast<const uint2*>(adamw_tensors(table) + plan->tensors);
+}
+
 }  // namespace
 
 extern "C" {
@@ -384,6 +551,8 @@ size_t qn_workspace_bytes(int32_t op, int64_t M, int64_t N, int64_t K, int32_t r
     case QN_OP_BWD_DX: return bwd_ws(M, N, r);
     case QN_OP_LORA_GRADS: return grads_ws(M, N, K, r);
     case QN_OP_BWD_DX_DROPOUT: return bwd_drop_ws(M, N, K, r);
+    case QN_OP_FP8_FWD: return fp8_ws(M, K, r).total;
+    case QN_OP_FP8_BWD_DX: return fp8_ws(M, N, r).total;
     default: return 0;
   }
 }
@@ -465,12 +634,160 @@ int lora_adamw_step(float* p, const float* g, float* m, float* v, qn_bf16* p_bf1
   if (!aligned(p, 16) || !aligned(g, 16) || !aligned(m, 16) || !aligned(v, 16) ||
       (p_bf16 && !aligned(p_bf16, 8)))
     return QN_ERR_ALIGN;
-  if (!(lr >= 0.0f) || !(beta1 >= 0.0f && beta1 < 1.0f) || !(beta2 >= 0.0f && beta2 < 1.0f) ||
-      !(eps > 0.0f) || !(weight_decay >= 0.0f))
-    return QN_ERR_SHAPE;
+  if (!adamw_hyper_ok(lr, beta1, beta2, eps, weight_decay)) return QN_ERR_SHAPE;
   (void)hipGetLastError();
   return hip_status(qn::launch_adamw(p, g, m, v, p_bf16, n, lr, beta1, beta2, eps, weight_decay,
                                      step, as_stream(stream)));
+}
+
+int fp8_quantize_blocks(const void* w, int32_t dtype, int64_t N, int64_t K, uint8_t* codes,
+                        float* scale, void* stream) {
+  if (dtype != QN_F32 && dtype != QN_BF16) return QN_ERR_UNSUPPORTED;
+  if (N < 0 || K < 0 || N % 16 != 0 || K % 16 != 0 || N > kFp8MaxDim || K > kFp8MaxDim ||
+      blocks128(N) * blocks128(K) > INT32_MAX)
+    return QN_ERR_SHAPE;
+  if (N == 0 || K == 0) return QN_OK;
+  if (!w || !codes || !scale) return QN_ERR_NULL;
+  if (!aligned(w, 16) || !aligned(codes, 16) || !aligned(scale, 4)) return QN_ERR_ALIGN;
+  (void)hipGetLastError();
+  return hip_status(qn::launch_fp8_quantize_blocks(w, dtype == QN_BF16, N, K, codes, scale,
+                                                   as_stream(stream)));
+}
+
+int fp8_quantize_rows(const qn_bf16* x, int64_t M, int64_t K, uint8_t* codes, float* scale,
+                      void* stream) {
+  if (K < 0 || K % 16 != 0 || K > kFp8MaxDim || !fp8_rows_ok(M, K)) return QN_ERR_SHAPE;
+  if (M == 0 || K == 0) return QN_OK;
+  if (!x || !codes || !scale) return QN_ERR_NULL;
+  if (!aligned(x, 16) || !aligned(codes, 16) || !aligned(scale, 4)) return QN_ERR_ALIGN;
+  (void)hipGetLastError();
+  return hip_status(qn::launch_fp8_quantize_rows(x, M, K, codes, scale, as_stream(stream)));
+}
+
+int fp8_dequant(const qn_fp8_weight* w, int32_t out_dtype, void* out, void* stream) {
+  qn::Fp8View v;
+  if (int st = check_fp8_weight(w, v); st != QN_OK) return st;
+  if (out_dtype != QN_F32 && out_dtype != QN_BF16) return QN_ERR_UNSUPPORTED;
+  if (v.N * v.K / 16 > int64_t{INT32_MAX} * 256) return QN_ERR_SHAPE;
+  if (!out) return QN_ERR_NULL;
+  if (!aligned(out, 16)) return QN_ERR_ALIGN;
+  (void)hipGetLastError();
+  return hip_status(qn::launch_fp8_dequant(v, out_dtype == QN_BF16, out, as_stream(stream)));
+}
+
+int fp8_matmul(const qn_fp8_weight* w, const uint8_t* x, const float* xscale, int64_t M,
+               int32_t transposed, qn_bf16* out, void* stream) {
+  qn::Fp8View v;
+  if (int st = check_fp8_weight(w, v); st != QN_OK) return st;
+  if (transposed != 0 && transposed != 1) return QN_ERR_UNSUPPORTED;
+  if (!fp8_rows_ok(M, v.N) || !fp8_rows_ok(M, v.K)) return QN_ERR_SHAPE;
+  if (M == 0) return QN_OK;
+  if (!x || !xscale || !out) return QN_ERR_NULL;
+  if (!aligned(x, 16) || !aligned(xscale, 4) || !aligned(out, 16)) return QN_ERR_ALIGN;
+  (void)hipGetLastError();
+  hipStream_t s = as_stream(stream);
+  if (!transposed && M <= qn::kFp8DecodeM)
+    return hip_status(qn::launch_fp8_decode(v, x, xscale, static_cast<int>(M), nullptr, 0, nullptr,
+                                            0, 0.0f, out, nullptr, s));
+  return hip_status(
+      qn::launch_fp8_gemm(v, x, xscale, M, nullptr, nullptr, 0, transposed == 1, out, s));
+}
+
+int fp8_linear_fwd(const qn_fp8_weight* w, const qn_bf16* x, int64_t M, const qn_bf16* A,
+                   const qn_bf16* B, int32_t r, float alpha, qn_bf16* y, qn_bf16* u_out, void* ws,
+                   size_t ws_bytes, void* stream) {
+  return fp8_linear(false, w, x, M, A, B, r, alpha, y, u_out, ws, ws_bytes, stream);
+}
+
+int fp8_linear_bwd_dx(const qn_fp8_weight* w, const qn_bf16* dy, int64_t M, const qn_bf16* A,
+                      const qn_bf16* B, int32_t r, float alpha, qn_bf16* dx, qn_bf16* t_out,
+                      void* ws, size_t ws_bytes, void* stream) {
+  return fp8_linear(true, w, dy, M, A, B, r, alpha, dx, t_out, ws, ws_bytes, stream);
+}
+
+size_t lora_adamw_table_bytes(const qn_adamw_tensor* t, int32_t count) {
+  if (!t || count < 0) return 0;
+  int32_t used = 0;
+  const int64_t chunks = adamw_chunks(t, count, used);
+  return chunks < 0 ? 0 : adamw_table_size(used, chunks);
+}
+
+int lora_adamw_table(const qn_adamw_tensor* t, int32_t count, int32_t grad_dtype, int32_t state,
+                     void* table, size_t bytes, qn_adamw_plan* plan) {
+  if (!plan || (count > 0 && !t)) return QN_ERR_NULL;
+  if ((grad_dtype != QN_F32 && grad_dtype != QN_BF16) ||
+      (state != QN_STATE_F32 && state != QN_STATE_8BIT))
+    return QN_ERR_UNSUPPORTED;
+  if (count < 0) return QN_ERR_SHAPE;
+  int32_t used = 0;
+  const int64_t chunks = adamw_chunks(t, count, used);
+  if (chunks < 0) return QN_ERR_SHAPE;
+  const bool state8 = state == QN_STATE_8BIT;
+  for (int32_t i = 0; i < count; ++i) {
+    const qn_adamw_tensor& a = t[i];
+    if (a.n == 0) continue;
+    if (!a.p || !a.g || !a.m || !a.v || (state8 && (!a.m_scale || !a.v_scale)))
+      return QN_ERR_NULL;
+    if (!aligned(a.p, 16) || !aligned(a.g, 16) || !aligned(a.m, 16) || !aligned(a.v, 16) ||
+        !aligned(a.p_bf16, 16) ||
+        (state8 && (!aligned(a.m_scale, 4) || !aligned(a.v_scale, 4))))
+      return QN_ERR_ALIGN;
+  }
+  const size_t need = adamw_table_size(used, chunks);
+  if (need > 0 && (!table || bytes < need)) return QN_ERR_WORKSPACE;
+  if (!aligned(table, 8)) return QN_ERR_ALIGN;
+  try {
+    if (adamw_overlaps(t, count, grad_dtype == QN_BF16 ? 2 : 4, state8)) return QN_ERR_SHAPE;
+  } catch (...) {  // no host memory for the ranges
+    return QN_ERR_WORKSPACE;
+  }
+  *plan = qn_adamw_plan{chunks, static_cast<int64_t>(need), used, grad_dtype, state, 0};
+  qn::AdamTensor* d = static_cast<qn::AdamTensor*>(table);
+  uint2* map = reinterpret_cast<uint2*>(d + used);
+  uint32_t k = 0;
+  for (int32_t i = 0; i < count; ++i) {
+    const qn_adamw_tensor& a = t[i];
+    if (a.n == 0) continue;
+    d[k] = qn::AdamTensor{a.p, a.g, a.m, a.v, state8 ? a.m_scale : nullptr,
+                          state8 ? a.v_scale : nullptr, a.p_bf16, a.n};
+    const int64_t c = (a.n - 1) / qn::kAdamChunk + 1;
+    for (int64_t j = 0; j < c; ++j) *map++ = uint2{k, static_cast<uint32_t>(j)};
+    ++k;
+  }
+  return QN_OK;
+}
+
+size_t lora_grad_norm_workspace_bytes(const qn_adamw_plan* plan) {
+  if (!plan || plan->chunks <= 0) return 0;
+  return static_cast<size_t>(qn::grad_norm_blocks(plan->chunks)) * sizeof(double);
+}
+
+int lora_grad_norm(const qn_adamw_plan* plan, const void* table, float max_norm, float* out,
+                   void* ws, size_t ws_bytes, void* stream) {
+  if (int st = check_adamw_plan(plan, table); st != QN_OK) return st;
+  if (!out) return QN_ERR_NULL;
+  if (!(max_norm > 0.0f)) return QN_ERR_SHAPE;
+  if (!aligned(out, 4)) return QN_ERR_ALIGN;
+  const size_t need = lora_grad_norm_workspace_bytes(plan);
+  if (need > 0 && (!ws || ws_bytes < need)) return QN_ERR_WORKSPACE;
+  if (!aligned(ws, 8)) return QN_ERR_ALIGN;
+  (void)hipGetLastError();
+  return hip_status(qn::launch_grad_norm(adamw_tensors(table), adamw_map(plan, table),
+                                         plan->chunks, plan->grad_dtype == QN_BF16, max_norm,
+                                         static_cast<double*>(ws), out, as_stream(stream)));
+}
+
+int lora_adamw_multi_step(const qn_adamw_plan* plan, const void* table, const float* grad_scale,
+                          float lr, float beta1, float beta2, float eps, float weight_decay,
+                          int32_t step, void* stream) {
+  if (int st = check_adamw_plan(plan, table); st != QN_OK) return st;
+  if (!aligned(grad_scale, 4)) return QN_ERR_ALIGN;
+  if (step < 1 || !adamw_hyper_ok(lr, beta1, beta2, eps, weight_decay)) return QN_ERR_SHAPE;
+  (void)hipGetLastError();
+  return hip_status(qn::launch_adamw_multi(
+      adamw_tensors(table), adamw_map(plan, table), plan->chunks, plan->state == QN_STATE_8BIT,
+      plan->grad_dtype == QN_BF16, grad_scale, lr, beta1, beta2, eps, weight_decay, step,
+      as_stream(stream)));
 }
 
 int lora_grads(const qn_bf16* x, const qn_bf16* dy, const qn_bf16* u, const qn_bf16* t,

@@ -1,0 +1,106 @@
+// Device helpers of the block-scaled FP8 kernels: E4M3 codes (1-4-3, bias 7,
+// no infinities; largest value 448) with one fp32 scale per 128 columns of a
+// row (activations, gradients) or per 128 x 128 block (weights).
+#pragma once
+
+#include "qn_device.h"
+
+namespace qn {
+
+// Scale of a group whose largest magnitude is amax: fl32(amax / 448), at
+// least 2^-100, so that no group divides by zero and the residuals of
+// fp8_ratio stay normal numbers.
+__device__ __forceinline__ float fp8_scale(float amax) {
+  return fmaxf(__fdiv_rn(amax, 448.0f), 0x1p-100f);
+}
+
+// fl32(x / s) in the codes' range, inv = fl32(1 / s): one Newton step on
+// x inv (x - q s is exact in the fused multiply-add).  bf16 values often lie
+// on the border between two codes, where the product x inv alone is an ulp
+// to one side.
+__device__ __forceinline__ float fp8_ratio(float x, float s, float inv) {
+  const float q = x * inv;
+  return __builtin_amdgcn_fmed3f(fmaf(fmaf(-q, s, x), inv, q), -448.0f, 448.0f);
+}
+
+// E4M3 codes of four values in [-448, 448], round to nearest even.
+__device__ __forceinline__ uint32_t fp8_pack4(float a, float b, float c, float d) {
+  int w = __builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false);
+  return static_cast<uint32_t>(__builtin_amdgcn_cvt_pk_fp8_f32(c, d, w, true));
+}
+
+// Codes of 8 values of one group.
+__device__ __forceinline__ uint2 fp8_codes8(const float (&v)[8], float s, float inv) {
+  return make_uint2(fp8_pack4(fp8_ratio(v[0], s, inv), fp8_ratio(v[1], s, inv),
+                              fp8_ratio(v[2], s, inv), fp8_ratio(v[3], s, inv)),
+                    fp8_pack4(fp8_ratio(v[4], s, inv), fp8_ratio(v[5], s, inv),
+                              fp8_ratio(v[6], s, inv), fp8_ratio(v[7], s, inv)));
+}
+
+__device__ __forceinline__ void bf16x8_to_f32(const uint4& w, float (&v)[8]) {
+  v[0] = bf16_lo(w.x), v[1] = bf16_hi(w.x), v[2] = bf16_lo(w.y), v[3] = bf16_hi(w.y);
+  v[4] = bf16_lo(w.z), v[5] = bf16_hi(w.z), v[6] = bf16_lo(w.w), v[7] = bf16_hi(w.w);
+}
+
+__device__ __forceinline__ float absmax8(const float (&v)[8]) {
+  float m = 0.0f;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) m = fmaxf(m, fabsf(v[j]));
+  return m;
+}
+
+// Max over aligned runs of 16 lanes (every lane gets it).
+__device__ __forceinline__ float max16(float x) {
+#pragma unroll
+  for (int off = 1; off <= 8; off <<= 1) x = fmaxf(x, __shfl_xor(x, off, 64));
+  return x;
+}
+
+typedef int i32x8_t __attribute__((ext_vector_type(8)));
+
+// c + a b^T of 16 x 128 E4M3 fragments: lane l gives row l % 16 of a and of
+// b, the same 32 of the 128 contraction values each; the result's lane l
+// holds column l % 16, rows 4 (l / 16) .. + 3.  No scale in the instruction.
+__device__ __forceinline__ f32x4_t mfma_fp8(i32x8_t a, i32x8_t b, f32x4_t c) {
+  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, c, 0, 0, 0, 0, 0, 0);
+}
+
+__device__ __forceinline__ i32x8_t frag8(const uint4& lo, const uint4& hi) {
+  return i32x8_t{static_cast<int>(lo.x), static_cast<int>(lo.y), static_cast<int>(lo.z),
+                 static_cast<int>(lo.w), static_cast<int>(hi.x), static_cast<int>(hi.y),
+                 static_cast<int>(hi.z), static_cast<int>(hi.w)};
+}
+
+// 8 bf16 values p[0 .. 7] of a row with `left` values left, zeros behind the
+// row's end; vec: p is 16-byte aligned and left a multiple of 8.
+__device__ __forceinline__ uint4 load_bf16x8(const uint16_t* p, int left, bool vec) {
+  if (left <= 0) return make_uint4(0, 0, 0, 0);
+  if (vec) return *reinterpret_cast<const uint4*>(p);
+  uint32_t w[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const uint32_t lo = 2 * j < left ? p[2 * j] : 0u;
+    const uint32_t hi = 2 * j + 1 < left ? p[2 * j + 1] : 0u;
+    w[j] = lo | hi << 16;
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// The same of 8 values a row pitch apart (a column of a row-major matrix).
+__device__ __forceinline__ uint4 load_bf16x8_strided(const uint16_t* p, int64_t pitch, int left) {
+  uint32_t w[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const uint32_t lo = 2 * j < left ? p[(2 * j) * pitch] : 0u;
+    const uint32_t hi = 2 * j + 1 < left ? p[(2 * j + 1) * pitch] : 0u;
+    w[j] = lo | hi << 16;
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+__device__ __forceinline__ f32x4_t mfma_bf16_32(const uint4& a, const uint4& b, f32x4_t c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, a),
+                                                  __builtin_bit_cast(bf16x8_t, b), c, 0, 0, 0);
+}
+
+}  // namespace qn

@@ -127,6 +127,41 @@ hipError_t launch_gemm_bwd(const WeightView& w, const uint16_t* dy, int64_t M,
 hipError_t launch_lora_reduce(const float* part, int nslice, int64_t n, float scale,
                               uint16_t* out_scaled, uint16_t* out, hipStream_t st);
 
+// A weight in E4M3 codes with one scale per 128 x 128 block.
+struct Fp8View {
+  const uint8_t* codes;  // [N, K]
+  const float* scale;    // [ceil(N / 128), ceil(K / 128)]
+  int64_t N, K;          // multiples of 16
+};
+
+// Block-scaled FP8 (see the fp8_* entries of the C ABI).  Row scales are
+// [ceil(K / 128), M].
+hipError_t launch_fp8_quantize_blocks(const void* w, bool bf16, int64_t N, int64_t K,
+                                      uint8_t* codes, float* scale, hipStream_t st);
+hipError_t launch_fp8_quantize_rows(const uint16_t* x, int64_t M, int64_t K, uint8_t* codes,
+                                    float* scale, hipStream_t st);
+// launch_fp8_quantize_rows of x [M, L], and partial sums part[slices][M][r]
+// of its LoRA projection x P^T (P [r, L], or [L, r] with rows_l; r >= 1).
+int fp8_project_slices(int64_t M, int64_t L);
+hipError_t launch_fp8_quantize_project(const uint16_t* x, int64_t M, int64_t L, const uint16_t* P,
+                                       int r, bool rows_l, uint8_t* codes, float* scale,
+                                       float* part, hipStream_t st);
+// bf16(scale sum over the slices) of n values, and bf16(sum) if plain.
+hipError_t launch_fp8_project_sum(const float* part, int slices, int64_t n, float scale,
+                                  uint16_t* scaled, uint16_t* plain, hipStream_t st);
+// y [M, N] for M <= kFp8DecodeM tokens: x W^T + (lora_scale u) B^T, u given
+// as slices partial sums [slices][M][r]; bf16(u) to u_out if not null.
+constexpr int kFp8DecodeM = 16;
+hipError_t launch_fp8_decode(const Fp8View& w, const uint8_t* x, const float* xs, int M,
+                             const float* part, int slices, const uint16_t* B, int r,
+                             float lora_scale, uint16_t* y, uint16_t* u_out, hipStream_t st);
+hipError_t launch_fp8_dequant(const Fp8View& w, bool out_bf16, void* out, hipStream_t st);
+// out = x W^T + lact lw^T (x [M, K], lact [M, r], lw [N, r]), or with bwd
+// out = x W + lact lw (x [M, N], lw [r, K]); x in codes with row scales.
+hipError_t launch_fp8_gemm(const Fp8View& w, const uint8_t* x, const float* xs, int64_t M,
+                           const uint16_t* lact, const uint16_t* lw, int r, bool bwd, uint16_t* out,
+                           hipStream_t st);
+
 // LoRA merge: out[N, K] = bf16(dequant(W) + s B A) (A [r, K], B [N, r]).
 hipError_t launch_merge(const WeightView& w, const uint16_t* A, const uint16_t* B, int r, float s,
                         uint16_t* out, hipStream_t st);
@@ -135,6 +170,32 @@ hipError_t launch_merge(const WeightView& w, const uint16_t* A, const uint16_t* 
 hipError_t launch_adamw(float* p, const float* g, float* m, float* v, uint16_t* p_bf16, int64_t n,
                         float lr, float beta1, float beta2, float eps, float weight_decay, int step,
                         hipStream_t st);
+
+// AdamW over many matrices (see lora_adamw_multi_step in the C ABI): the
+// device table is the descriptors, then the chunk map: entry b names the
+// descriptor and the chunk of kAdamChunk elements that workgroup b takes.
+struct AdamTensor {
+  float* p;
+  const void* g;  // fp32 or bf16
+  void* m;        // fp32, or E4M3 codes
+  void* v;        // fp32, or E5M2 codes
+  float* m_scale;
+  float* v_scale;
+  uint16_t* p_bf16;
+  int64_t n;
+};
+constexpr int kAdamChunk = 2048;
+constexpr int kAdamStateBlock = 256;  // elements per scale of the 8-bit states
+constexpr int kGradNormBlocks = 2048;  // most partial sums of the gradient norm
+int grad_norm_blocks(int64_t chunks);
+hipError_t launch_adamw_multi(const AdamTensor* tab, const uint2* map, int64_t chunks, bool state8,
+                              bool bf16_grad, const float* grad_scale, float lr, float beta1,
+                              float beta2, float eps, float weight_decay, int step,
+                              hipStream_t st);
+// part: grad_norm_blocks(chunks) doubles; out[0] = norm, out[1] = clip
+// coefficient.
+hipError_t launch_grad_norm(const AdamTensor* tab, const uint2* map, int64_t chunks, bool bf16_grad,
+                            float max_norm, double* part, float* out, hipStream_t st);
 
 // LoRA dropout on the adapter branch (see lora_dropout in the C ABI):
 // threshold = floor(p 2^32) on the 32-bit Philox halves, inv_keep =

@@ -66,6 +66,8 @@ extern "C" {
 #define QN_OP_BWD_DX      1
 #define QN_OP_LORA_GRADS  2
 #define QN_OP_BWD_DX_DROPOUT 3
+#define QN_OP_FP8_FWD     4
+#define QN_OP_FP8_BWD_DX  5
 
 typedef uint16_t qn_bf16; /* bf16 bit pattern */
 
@@ -271,8 +273,8 @@ QN_API int nf4_dequant(const qn_weight* w, int32_t out_dtype, void* out, void* s
 
 /*
  * qn_workspace_bytes -- HOST function.  Bytes of device workspace that op
- * (QN_OP_FWD, QN_OP_BWD_DX, QN_OP_LORA_GRADS or QN_OP_BWD_DX_DROPOUT)
- * needs for these sizes.
+ * (QN_OP_FWD, QN_OP_BWD_DX, QN_OP_LORA_GRADS, QN_OP_BWD_DX_DROPOUT,
+ * QN_OP_FP8_FWD or QN_OP_FP8_BWD_DX) needs for these sizes.
  * Returns 0 for invalid arguments.  The forward and backward keep the LoRA
  * projection (x A^T or dy B) there as fp32 partial sums over slices of the
  * contraction (at most 512 slices for M <= 16, 16 above), which are added
@@ -451,6 +453,195 @@ QN_API int qlora_linear_bwd_dx_dropout(const qn_weight* w, const qn_bf16* dy, in
 QN_API int lora_adamw_step(float* p, const float* g, float* m, float* v, qn_bf16* p_bf16,
                            int64_t n, float lr, float beta1, float beta2, float eps,
                            float weight_decay, int32_t step, void* stream);
+
+/*
+ * A frozen weight W[N, K] in 8-bit floating point, for layers that are kept
+ * at 8 bits (or come from a checkpoint with block scales) instead of 4:
+ *   codes  uint8[N, K], E4M3 (1 sign, 4 exponent bits of bias 7, 3 mantissa
+ *          bits, no infinities, largest value 448).
+ *   scale  fp32[ceil(N/128), ceil(K/128)]: one per 128 x 128 block; the
+ *          last blocks of a row or column may be partial.  A weight's value
+ *          is its code's value times its block's scale.
+ *   N, K   positive multiples of 16, at most 2^23.
+ */
+typedef struct qn_fp8_weight {
+  const uint8_t* codes;
+  const float* scale;
+  int64_t N;
+  int64_t K;
+} qn_fp8_weight;
+
+/*
+ * fp8_quantize_blocks -- E4M3 codes and block scales of a weight.
+ *   w      device, [N, K] of type dtype (QN_F32 or QN_BF16).
+ *   codes  device uint8[N, K] out;  scale fp32[ceil(N/128), ceil(K/128)] out.
+ * Per block: scale = max(fl32(max|w| / 448), 2^-100); code = the E4M3
+ * number nearest to fl32(w / scale), ties to the even code.  N and K are
+ * non-negative multiples of 16.  Results are bit-reproducible.
+ */
+QN_API int fp8_quantize_blocks(const void* w, int32_t dtype, int64_t N, int64_t K, uint8_t* codes,
+                               float* scale, void* stream);
+
+/*
+ * fp8_quantize_rows -- the same of activations or gradients, one scale per
+ * 128 columns of a row.
+ *   x      device bf16[M, K], K a multiple of 16.
+ *   codes  device uint8[M, K] out.
+ *   scale  device fp32[ceil(K/128), M] out: scale[b M + m] is that of row m,
+ *          columns 128 b .. 128 b + 127 (the order the product reads).
+ */
+QN_API int fp8_quantize_rows(const qn_bf16* x, int64_t M, int64_t K, uint8_t* codes, float* scale,
+                             void* stream);
+
+/*
+ * fp8_dequant -- out[N, K] = the weight's values: fl32(code value * scale),
+ * as QN_F32 or rounded (nearest even) to QN_BF16.
+ */
+QN_API int fp8_dequant(const qn_fp8_weight* w, int32_t out_dtype, void* out, void* stream);
+
+/*
+ * fp8_matmul -- the product of quantised rows with a quantised weight:
+ *   transposed == 0:  out[M, N] = x W^T,  x [M, K] and xscale from
+ *                     fp8_quantize_rows(.., M, K, ..);
+ *   transposed == 1:  out[M, K] = x W,    x [M, N] and xscale from
+ *                     fp8_quantize_rows(.., M, N, ..).
+ * 8-bit products summed in fp32 over each block of 128 of the contraction,
+ * multiplied by the block's two scales and summed in fp32; out bf16.  Other
+ * values of transposed are QN_ERR_UNSUPPORTED.  For sharing quantised rows
+ * among several weights; fp8_linear_fwd does all of it for one.
+ */
+QN_API int fp8_matmul(const qn_fp8_weight* w, const uint8_t* x, const float* xscale, int64_t M,
+                      int32_t transposed, qn_bf16* out, void* stream);
+
+/*
+ * fp8_linear_fwd -- qlora_linear_fwd on an 8-bit weight:
+ *   y = Q(x) * value(W)^T + (alpha/r) * (x * A^T) * B^T,
+ * Q(x) the values of x's codes (fp8_quantize_rows).  The adapter reads the
+ * unquantised x.  Arguments, shapes of x, A, B, y, u_out and the rules for r
+ * and NULL adapters as qlora_linear_fwd; out bf16.
+ *   ws  device workspace of ws_bytes >= qn_workspace_bytes(QN_OP_FP8_FWD,..)
+ *       (needed for r == 0 too: x's codes lie there).
+ */
+QN_API int fp8_linear_fwd(const qn_fp8_weight* w, const qn_bf16* x, int64_t M, const qn_bf16* A,
+                          const qn_bf16* B, int32_t r, float alpha, qn_bf16* y, qn_bf16* u_out,
+                          void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * fp8_linear_bwd_dx -- dx = Q(dy) * value(W) + (alpha/r) * (dy * B) * A, the
+ * gradient to the input with dy quantised along N (the forward's rounding of
+ * x passes gradients unchanged).  Arguments as qlora_linear_bwd_dx, ws sized
+ * with QN_OP_FP8_BWD_DX.  The gradients of A and B are lora_grads of the
+ * unquantised x and dy.
+ */
+QN_API int fp8_linear_bwd_dx(const qn_fp8_weight* w, const qn_bf16* dy, int64_t M,
+                             const qn_bf16* A, const qn_bf16* B, int32_t r, float alpha,
+                             qn_bf16* dx, qn_bf16* t_out, void* ws, size_t ws_bytes, void* stream);
+
+/* optimizer states of lora_adamw_multi_step */
+#define QN_STATE_F32   0
+#define QN_STATE_8BIT  1
+
+/*
+ * One LoRA matrix of lora_adamw_multi_step (device pointers, 16-byte
+ * aligned; the scales 4-byte aligned):
+ *   p        fp32[n], updated in place.
+ *   g        the gradient, fp32[n] or bf16[n] (one type for all matrices).
+ *   m, v     QN_STATE_F32: fp32[n].  QN_STATE_8BIT: uint8[n] codes, m E4M3
+ *            (1-4-3, bias 7, no infinities) and v E5M2 (1-5-2, bias 15).
+ *   m_scale, v_scale  QN_STATE_8BIT: fp32[ceil(n/256)], one per 256
+ *            elements: a state's value is its code's value times its scale.
+ *            A first step starts from all-zero codes (any finite scale).
+ *            Ignored (may be NULL) for QN_STATE_F32.
+ *   p_bf16   bf16[n] out (the new p rounded to bf16), or NULL.
+ *   n        >= 0; a matrix of 0 elements is skipped, its pointers not read.
+ */
+typedef struct qn_adamw_tensor {
+  float* p;
+  const void* g;
+  void* m;
+  void* v;
+  float* m_scale;
+  float* v_scale;
+  qn_bf16* p_bf16;
+  int64_t n;
+} qn_adamw_tensor;
+
+/* What lora_adamw_table built; the calls that take a table take its plan. */
+typedef struct qn_adamw_plan {
+  int64_t chunks;      /* workgroups of a step */
+  int64_t bytes;       /* bytes of the table */
+  int32_t tensors;     /* matrices with n > 0 */
+  int32_t grad_dtype;  /* QN_F32 or QN_BF16 */
+  int32_t state;       /* QN_STATE_F32 or QN_STATE_8BIT */
+  int32_t reserved;
+} qn_adamw_plan;
+
+/*
+ * lora_adamw_table_bytes -- HOST function.  Bytes of the table of `count`
+ * matrices (0 for invalid arguments, and for nothing to do).
+ */
+QN_API size_t lora_adamw_table_bytes(const qn_adamw_tensor* t, int32_t count);
+
+/*
+ * lora_adamw_table -- HOST function.  Checks the matrices and writes the
+ * table that lora_adamw_multi_step and lora_grad_norm read to host memory
+ * at `table` (8-byte aligned), and its plan.  The caller copies the table
+ * to device memory (16-byte aligned) once, and keeps it, the matrices and
+ * the plan for as long as it calls with them; new addresses or sizes need a
+ * new table.
+ *   t           host array of `count` (>= 0) matrices, read during the call.
+ *   grad_dtype  QN_F32 or QN_BF16;  state QN_STATE_F32 or QN_STATE_8BIT.
+ *   bytes       room at table, at least lora_adamw_table_bytes(t, count)
+ *               (QN_ERR_WORKSPACE otherwise).
+ * Memory that a step writes must not overlap any other operand of the
+ * table: QN_ERR_SHAPE (the same matrix twice would be updated twice at the
+ * same time).  Gradients may be shared.
+ */
+QN_API int lora_adamw_table(const qn_adamw_tensor* t, int32_t count, int32_t grad_dtype,
+                            int32_t state, void* table, size_t bytes, qn_adamw_plan* plan);
+
+/*
+ * lora_grad_norm -- global L2 norm of the gradients of all matrices of a
+ * table, and the coefficient that clips it: the pages train with a bound on
+ * the gradient norm.
+ *   out  device fp32[2]: out[0] = sqrt(sum g^2) (squares and sums in fp64,
+ *        in a fixed order), out[1] = min(1, max_norm / (out[0] + 1e-6)),
+ *        or NaN if the sum is not finite.
+ *   max_norm  > 0 (QN_ERR_SHAPE).
+ *   ws   device workspace, 8-byte aligned, of at least
+ *        lora_grad_norm_workspace_bytes(plan); not shared by calls that may
+ *        run at the same time.
+ * A table without elements gives norm 0 and coefficient 1.
+ */
+QN_API size_t lora_grad_norm_workspace_bytes(const qn_adamw_plan* plan);
+QN_API int lora_grad_norm(const qn_adamw_plan* plan, const void* table, float max_norm, float* out,
+                          void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * lora_adamw_multi_step -- lora_adamw_step over all matrices of a table in
+ * one launch, with states in 32 or 8 bits ([rkmt] §3.5, [czcl] §3.2).  Per
+ * element, every operation rounded to fp32:
+ *   g <- c g;  m <- b1 m + (1 - b1) g;  v <- b2 v + (1 - b2) g^2;
+ *   p <- p (1 - lr wd) - (lr / (1 - b1^step)) m /
+ *                        (sqrt(v) / sqrt(1 - b2^step) + eps).
+ *   grad_scale  device fp32[1], the c above (out + 1 of lora_grad_norm), or
+ *               NULL for 1.  If it is NaN or infinite the step does nothing.
+ *   lr .. step  as lora_adamw_step (the same errors).
+ * 8-bit states: p moves by the unrounded m and v; what is kept is rounded,
+ * per block of 256 elements of a matrix, with s = max(fl32(max|x| / top),
+ * 2^-100) (top 448 for m, 57344 for v) and n = fl32(|x| fl32(1 / s)), to
+ * the code just below or above n: d = i 0x6A09E667 + step 0x9E3779B9 mod
+ * 2^32 (i the element's place in its block) is added below the code's last
+ * mantissa bit (d's high 20 bits for m; for v the high 21 bits of ~d) and
+ * the sum is cut.  Over the steps the codes' mean follows x, where
+ * rounding to nearest would lose every change smaller than half a code.
+ * The code of a v > 0 is at least 1.  Results are bit-reproducible.
+ * `step` and the hyperparameters are host values: a captured graph repeats
+ * the step that it was captured with.
+ */
+QN_API int lora_adamw_multi_step(const qn_adamw_plan* plan, const void* table,
+                                 const float* grad_scale, float lr, float beta1, float beta2,
+                                 float eps, float weight_decay, int32_t step, void* stream);
 
 #ifdef __cplusplus
 }

@@ -16,6 +16,9 @@ Modules
   optim   -- the AdamW step on the LoRA matrices (fp64).
   dropout -- LoRA dropout on the adapter branch: the counter-based mask
              (Philox4x64-10) and the dropped forward, backward (fp64).
+  fp8     -- block-scaled FP8 (E4M3) weights and rows (IEEE fp32 where the
+             code is decided, fp64 values).
+  optim8  -- AdamW's 8-bit states: dithered rounding to E4M3 / E5M2 codes.
   codebooks -- the FP4 weight table, the FP8 (E4M3) level-2 code, mean-
              centred double quantisation (signed 8-bit code) and the
              uniform INT4 strawman of the error study.
@@ -34,4 +37,4 @@ table printed in the original publication, which none of the pages carries
 (parity unpinned for that comparison only).
 """
 
-from . import nf4, linear, memory, optim, dropout, codebooks  # noqa: F401
+from . import nf4, linear, memory, optim, dropout, codebooks, fp8, optim8  # noqa: F401

@@ -1,0 +1,325 @@
+"""Block-scaled FP8 linear layer against the fp64 oracle (GPU).
+
+Codes and scales must be the oracle's bit for bit.  Bounds of the products,
+per element, derived from the arithmetic:
+  * the matrix unit adds the products of 8 consecutive contraction values
+    aligned to the largest of them and cuts what lies below 2^-13 of its
+    power of two (measured on single products: 2^-13 survives beside 1, 2^-14
+    does not; products of other groups keep 24 bits).  The largest keeps all
+    its bits, the other 7 lose less than 2^-13 of it each: 7 2^-13 sum over
+    groups of max |x w|;
+  * the groups' sums, the two scale products and the blocks' sums are fp32: L
+    additions and 4 products, each within one ulp (2^-23) of the magnitude
+    summed so far: (L + 4) 2^-23 sum |x w|;
+  * the LoRA term rounds s u to bf16 (2^-8 relative) and sums L + r products
+    in fp32: (2^-8 + (L + r + 4) 2^-23) |s| (|x| |A|) |B|;
+  * the result is rounded to bf16: 2^-8 |y| (half of bf16's spacing, eps / 2).
+"""
+
+import numpy as np
+import pytest
+import torch
+
+import bit_nf4_quantized_22_amd as qn
+from oracle import fp8
+from tests.gpu_helpers import bf16_dev, check, f64, synth, to_np
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+
+
+def bf16_of(a):
+    return synth.bf16_bits(np.asarray(a, np.float32))
+
+
+def weights(N, K, seed):
+    rng = np.random.default_rng(seed)
+    w = (rng.standard_normal((N, K)) * 0.02 * np.exp(0.3 * rng.standard_normal((N, 1))))
+    w.reshape(-1)[::97] *= 8
+    return w.astype(np.float32)
+
+
+def acts(M, L, seed, size=1.0):
+    rng = np.random.default_rng(seed)
+    x = rng.standard_normal((M, L)) * np.exp(rng.standard_normal((1, L))) * size
+    return bf16_of(x)
+
+
+def codes_np(t):
+    return t.view(torch.uint8).cpu().numpy()
+
+
+def bits32(a):
+    return np.ascontiguousarray(a, np.float32).view(np.uint32)
+
+
+def rel_to_bound(got, ref, bound):
+    got, ref = np.asarray(got, np.float64), np.asarray(ref, np.float64)
+    assert np.all(np.isfinite(got))
+    return float(np.max(np.abs(got - ref) / bound))
+
+
+def group_max_sum(x, w):
+    """sum over groups of 8 of the contraction of max |x w|, [M, n]."""
+    x, w = np.abs(x).astype(np.float32), np.abs(w).astype(np.float32)
+    out = np.zeros((x.shape[0], w.shape[1]))
+    for k in range(0, x.shape[1], 8):
+        most = x[:, k, None] * w[k]
+        for j in range(k + 1, k + 8):
+            np.maximum(most, x[:, j, None] * w[j], out=most)
+        out += most
+    return out
+
+
+def layer_bound(ref, xv, wv, x, A, B, s, L):
+    r = 0 if A is None else A.shape[0]
+    b = 7 * 2.0 ** -13 * 1.001 * group_max_sum(xv, wv)
+    b += (L + 4) * 2.0 ** -23 * (np.abs(xv) @ np.abs(wv)) + 2.0 ** -8 * np.abs(ref) * 1.01 + 1e-30
+    if r:
+        lo = (np.abs(x) @ np.abs(A.T)) @ np.abs(B.T) * abs(s)
+        b += (2.0 ** -8 * 1.01 + (L + r + 4) * 2.0 ** -23) * lo
+    return b
+
+
+# sizes: one block, partial last blocks in either direction, several tiles
+WEIGHTS = [(16, 16), (128, 128), (144, 272), (1088, 2112), (16, 4096), (2064, 48)]
+
+
+@pytest.mark.parametrize("N,K", WEIGHTS)
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_quantised_weight_is_the_oracles(N, K, dtype):
+    w = weights(N, K, N + K)
+    if dtype == "bf16":
+        w = synth.bf16_to_f32(bf16_of(w))
+    t = torch.from_numpy(w).to(DEV)
+    codes, scale = qn.fp8_quantize_blocks(t if dtype == "f32" else t.bfloat16())
+    rc, rs = fp8.quantize_blocks(w)
+    assert np.array_equal(bits32(scale.cpu().numpy()), bits32(rs))
+    assert np.array_equal(codes_np(codes), rc)
+    fw = qn.Fp8Weight(codes, scale)
+    val = fp8.weight_values(rc, rs)
+    assert np.array_equal(bits32(qn.fp8_dequant(fw, torch.float32).cpu().numpy()), bits32(val))
+    want = torch.from_numpy(val.astype(np.float32)).bfloat16()
+    assert torch.equal(qn.fp8_dequant(fw).cpu().view(torch.int16), want.view(torch.int16))
+
+
+@pytest.mark.parametrize("M,K", [(1, 16), (7, 272), (33, 2112), (513, 128), (2, 11008)])
+def test_quantised_rows_are_the_oracles(M, K):
+    x = acts(M, K, M + K)
+    x.reshape(-1)[:16] = 0
+    codes, scale = qn.fp8_quantize_rows(bf16_dev(x))
+    rc, rs = fp8.quantize_rows(synth.bf16_to_f32(x))
+    assert np.array_equal(bits32(scale.cpu().numpy()), bits32(rs))
+    assert np.array_equal(codes_np(codes), rc)
+
+
+def test_borders_between_codes_and_the_ends_of_the_range():
+    """Values on and next to the borders between two codes for every mantissa
+    of the block's maximum, all-zero and tiny blocks, the largest numbers."""
+    pos = fp8.e4m3_values()[:0x7F]
+    mids = (pos[1:] + pos[:-1]) / 2
+    rows = []
+    for i in range(128):
+        amax = (1 + i / 128) * 2.0 ** (i % 37 - 18)
+        row = np.concatenate([mids, [448.0, -448.0]]) / 448.0 * amax
+        rows.append(row[:128])
+    x = bf16_of(np.array(rows))
+    x = np.vstack([x, x])
+    x[130:133] = 0
+    x[133] = bf16_of(np.full(128, 1e-38))
+    x[134] = bf16_of(np.full(128, 3.3e38))
+    x[135, 1:] = 0
+    f = synth.bf16_to_f32(x)
+    codes, scale = qn.fp8_quantize_rows(bf16_dev(x))
+    rc, rs = fp8.quantize_rows(f)
+    assert np.array_equal(bits32(scale.cpu().numpy()), bits32(rs))
+    assert np.array_equal(codes_np(codes), rc)
+    bc, bs = qn.fp8_quantize_blocks(torch.from_numpy(f).to(DEV))
+    oc, os_ = fp8.quantize_blocks(f)
+    assert np.array_equal(bits32(bs.cpu().numpy()), bits32(os_))
+    assert np.array_equal(codes_np(bc), oc)
+
+
+# (M, N, K, r): decode and batches, partial blocks and tiles, ranks below,
+# between and above the MFMA's 32
+LAYERS = [(1, 16, 16, 0), (1, 144, 272, 16), (3, 128, 1040, 5), (16, 272, 2112, 64),
+          (17, 16, 16, 1), (17, 144, 272, 16), (64, 128, 128, 0), (65, 1088, 2112, 64),
+          (127, 272, 144, 128), (300, 784, 656, 24), (129, 2064, 48, 33), (1, 4096, 4096, 16),
+          (9, 1024, 11008, 16)]
+
+
+@pytest.mark.parametrize("M,N,K,r", LAYERS)
+def test_linear_layer_against_the_oracle(M, N, K, r):
+    w = weights(N, K, M + N)
+    rng = np.random.default_rng(M * N + K)
+    xb, dyb = acts(M, K, 1), acts(M, N, 2, 1e-3)
+    A = bf16_of(rng.standard_normal((r, K)) * 0.02) if r else None
+    B = bf16_of(rng.standard_normal((N, r)) * 0.02) if r else None
+    alpha = 16.0
+    s = alpha / r if r else 0.0
+    fw = qn.fp8_quantize_weight(torch.from_numpy(w).to(DEV))
+    wv = fp8.weight_values(*fp8.quantize_blocks(w))
+    x, dy = bf16_dev(xb), bf16_dev(dyb)
+    Ad, Bd = (bf16_dev(A), bf16_dev(B)) if r else (None, None)
+    # rows behind the last one stay as they were
+    y = torch.full((M + 1, N), 7.0, dtype=torch.bfloat16, device=DEV)
+    dx = torch.full((M + 1, K), 7.0, dtype=torch.bfloat16, device=DEV)
+    u = torch.empty((M, r), dtype=torch.bfloat16, device=DEV) if r else None
+    t = torch.empty((M, r), dtype=torch.bfloat16, device=DEV) if r else None
+    qn.fp8_linear_fwd(fw, x, Ad, Bd, r, alpha, y=y[:M], u_out=u)
+    qn.fp8_linear_bwd_dx(fw, dy, Ad, Bd, r, alpha, dx=dx[:M], t_out=t)
+    torch.cuda.synchronize()
+    assert torch.all(y[M] == 7.0) and torch.all(dx[M] == 7.0)
+    xf, dyf = f64(xb), f64(dyb)
+    xv = fp8.row_values(*fp8.quantize_rows(xf.astype(np.float32)))
+    dv = fp8.row_values(*fp8.quantize_rows(dyf.astype(np.float32)))
+    ref_y, ref_dx = xv @ wv.T, dv @ wv
+    Af = Bf = None
+    if r:
+        Af, Bf = f64(A), f64(B)
+        ref_y = ref_y + s * (xf @ Af.T) @ Bf.T
+        ref_dx = ref_dx + s * (dyf @ Bf) @ Af
+        bu = 2.0 ** -8 * 1.01 * np.abs(xf @ Af.T) + (K + 4) * 2.0 ** -23 * (np.abs(xf) @ np.abs(Af.T))
+        bt = 2.0 ** -8 * 1.01 * np.abs(dyf @ Bf) + (N + 4) * 2.0 ** -23 * (np.abs(dyf) @ np.abs(Bf))
+        assert rel_to_bound(to_np(u), xf @ Af.T, bu + 1e-30) <= 1
+        assert rel_to_bound(to_np(t), dyf @ Bf, bt + 1e-30) <= 1
+    by = layer_bound(ref_y, xv, wv.T, xf, Af, Bf, s, K)
+    bd = layer_bound(ref_dx, dv, wv, dyf, Bf.T if r else None, Af.T if r else None, s, N)
+    assert rel_to_bound(to_np(y[:M]), ref_y, by) <= 1
+    assert rel_to_bound(to_np(dx[:M]), ref_dx, bd) <= 1
+    check(f"fp8 y {M}x{N}x{K} r={r}", to_np(y[:M]), ref_y)
+    check(f"fp8 dx {M}x{N}x{K} r={r}", to_np(dx[:M]), ref_dx)
+    # the product of given rows is the layer without an adapter
+    if r == 0:
+        c, sc = qn.fp8_quantize_rows(x)
+        assert torch.equal(qn.fp8_matmul(fw, c, sc).view(torch.int16), y[:M].view(torch.int16))
+        c, sc = qn.fp8_quantize_rows(dy)
+        got = qn.fp8_matmul(fw, c, sc, transposed=True)
+        assert torch.equal(got.view(torch.int16), dx[:M].view(torch.int16))
+
+
+def test_large_tiles_against_the_oracle_on_some_rows():
+    """A batch with more than 256 large tiles, on rows spread over all of
+    them; the last row and column tiles are partial."""
+    M, N, K, r = 3000, 6000 // 16 * 16, 1552, 16
+    w = weights(N, K, 5)
+    rng = np.random.default_rng(6)
+    xb, dyb = acts(M, K, 3), acts(M, N, 4, 1e-3)
+    A, B = (bf16_of(rng.standard_normal(sh) * 0.02) for sh in ((r, K), (N, r)))
+    fw = qn.fp8_quantize_weight(torch.from_numpy(w).to(DEV))
+    wv = fp8.weight_values(*fp8.quantize_blocks(w))
+    y = qn.fp8_linear_fwd(fw, bf16_dev(xb), bf16_dev(A), bf16_dev(B), r, 32.0)
+    dx = qn.fp8_linear_bwd_dx(fw, bf16_dev(dyb), bf16_dev(A), bf16_dev(B), r, 32.0)
+    torch.cuda.synchronize()
+    rows = np.unique(np.concatenate([np.arange(0, M, 61), [M - 1]]))
+    Af, Bf = f64(A), f64(B)
+    for got, bits, ww, P, Q, L in ((y, xb, wv.T, Af, Bf, K), (dx, dyb, wv, Bf.T, Af.T, N)):
+        v = f64(bits[rows])
+        qv = fp8.row_values(*fp8.quantize_rows(v.astype(np.float32)))
+        ref = qv @ ww + 2.0 * (v @ P.T) @ Q.T
+        b = layer_bound(ref, qv, ww, v, P, Q, 2.0, L)
+        assert rel_to_bound(to_np(got)[rows], ref, b) <= 1
+
+
+@pytest.mark.parametrize("M", [5, 80])
+def test_backward_is_the_forwards_derivative(M):
+    """<dx, d> of the layer without input rounding: with x on the grid of its
+    own codes and dy on its, Q is the identity, the layer is linear in x, and
+    dx must be the exact transpose of the forward within the products'
+    bounds: <dy, f(x)> = <dx, x>."""
+    N, K = 272, 400
+    rng = np.random.default_rng(M)
+    w = weights(N, K, 9)
+    fw = qn.fp8_quantize_weight(torch.from_numpy(w).to(DEV))
+    # powers of two with the block's maximum 448: every value is a code
+    grid = np.array([448.0, 1, 2, 4, 8, 16, 32, 64, 128, 256])
+    def on_grid(n):
+        a = rng.choice(grid, (M, n)) * rng.choice([-1, 1], (M, n))
+        a[:, ::16] = 448.0
+        return bf16_of(a)
+    xb, dyb = on_grid(K), on_grid(N)
+    y = to_np(qn.fp8_linear_fwd(fw, bf16_dev(xb), None, None, 0, 1.0)).astype(np.float64)
+    dx = to_np(qn.fp8_linear_bwd_dx(fw, bf16_dev(dyb), None, None, 0, 1.0)).astype(np.float64)
+    x, dy = f64(xb), f64(dyb)
+    wv = np.abs(fp8.weight_values(*fp8.quantize_blocks(w)))
+    mass = np.sum(np.abs(dy) * (np.abs(x) @ wv.T))
+    # the groups' cuts: at most 7 2^-13 of each group's sum, on either side
+    bound = 2.0 ** -8 * (np.sum(np.abs(dy * y)) + np.sum(np.abs(dx * x))) * 1.01 \
+        + ((K + N + 8) * 2.0 ** -23 + 2 * 7 * 2.0 ** -13) * mass
+    assert abs(np.sum(dy * y) - np.sum(dx * x)) <= bound
+
+
+def test_a_row_does_not_depend_on_its_batch():
+    """A padded batch gives its first rows the same bits as a longer one, on
+    one path (the decode path and the tiles sum in their own orders)."""
+    N, K, r = 272, 1040, 16
+    rng = np.random.default_rng(3)
+    fw = qn.fp8_quantize_weight(torch.from_numpy(weights(N, K, 1)).to(DEV))
+    A, B = (bf16_dev(bf16_of(rng.standard_normal(s) * 0.02)) for s in ((r, K), (N, r)))
+    x = bf16_dev(acts(200, K, 8))
+    for few, many in ((3, 16), (48, 64)):
+        a = qn.fp8_linear_fwd(fw, x[:few], A, B, r, 16.0)
+        b = qn.fp8_linear_fwd(fw, x[:many], A, B, r, 16.0)
+        assert torch.equal(a.view(torch.int16), b[:few].view(torch.int16))
+
+
+def test_repeated_calls_and_another_stream_give_the_same_bits():
+    M, N, K, r = 200, 528, 784, 24
+    rng = np.random.default_rng(11)
+    fw = qn.fp8_quantize_weight(torch.from_numpy(weights(N, K, 2)).to(DEV))
+    A, B = (bf16_dev(bf16_of(rng.standard_normal(s) * 0.02)) for s in ((r, K), (N, r)))
+    x = bf16_dev(acts(M, K, 9))
+    first = qn.fp8_linear_fwd(fw, x, A, B, r, 16.0)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        other = qn.fp8_linear_fwd(fw, x, A, B, r, 16.0)
+    torch.cuda.synchronize()
+    assert torch.equal(first.view(torch.int16), other.view(torch.int16))
+    third = qn.fp8_linear_fwd(fw, x, A, B, r, 16.0, stream=torch.cuda.default_stream())
+    torch.cuda.synchronize()
+    assert torch.equal(first.view(torch.int16), third.view(torch.int16))
+
+
+@pytest.mark.parametrize("M", [1, 100])
+def test_captured_graph_replays(M):
+    N, K, r = 272, 1040, 16
+    rng = np.random.default_rng(4)
+    fw = qn.fp8_quantize_weight(torch.from_numpy(weights(N, K, 1)).to(DEV))
+    A, B = (bf16_dev(bf16_of(rng.standard_normal(s) * 0.02)) for s in ((r, K), (N, r)))
+    x = bf16_dev(acts(M, K, 1))
+    dy = bf16_dev(acts(M, N, 2))
+    y, dx = torch.empty((M, N), dtype=torch.bfloat16, device=DEV), torch.empty_like(x)
+    ws = [qn.workspace(qn.qn_workspace_bytes(op, M, N, K, r), DEV)
+          for op in (qn.QN_OP_FP8_FWD, qn.QN_OP_FP8_BWD_DX)]
+
+    def both():
+        qn.fp8_linear_fwd(fw, x, A, B, r, 16.0, y=y, ws=ws[0])
+        qn.fp8_linear_bwd_dx(fw, dy, A, B, r, 16.0, dx=dx, ws=ws[1])
+
+    both()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        both()
+    for i in range(4):
+        x.copy_(bf16_dev(acts(M, K, 20 + i)))
+        dy.copy_(bf16_dev(acts(M, N, 30 + i)))
+        both()
+        torch.cuda.synchronize()
+        want = y.clone(), dx.clone()
+        y.zero_(), dx.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(y.view(torch.int16), want[0].view(torch.int16))
+        assert torch.equal(dx.view(torch.int16), want[1].view(torch.int16))
+
+
+def test_empty_batch_writes_nothing():
+    fw = qn.fp8_quantize_weight(torch.from_numpy(weights(32, 32, 1)).to(DEV))
+    x = torch.empty((0, 32), dtype=torch.bfloat16, device=DEV)
+    assert qn.fp8_linear_fwd(fw, x, None, None, 0, 1.0).shape == (0, 32)
+    assert qn.fp8_linear_bwd_dx(fw, x, None, None, 0, 1.0).shape == (0, 32)
+    c, s = qn.fp8_quantize_rows(x)
+    assert qn.fp8_matmul(fw, c, s).shape == (0, 32)
+    torch.cuda.synchronize()
