@@ -14,10 +14,12 @@
 // weight, so the weight's scale is wave-uniform; the MFMAs take the weight as
 // first operand, so a lane's four results are four columns of one token and
 // the token's scale is one register.  Both operand tiles (128 bytes of the
-// contraction per step) are brought in by direct-to-LDS DMA, one step ahead
-// in the other of two buffers; 16-byte chunks of a row are XOR-swizzled by
-// the choice of each lane's source address, so that the fragment reads hit
-// all banks.  The backward's weight tile lies [n][k] in memory while a lane
+// contraction per step) and their scales are brought in by direct-to-LDS DMA,
+// one step ahead in the other of two buffers; 16-byte chunks of a row are
+// XOR-swizzled by the choice of each lane's source address, so that the
+// fragment reads hit all banks.  The loop holds no other vector-memory
+// instruction: one scale loaded to a register made the compiler wait for all
+// outstanding DMAs in every step (4096 x 22016 x 8192: 720 -> 656 us).  The backward's weight tile lies [n][k] in memory while a lane
 // needs 32 n of one k: it is read through the transposing LDS loads (8 rows
 // x 16 columns of bytes per 16 lanes).
 
@@ -51,17 +53,25 @@ struct Tile {
   static constexpr int kBM = kWTM * kGM, kBN = 64 * kGN;
   static constexpr int kWaves = kGM * kGN, kThreads = 64 * kWaves;
   static constexpr int kA = kBM * 128, kB = kBN * 128;    // bytes of an operand tile
-  static constexpr int kStage = kA + kB + kBM * 4;        // + the tokens' scales
+  static constexpr int kScales = kA + kB;                 // offset of the tokens' scales
+  static constexpr int kWScales = kScales + kBM * 4;      // and of the weight's, 64 floats
+  static constexpr int kStage = kWScales + 256;
   static constexpr int kDmaA = kA / 1024 / kWaves, kDmaB = kB / 1024 / kWaves;
   static constexpr int kDmaS = kBM / 64;                  // waves that fetch 64 scales each
   static constexpr int kTI = kWTM / 16, kTJ = 4;          // MFMA tiles of a wave
+  static constexpr int kShare = kTI == 8 ? 2 : 4;         // DMAs issued at a time
   static_assert(kDmaA * 1024 * kWaves == kA && kDmaB * 1024 * kWaves == kB && kDmaS <= kWaves,
                 "tile split");
+  static_assert(kDmaS < kWaves, "a wave is left for the weight's scales");
 };
 
-// Slot of 16-byte chunk c in a 128-byte row: 16 consecutive rows' reads of
-// one chunk fall into 16 different groups of 4 banks.
-__device__ __forceinline__ int row_swz(int row) { return (row >> 1) & 7; }
+// Slot of 16-byte chunk c in a 128-byte row is c ^ row_swz(row).  A 16-byte
+// LDS read serves lanes 0-3, 12-15, 20-27 at once (then 4-11, 16-19, 28-31,
+// and the same of the upper half): with lane = 16 g + row and chunk 2 g, half
+// of the 16 rows are read at chunk c and half at c ^ 2, and this swizzle
+// gives them 16 different groups of 4 banks.  ((row >> 1) & 7, right for 16
+// consecutive lanes, cost 4 extra cycles a read.)
+__device__ __forceinline__ int row_swz(int row) { return (row >> 1) & 5; }
 
 // The same for the backward's weight tile of kBN bytes a row, whose reads
 // take rows 8 q + 32 g .. + 7 of two g at a time.
@@ -110,48 +120,77 @@ __device__ __forceinline__ void fp8_tile_of(int bid, int nc, int nr, int& row, i
   row = band * kBandRows + local % rows;
 }
 
+// Fragments of a step: weight columns 16 j .. + 15 of the wave's tile, and
+// the tokens 16 i .. + 15.
 template <typename T, bool kBwd>
-__device__ __forceinline__ void mma_step(const uint8_t* st, float sw, int wm, int wn, int li, int g,
-                                         f32x4_t (&acc)[T::kTI][T::kTJ]) {
-  const uint8_t* sA = st;
-  const uint8_t* sB = st + T::kA;
-  const float* sS = reinterpret_cast<const float*>(st + T::kA + T::kB);
+__device__ __forceinline__ i32x8_t weight_frag(const uint8_t* sB, int wn, int j, int li, int g) {
+  if constexpr (kBwd) {
+    // lanes 2 r, 2 r + 1 of a group point at row 32 g + 8 q + r, columns 0-7
+    // and 8-15; lane c receives column c of the 8 rows
+    const int f = col_swz<T::kBN>((li >> 1) + 32 * g);
+    const uint8_t* p =
+        sB + (32 * g + (li >> 1)) * T::kBN + (((wn * 4 + j) ^ f) << 4) + (li & 1) * 8;
+    i32x8_t b;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const i32x2_t v = __builtin_amdgcn_ds_read_tr8_b64_v2i32(
+          (lds_i32x2_t*)(lds_u8_t*)(p + q * 8 * T::kBN));
+      b[2 * q] = v[0];
+      b[2 * q + 1] = v[1];
+    }
+    return b;
+  }
   const int slot = (2 * g) ^ row_swz(li);
-  i32x8_t b[T::kTJ];
+  const uint8_t* p = sB + (wn * 64 + j * 16 + li) * 128;
+  return frag8(*reinterpret_cast<const uint4*>(p + slot * 16),
+               *reinterpret_cast<const uint4*>(p + (slot ^ 1) * 16));
+}
+
+template <typename T>
+__device__ __forceinline__ i32x8_t token_frag(const uint8_t* sA, int wm, int i, int li, int g) {
+  const int slot = (2 * g) ^ row_swz(li);
+  const uint8_t* p = sA + (wm * T::kWTM + i * 16 + li) * 128;
+  return frag8(*reinterpret_cast<const uint4*>(p + slot * 16),
+               *reinterpret_cast<const uint4*>(p + (slot ^ 1) * 16));
+}
+
+// Fragments of a block that are read ahead of it: the weight's, the first
+// tokens' and all tokens' scales.
+template <typename T>
+struct Ahead {
+  i32x8_t a[2], b[T::kTJ];
+  float s[T::kTI], sw;
+};
+
+template <typename T>
+__device__ __forceinline__ void read_scales(const uint8_t* st, int wm, int wn, int li,
+                                            Ahead<T>& f) {
+  const float* sS = reinterpret_cast<const float*>(st + T::kScales) + wm * T::kWTM + li;
 #pragma unroll
-  for (int j = 0; j < T::kTJ; ++j) {
-    if constexpr (kBwd) {
-      // lanes 2 r, 2 r + 1 of a group point at row 8 q + 32 g + r, columns
-      // 0-7 and 8-15; lane c receives column c of the 8 rows
-      const int f = col_swz<T::kBN>((li >> 1) + 32 * g);
-      const uint8_t* p =
-          sB + (32 * g + (li >> 1)) * T::kBN + (((wn * 4 + j) ^ f) << 4) + (li & 1) * 8;
+  for (int i = 0; i < T::kTI; ++i) f.s[i] = sS[16 * i];
+  f.sw = reinterpret_cast<const float*>(st + T::kWScales)[wn / 2];
+}
+
+template <typename T, bool kBwd>
+__device__ __forceinline__ void read_ahead(const uint8_t* st, int wm, int wn, int li, int g,
+                                           Ahead<T>& f) {
+  f.a[0] = token_frag<T>(st, wm, 0, li, g);
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const i32x2_t v = __builtin_amdgcn_ds_read_tr8_b64_v2i32(
-            (lds_i32x2_t*)(lds_u8_t*)(p + q * 8 * T::kBN));
-        b[j][2 * q] = v[0];
-        b[j][2 * q + 1] = v[1];
-      }
-    } else {
-      const uint8_t* p = sB + (wn * 64 + j * 16 + li) * 128;
-      b[j] = frag8(*reinterpret_cast<const uint4*>(p + slot * 16),
-                   *reinterpret_cast<const uint4*>(p + (slot ^ 1) * 16));
-    }
-  }
+  for (int j = 0; j < T::kTJ; ++j) f.b[j] = weight_frag<T, kBwd>(st + T::kA, wn, j, li, g);
+  read_scales<T>(st, wm, wn, li, f);
+}
+
+// Results of the MFMAs that are still to be scaled and added.
+template <typename T>
+struct Pending {
+  f32x4_t c[T::kTJ];
+  float f;
+};
+
+template <typename T>
+__device__ __forceinline__ void add_pending(const Pending<T>& p, int j, f32x4_t& acc) {
 #pragma unroll
-  for (int i = 0; i < T::kTI; ++i) {
-    const uint8_t* p = sA + (wm * T::kWTM + i * 16 + li) * 128;
-    const i32x8_t a = frag8(*reinterpret_cast<const uint4*>(p + slot * 16),
-                            *reinterpret_cast<const uint4*>(p + (slot ^ 1) * 16));
-    const float s = sS[wm * T::kWTM + i * 16 + li] * sw;
-#pragma unroll
-    for (int j = 0; j < T::kTJ; ++j) {
-      const f32x4_t c = mfma_fp8(b[j], a, f32x4_t{0.f, 0.f, 0.f, 0.f});
-#pragma unroll
-      for (int e = 0; e < 4; ++e) acc[i][j][e] = fmaf(c[e], s, acc[i][j][e]);
-    }
-  }
+  for (int e = 0; e < 4; ++e) acc[e] = fmaf(p.c[j][e], p.f, acc[e]);
 }
 
 template <typename T, bool kBwd>
@@ -169,14 +208,6 @@ __global__ __launch_bounds__(T::kThreads) void fp8_gemm_kernel(Fp8Args g) {
   const int64_t c0 = static_cast<int64_t>(tcol) * T::kBN;
   const int nfull = static_cast<int>(L / 128), tail = static_cast<int>(L % 128);
   const int64_t kb = (g.K + 127) / 128;
-  // the weight's scale of contraction block b, the same for the whole wave;
-  // a wave past the last column re-reads the last block's
-  int64_t cblk = (c0 + wn * 64) / 128;
-  const int64_t cmax = (ncols - 1) / 128;
-  cblk = cblk < cmax ? cblk : cmax;
-  const float* wsp = kBwd ? g.ws + cblk : g.ws + cblk * kb;
-  const int64_t ws_step = kBwd ? kb : 1;
-
   // byte offsets of this lane's DMA sources; rows and columns past the edge
   // re-read the last valid ones (they only feed outputs that are not stored)
   uint32_t offA[T::kDmaA], offB[T::kDmaB];
@@ -199,24 +230,36 @@ __global__ __launch_bounds__(T::kThreads) void fp8_gemm_kernel(Fp8Args g) {
       offB[j] = static_cast<uint32_t>(n * L + ((lane & 7) ^ row_swz(row)) * 16);
     }
   }
-  const int64_t srow = m0 + wave * 64 + lane;
-  const uint32_t offS = static_cast<uint32_t>((srow < g.M ? wave * 64 + lane : g.M - 1 - m0) * 4);
+  // Scales of a block: the first kDmaS waves fetch 64 tokens' each, the
+  // others the weight's (lane l that of column block l % 4 of the tile).
+  const bool tok = wave < T::kDmaS;
+  const int64_t cmax = (ncols - 1) / 128;
+  const int srow = wave * 64 + lane;
+  int64_t cblk = c0 / 128 + (lane & 3);
+  cblk = cblk < cmax ? cblk : cmax;
+  const uint32_t offS = static_cast<uint32_t>(
+      tok ? (m0 + srow < g.M ? srow : g.M - 1 - m0) * 4 : (cblk - c0 / 128) * (kBwd ? 1 : kb) * 4);
+  const float* baseS = tok ? g.xs + m0 : kBwd ? g.ws + c0 / 128 : g.ws + c0 / 128 * kb;
+  const int64_t stepS = tok ? g.M : kBwd ? kb : 1;
+  const uint32_t dstS = tok ? T::kScales + wave * 256 : T::kWScales;
   const uint8_t* baseA = g.x + m0 * L;
   const uint8_t* baseB = kBwd ? g.w + c0 : g.w + c0 * L;
-  const float* baseS = g.xs + m0;
   const uint32_t lds0 = lds_addr(smem);
-  auto issue = [&](int b) {
-    const uint32_t st = lds0 + (b & 1) * T::kStage;
+  // share q of the DMAs of block b, into buffer buf
+  constexpr int kDma = T::kDmaA + T::kDmaB;
+  auto issue = [&](int b, int buf, int q) {
+    const uint32_t st = lds0 + buf * T::kStage;
     const uint8_t* pa = baseA + static_cast<int64_t>(b) * 128;
     const uint8_t* pb = kBwd ? baseB + static_cast<int64_t>(b) * 128 * g.K
                              : baseB + static_cast<int64_t>(b) * 128;
 #pragma unroll
-    for (int j = 0; j < T::kDmaA; ++j) dma16(offA[j], pa, st + (wave * T::kDmaA + j) * 1024);
-#pragma unroll
-    for (int j = 0; j < T::kDmaB; ++j)
-      dma16(offB[j], pb, st + T::kA + (wave * T::kDmaB + j) * 1024);
-    if (wave < T::kDmaS)
-      dma4(offS, baseS + static_cast<int64_t>(b) * g.M, st + T::kA + T::kB + wave * 256);
+    for (int d = q * T::kShare; d < (q + 1) * T::kShare && d < kDma; ++d) {
+      if (d < T::kDmaA)
+        dma16(offA[d], pa, st + (wave * T::kDmaA + d) * 1024);
+      else
+        dma16(offB[d - T::kDmaA], pb, st + T::kA + (wave * T::kDmaB + d - T::kDmaA) * 1024);
+    }
+    if (q == 0) dma4(offS, baseS + b * stepS, st + dstS);
   };
 
   f32x4_t acc[T::kTI][T::kTJ];
@@ -225,13 +268,62 @@ __global__ __launch_bounds__(T::kThreads) void fp8_gemm_kernel(Fp8Args g) {
 #pragma unroll
     for (int j = 0; j < T::kTJ; ++j) acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
 
-  if (nfull > 0) issue(0);
-  for (int b = 0; b < nfull; ++b) {
-    const float sw = wsp[b * ws_step];
-    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // block b landed (this wave's part)
-    __syncthreads();  // everyone's part, and everyone is done with block b - 1
-    if (b + 1 < nfull) issue(b + 1);
-    mma_step<T, kBwd>(smem + (b & 1) * T::kStage, sw, wm, wn, li, lg, acc);
+  // Step b multiplies block b (buffer b & 1).  Its MFMAs of tokens 16 i run
+  // while the fragment of tokens 16 (i + 1) is read and the results of tokens
+  // 16 (i - 1) are scaled and added.  Before the last i comes the turn: this
+  // wave's reads of buffer b & 1 have returned and block b + 1 has landed,
+  // for all waves after the barrier; from there on block b + 1's first
+  // fragments are read under the last MFMAs, and the DMAs of block b + 2 go
+  // out, a share per i (a DMA takes the address unit 16 cycles, so all at
+  // once would hold the reads up; too late and the next turn waits for
+  // them).  Blocks past the end are the last one again: no branch cuts the
+  // step into pieces, and what they bring is not used.
+  if (nfull > 0) {
+    constexpr int kShares = (kDma + T::kShare - 1) / T::kShare;
+    static_assert(kShares <= T::kTI, "the DMAs of a block go out within a step");
+    const int last = nfull - 1;
+#pragma unroll
+    for (int q = 0; q < kShares; ++q) issue(0, 0, q);
+    asm volatile("s_waitcnt vmcnt(0)\n\ts_barrier" ::: "memory");
+    issue(last < 1 ? last : 1, 1, 0);
+    Ahead<T> f;
+    Pending<T> p;
+#pragma unroll
+    for (int j = 0; j < T::kTJ; ++j) p.c[j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+    p.f = 0.0f;
+    read_ahead<T, kBwd>(smem, wm, wn, li, lg, f);
+    for (int b = 0; b <= last; ++b) {
+      const uint8_t* cur = smem + (b & 1) * T::kStage;
+      const uint8_t* nxt = smem + ((b & 1) ^ 1) * T::kStage;
+      const int b1 = b + 1 < last ? b + 1 : last, b2 = b + 2 < last ? b + 2 : last;
+#pragma unroll
+      for (int i = 0; i < T::kTI; ++i) {
+        if (i + 1 < T::kTI) {
+          f.a[(i + 1) & 1] = token_frag<T>(cur, wm, i + 1, li, lg);
+        } else {
+          asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+          f.a[0] = token_frag<T>(nxt, wm, 0, li, lg);
+        }
+#pragma unroll
+        for (int j = 0; j < T::kTJ; ++j) {
+          add_pending<T>(p, j, acc[i > 0 ? i - 1 : T::kTI - 1][j]);
+          p.c[j] = mfma_fp8(f.b[j], f.a[i & 1], f32x4_t{0.f, 0.f, 0.f, 0.f});
+          if (i + 1 == T::kTI) f.b[j] = weight_frag<T, kBwd>(nxt + T::kA, wn, j, li, lg);
+        }
+        p.f = f.s[i] * f.sw;
+        if (i + 1 == T::kTI) {
+          read_scales<T>(nxt, wm, wn, li, f);
+          issue(b2, b & 1, 0);
+        } else if (i + 1 < kShares) {
+          issue(b1, (b & 1) ^ 1, i + 1);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < T::kTJ; ++j) add_pending<T>(p, j, acc[T::kTI - 1][j]);
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    __syncthreads();
   }
   if (tail) {
     // the last, partial block: through registers, zeros behind its end
@@ -260,11 +352,26 @@ __global__ __launch_bounds__(T::kThreads) void fp8_gemm_kernel(Fp8Args g) {
     } else {
       row_tile(st + T::kA, g.w, c0, g.N, T::kBN);
     }
-    float* sS = reinterpret_cast<float*>(st + T::kA + T::kB);
+    float* sS = reinterpret_cast<float*>(st + T::kScales);
     for (int q = t; q < T::kBM; q += T::kThreads)
       sS[q] = g.xs[nfull * g.M + (m0 + q < g.M ? m0 + q : g.M - 1)];
+    if (t < 4) {
+      const int64_t c = c0 / 128 + t < cmax ? c0 / 128 + t : cmax;
+      reinterpret_cast<float*>(st + T::kWScales)[t] = g.ws[kBwd ? nfull * kb + c : c * kb + nfull];
+    }
     __syncthreads();
-    mma_step<T, kBwd>(st, wsp[nfull * ws_step], wm, wn, li, lg, acc);
+Ahead<T> f;
+    read_ahead<T, kBwd>(st, wm, wn, li, lg, f);
+#pragma unroll
+    for (int i = 0; i < T::kTI; ++i) {
+      if (i > 0) f.a[0] = token_frag<T>(st, wm, i, li, lg);
+#pragma unroll
+      for (int j = 0; j < T::kTJ; ++j) {
+        const f32x4_t c = mfma_fp8(f.b[j], f.a[0], f32x4_t{0.f, 0.f, 0.f, 0.f});
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[i][j][e] = fmaf(c[e], f.s[i] * f.sw, acc[i][j][e]);
+      }
+    }
   }
 
   // LoRA term, 32 ranks at a time, operands from the caches: they are a few
@@ -342,6 +449,7 @@ hipError_t launch_fp8_gemm(const Fp8View& w, const uint8_t* x, const float* xs, 
   const int64_t ncols = bwd ? w.K : w.N;
   const int64_t big = ((ncols + 255) / 256) * ((M + 255) / 256);
   if (big >= 256) return run<Tile<128, 2, 4>>(g, bwd, st);
+  if (big >= 64) return run<Tile<64, 2, 4>>(g, bwd, st);
   return run<Tile<64, 2, 2>>(g, bwd, st);
 }
 
