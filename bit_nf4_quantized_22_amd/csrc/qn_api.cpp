@@ -270,22 +270,25 @@ bool fp8_rows_ok(int64_t M, int64_t n) {
 }
 
 // Workspace of a quantised batch [M, L] and its LoRA projection: codes, row
-// scales, partial sums of the projection, its bf16 scaled sum.
+// scales, partial sums of the projection, and (but for the decode path) its
+// scaled bf16 sum in padded rows.
 struct Fp8Ws {
-  size_t scale, part, sum, total;
+  size_t scale, part, act, total;
 };
 
-Fp8Ws fp8_ws(int64_t M, int64_t L, int32_t r) {
+Fp8Ws fp8_ws(bool bwd, int64_t M, int64_t L, int32_t r) {
   Fp8Ws f{};
-  if (M <= 0) return f;
-  const size_t m = static_cast<size_t>(M), l = static_cast<size_t>(L);
-  f.scale = round_up(m * l, 256);
+  if (M <= 0 || L <= 0) return f;
+  const size_t m = static_cast<size_t>(M);
+  f.scale = round_up(m * static_cast<size_t>(L), 256);
   f.part = f.scale + round_up(m * static_cast<size_t>(blocks128(L)) * 4, 256);
-  f.sum = f.part;
-  if (r > 0)
-    f.sum += round_up(m * static_cast<size_t>(r) * 4 *
-                          static_cast<size_t>(qn::fp8_project_slices(M, L)), 256);
-  f.total = f.sum + lora_bf16_bytes(M, r);
+  f.act = f.total = f.part;
+  if (r == 0) return f;
+  f.act += round_up(m * static_cast<size_t>(r) * 4 *
+                        static_cast<size_t>(qn::fp8_project_slices(M, L)), 256);
+  f.total = f.act;
+  if (bwd || M > qn::kFp8DecodeM)
+    f.total += round_up(m * static_cast<size_t>(qn::fp8_lora_pitch(r)) * 2, 256);
   return f;
 }
 
@@ -306,7 +309,7 @@ int fp8_linear(bool bwd, const qn_fp8_weight* w, const qn_bf16* in, int64_t M, c
   if (!aligned(in, 16) || !aligned(out, 16) || (r > 0 && (!aligned(A, 2) || !aligned(B, 2))) ||
       !aligned(low_out, 2))
     return QN_ERR_ALIGN;
-  const Fp8Ws f = fp8_ws(M, L, r);
+  const Fp8Ws f = fp8_ws(bwd, M, L, r);
   if (!ws || ws_bytes < f.total) return QN_ERR_WORKSPACE;
   if (!aligned(ws, 16)) return QN_ERR_ALIGN;
   hipStream_t s = as_stream(stream);
@@ -314,7 +317,7 @@ int fp8_linear(bool bwd, const qn_fp8_weight* w, const qn_bf16* in, int64_t M, c
   uint8_t* codes = static_cast<uint8_t*>(ws);
   float* scale = reinterpret_cast<float*>(codes + f.scale);
   float* part = reinterpret_cast<float*>(codes + f.part);
-  uint16_t* sum = reinterpret_cast<uint16_t*>(codes + f.sum);
+  uint16_t* act = reinterpret_cast<uint16_t*>(codes + f.act);
   const float ls = r > 0 ? alpha / static_cast<float>(r) : 0.0f;
   hipError_t e = r > 0 ? qn::launch_fp8_quantize_project(in, M, L, bwd ? B : A, r, bwd, codes,
                                                          scale, part, s)
@@ -324,10 +327,9 @@ int fp8_linear(bool bwd, const qn_fp8_weight* w, const qn_bf16* in, int64_t M, c
   if (!bwd && M <= qn::kFp8DecodeM)
     return hip_status(qn::launch_fp8_decode(v, codes, scale, static_cast<int>(M), part, slices, B,
                                             r, ls, out, r > 0 ? low_out : nullptr, s));
-  if (r > 0 &&
-      qn::launch_fp8_project_sum(part, slices, M * r, ls, sum, low_out, s) != hipSuccess)
+  if (r > 0 && qn::launch_fp8_project_sum(part, slices, M, r, ls, act, low_out, s) != hipSuccess)
     return QN_ERR_HIP;
-  return hip_status(qn::launch_fp8_gemm(v, codes, scale, M, sum, bwd ? A : B, r, bwd, out, s));
+  return hip_status(qn::launch_fp8_gemm(v, codes, scale, M, act, bwd ? A : B, r, bwd, out, s));
 }
 
 bool adamw_hyper_ok(float lr, float beta1, float beta2, float eps, float weight_decay) {
@@ -551,8 +553,8 @@ size_t qn_workspace_bytes(int32_t op, int64_t M, int64_t N, int64_t K, int32_t r
     case QN_OP_BWD_DX: return bwd_ws(M, N, r);
     case QN_OP_LORA_GRADS: return grads_ws(M, N, K, r);
     case QN_OP_BWD_DX_DROPOUT: return bwd_drop_ws(M, N, K, r);
-    case QN_OP_FP8_FWD: return fp8_ws(M, K, r).total;
-    case QN_OP_FP8_BWD_DX: return fp8_ws(M, N, r).total;
+    case QN_OP_FP8_FWD: return fp8_ws(false, M, K, r).total;
+    case QN_OP_FP8_BWD_DX: return fp8_ws(true, M, N, r).total;
     default: return 0;
   }
 }

@@ -8,7 +8,9 @@
 // 16x16x128 FP8 MFMA per 16 x 16 outputs; its fp32 result is multiplied by
 // the block's two scales and added to the fp32 accumulator with one fused
 // multiply-add per output, so no scale is ever rounded to fewer bits.  The
-// LoRA term follows on the same accumulators as bf16 MFMAs.
+// LoRA term follows on the same accumulators: 64 ranks of bf16 are a block of
+// 128 bytes too, brought in by the same DMAs under the last block's MFMAs and
+// multiplied by bf16 MFMAs.
 //
 // Tiles.  A wave holds kWTM x 64 outputs, which lie in one 128-block of the
 // weight, so the weight's scale is wave-uniform; the MFMAs take the weight as
@@ -32,6 +34,8 @@ namespace {
 
 typedef int i32x2_t __attribute__((ext_vector_type(2)));
 typedef __attribute__((address_space(3))) i32x2_t lds_i32x2_t;
+typedef short i16x4_t __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) i16x4_t lds_i16x4_t;
 typedef __attribute__((address_space(3))) uint8_t lds_u8_t;
 
 struct Fp8Args {
@@ -40,10 +44,10 @@ struct Fp8Args {
   const uint8_t* x;    // codes [M, L], L the contraction length
   const float* xs;     // scales [ceil(L / 128), M]
   int64_t M, N, K;
-  const uint16_t* lact;  // bf16(s u) or bf16(s t), [M, r]
-  const uint16_t* lw;    // B [N, r] or A [r, K]
-  int r;
-  bool vec_w;            // rows of lw can be read 16 bytes at a time (forward)
+  const uint16_t* act;  // bf16(s u) or bf16(s t), [M] rows of `pitch` values
+  const uint16_t* lw;   // B [N, r] or A [r, K]
+  int r, pitch;
+  bool vec_w;           // lw can be read 16 bytes at a time
   uint16_t* out;
 };
 
@@ -80,6 +84,10 @@ __device__ __forceinline__ int col_swz(int row) {
   if constexpr (kBN == 256) return (row & 7) | ((row >> 5) & 1) << 3;
   return ((row >> 1) & 3) | ((row >> 5) & 1) << 2;
 }
+
+// And of A's 32-byte chunks of 16 columns in the LoRA term's rank rows, whose
+// reads take rows 8 g + 0 .. 3 of all four g at a time.
+__device__ __forceinline__ int lora_swz(int row) { return (row & 3) | ((row >> 3) & 1) << 2; }
 
 // LDS DMAs as inline assembly: the compiler waits for every DMA it knows of
 // at each LDS read.  Nothing is returned to registers; the waits below cover
@@ -194,7 +202,7 @@ __device__ __forceinline__ void add_pending(const Pending<T>& p, int j, f32x4_t&
 }
 
 template <typename T, bool kBwd>
-__global__ __launch_bounds__(T::kThreads) void fp8_gemm_kernel(Fp8Args g) {
+__global__ __launch_bounds__(T::kThreads, 2) void fp8_gemm_kernel(Fp8Args g) {
   __shared__ __attribute__((aligned(1024))) uint8_t smem[2 * T::kStage];
   const int t = threadIdx.x, lane = t & 63;
   const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
@@ -276,10 +284,12 @@ __global__ __launch_bounds__(T::kThreads) void fp8_gemm_kernel(Fp8Args g) {
   // fragments are read under the last MFMAs, and the DMAs of block b + 2 go
   // out, a share per i (a DMA takes the address unit 16 cycles, so all at
   // once would hold the reads up; too late and the next turn waits for
-  // them).  Blocks past the end are the last one again: no branch cuts the
-  // step into pieces, and what they bring is not used.
+  // them).  Blocks past the end are the last one again: a branch would cut the
+  // step into pieces, and the last steps compiled apart without those DMAs
+  // spilled registers (656 -> 745 us at 4096 x 22016 x 8192).
   if (nfull > 0) {
     constexpr int kShares = (kDma + T::kShare - 1) / T::kShare;
+    constexpr int kEnd = T::kTI - 1;
     static_assert(kShares <= T::kTI, "the DMAs of a block go out within a step");
     const int last = nfull - 1;
 #pragma unroll
@@ -298,7 +308,7 @@ __global__ __launch_bounds__(T::kThreads) void fp8_gemm_kernel(Fp8Args g) {
       const int b1 = b + 1 < last ? b + 1 : last, b2 = b + 2 < last ? b + 2 : last;
 #pragma unroll
       for (int i = 0; i < T::kTI; ++i) {
-        if (i + 1 < T::kTI) {
+        if (i < kEnd) {
           f.a[(i + 1) & 1] = token_frag<T>(cur, wm, i + 1, li, lg);
         } else {
           asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
@@ -306,12 +316,12 @@ __global__ __launch_bounds__(T::kThreads) void fp8_gemm_kernel(Fp8Args g) {
         }
 #pragma unroll
         for (int j = 0; j < T::kTJ; ++j) {
-          add_pending<T>(p, j, acc[i > 0 ? i - 1 : T::kTI - 1][j]);
+          add_pending<T>(p, j, acc[i > 0 ? i - 1 : kEnd][j]);
           p.c[j] = mfma_fp8(f.b[j], f.a[i & 1], f32x4_t{0.f, 0.f, 0.f, 0.f});
-          if (i + 1 == T::kTI) f.b[j] = weight_frag<T, kBwd>(nxt + T::kA, wn, j, li, lg);
+          if (i == kEnd) f.b[j] = weight_frag<T, kBwd>(nxt + T::kA, wn, j, li, lg);
         }
         p.f = f.s[i] * f.sw;
-        if (i + 1 == T::kTI) {
+        if (i == kEnd) {
           read_scales<T>(nxt, wm, wn, li, f);
           issue(b2, b & 1, 0);
         } else if (i + 1 < kShares) {
@@ -321,10 +331,99 @@ __global__ __launch_bounds__(T::kThreads) void fp8_gemm_kernel(Fp8Args g) {
       }
     }
 #pragma unroll
-    for (int j = 0; j < T::kTJ; ++j) add_pending<T>(p, j, acc[T::kTI - 1][j]);
+    for (int j = 0; j < T::kTJ; ++j) add_pending<T>(p, j, acc[kEnd][j]);
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     __syncthreads();
   }
+
+  // LoRA term, 64 ranks at a time in the two buffers in turn: the tokens' side
+  // (padded rows of 128 bytes) by DMA, the adapter's from where it lies,
+  // through registers: rows of B as the codes' rows, or A's 64 rows of kBN
+  // columns, which the transposing LDS loads read.
+  for (int lb = 0; lb * 64 < g.r; ++lb) {
+    uint8_t* st = smem + (lb & 1) * T::kStage;
+    const uint16_t* pa = g.act + m0 * g.pitch + lb * 64;
+#pragma unroll
+    for (int d = 0; d < T::kDmaA; ++d) {
+      const int row = 8 * (wave * T::kDmaA + d) + (lane >> 3);
+      const int64_t at = m0 + row < g.M ? row : g.M - 1 - m0;
+      dma16(static_cast<uint32_t>(at * g.pitch * 2 + ((lane & 7) ^ row_swz(row)) * 16), pa,
+            lds_addr(st) + (wave * T::kDmaA + d) * 1024);
+    }
+    constexpr int kPer = T::kBN * 8 / T::kThreads;  // 16-byte chunks per thread
+    uint4 v[kPer];
+#pragma unroll
+    for (int q = 0; q < kPer; ++q) {
+      const int e = q * T::kThreads + t;
+      const uint16_t* src;
+      bool in;
+      int left;
+      if constexpr (kBwd) {
+        const int64_t c = c0 + e % (T::kBN / 8) * 8;
+        const int j = lb * 64 + e / (T::kBN / 8);
+        in = j < g.r;
+        left = 8;
+        src = g.lw + (in ? j : 0) * g.K + (c < g.K ? c : g.K - 8);
+      } else {
+        const int64_t n = c0 + (e >> 3);
+        const int j = lb * 64 + (e & 7) * 8;
+        in = j < g.r;
+        left = in ? g.r - j : 8;
+        src = g.lw + (n < g.N ? n : g.N - 1) * g.r + (in ? j : 0);
+      }
+      if (g.vec_w) {
+        v[q] = *reinterpret_cast<const uint4*>(src);
+        if (!in) v[q] = make_uint4(0, 0, 0, 0);
+      } else {
+        v[q] = load_bf16x8(src, in ? left : 0, false);
+      }
+    }
+#pragma unroll
+    for (int q = 0; q < kPer; ++q) {
+      const int e = q * T::kThreads + t;
+      uint8_t* dst = st + T::kA;
+      if constexpr (kBwd) {
+        const int j = e / (T::kBN / 8), c = e % (T::kBN / 8);
+        dst += j * (T::kBN * 2) + (((c >> 1) ^ lora_swz(j)) << 5) + (c & 1) * 16;
+      } else {
+        dst += (e >> 3) * 128 + ((e & 7) ^ row_swz(e >> 3)) * 16;
+      }
+      *reinterpret_cast<uint4*>(dst) = v[q];
+    }
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    __syncthreads();
+#pragma unroll 1
+    for (int kk = 0; kk < 2 && lb * 64 + kk * 32 < g.r; ++kk) {
+      const int at = ((4 * kk + lg) ^ row_swz(li)) * 16;
+      uint4 b[T::kTJ];
+#pragma unroll
+      for (int j = 0; j < T::kTJ; ++j) {
+        if constexpr (kBwd) {
+          // lane 4 a + e of a group points at rank row a, columns 4 e .. + 3
+          uint2 h[2];
+#pragma unroll
+          for (int q = 0; q < 2; ++q) {
+            const int row = 32 * kk + 8 * lg + 4 * q + (li >> 2);
+            const i16x4_t d = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                (lds_i16x4_t*)(lds_u8_t*)(st + T::kA + row * (T::kBN * 2) +
+                                          (((wn * 4 + j) ^ lora_swz(row)) << 5) + (li & 3) * 8));
+            h[q] = __builtin_bit_cast(uint2, d);
+          }
+          b[j] = make_uint4(h[0].x, h[0].y, h[1].x, h[1].y);
+        } else {
+          b[j] = *reinterpret_cast<const uint4*>(st + T::kA + (wn * 64 + j * 16 + li) * 128 + at);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < T::kTI; ++i) {
+        const uint4 a =
+            *reinterpret_cast<const uint4*>(st + (wm * T::kWTM + i * 16 + li) * 128 + at);
+#pragma unroll
+        for (int j = 0; j < T::kTJ; ++j) acc[i][j] = mfma_bf16_32(b[j], a, acc[i][j]);
+      }
+    }
+  }
+  __syncthreads();
   if (tail) {
     // the last, partial block: through registers, zeros behind its end
     uint8_t* st = smem + (nfull & 1) * T::kStage;
@@ -371,28 +470,7 @@ Ahead<T> f;
 #pragma unroll
         for (int e = 0; e < 4; ++e) acc[i][j][e] = fmaf(c[e], f.s[i] * f.sw, acc[i][j][e]);
       }
-    }
-  }
-
-  // LoRA term, 32 ranks at a time, operands from the caches: they are a few
-  // KB per tile against the main loop's hundreds.
-  for (int j0 = 0; j0 < g.r; j0 += 32) {
-    const int rj = j0 + 8 * lg, left = g.r - rj;
-    uint4 wf[T::kTJ];
-#pragma unroll
-    for (int j = 0; j < T::kTJ; ++j) {
-      int64_t n = c0 + wn * 64 + j * 16 + li;
-      n = n < ncols ? n : ncols - 1;
-      wf[j] = kBwd ? load_bf16x8_strided(g.lw + rj * g.K + n, g.K, left)
-                   : load_bf16x8(g.lw + n * g.r + rj, left, g.vec_w);
-    }
-#pragma unroll
-    for (int i = 0; i < T::kTI; ++i) {
-      int64_t m = m0 + wm * T::kWTM + i * 16 + li;
-      m = m < g.M ? m : g.M - 1;
-      const uint4 af = load_bf16x8(g.lact + m * g.r + rj, left, (g.r & 7) == 0);
-#pragma unroll
-      for (int j = 0; j < T::kTJ; ++j) acc[i][j] = mfma_bf16_32(wf[j], af, acc[i][j]);
+      __builtin_amdgcn_sched_barrier(0);
     }
   }
 
@@ -441,11 +519,12 @@ hipError_t run(const Fp8Args& g, bool bwd, hipStream_t st) {
 }  // namespace
 
 hipError_t launch_fp8_gemm(const Fp8View& w, const uint8_t* x, const float* xs, int64_t M,
-                           const uint16_t* lact, const uint16_t* lw, int r, bool bwd, uint16_t* out,
+                           const uint16_t* act, const uint16_t* lw, int r, bool bwd, uint16_t* out,
                            hipStream_t st) {
   if (M == 0) return hipSuccess;
-  const bool vec_w = (r & 7) == 0 && (reinterpret_cast<uintptr_t>(lw) & 15) == 0;
-  Fp8Args g{w.codes, w.scale, x, xs, M, w.N, w.K, lact, lw, r, vec_w, out};
+  // rows of B have r values, those of A K, a multiple of 16
+  const bool vec_w = (reinterpret_cast<uintptr_t>(lw) & 15) == 0 && (bwd || (r & 7) == 0);
+  Fp8Args g{w.codes, w.scale, x, xs, M, w.N, w.K, act, lw, r, fp8_lora_pitch(r), vec_w, out};
   const int64_t ncols = bwd ? w.K : w.N;
   const int64_t big = ((ncols + 255) / 256) * ((M + 255) / 256);
   if (big >= 256) return run<Tile<128, 2, 4>>(g, bwd, st);

@@ -6,6 +6,8 @@
 // nearest to fl32(x / s), ties to even.  All three are one pass over the
 // data: a block's values stay in registers between its maximum and its codes.
 
+#include <type_traits>
+
 #include "qn_fp8.h"
 #include "qn_launch.h"
 
@@ -90,36 +92,95 @@ __global__ __launch_bounds__(kT) void quantize_rows_kernel(const uint16_t* __res
 }
 
 // Quantisation of x [M, L] and its LoRA projection x P^T in one pass over x:
-// a wave takes 16 tokens and the blocks of 128 columns of one slice.  Lane
-// (li, lg) holds columns 32 c + 8 lg .. + 7 (c = 0..3) of token li, which is
-// the bf16 MFMA's operand layout, so the values that are quantised are the
-// ones that are multiplied.  P is A [r, L] (forward) or, with kRowsL, B
-// [L, r] read in place (backward).  part[slice][M][r] gets the slice's sums.
+// a wave takes 16 tokens, its workgroup the blocks of 128 columns of one
+// slice.  Lane (li, lg) holds columns 32 c + 8 lg .. + 7 (c = 0..3) of token
+// li, which is the bf16 MFMA's operand layout, so the values that are
+// quantised are the ones that are multiplied.  P is A [r, L] (forward) or,
+// with kRowsL, B [L, r] read in place (backward); its 128 columns (rows) of a
+// block are staged in LDS for the workgroup's waves, in the other of two
+// buffers, and x and P of the next block are in flight meanwhile.  B's tile
+// lies [column][rank] and is read through the transposing LDS loads (4 rows x
+// 16 ranks per 16 lanes).  part[slice][M][r] gets the slice's sums.
+typedef short i16x4_t __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) i16x4_t lds_i16x4_t;
+typedef __attribute__((address_space(3))) uint16_t lds_u16_t;
+
+// Places of P's 16-byte (32-byte with kRowsL) chunks in LDS: XOR-swizzled by
+// the row so that a wave's reads spread over all banks.
 template <bool kRowsL, int kRT>
-__global__ __launch_bounds__(kT) void quantize_project_kernel(
+__device__ __forceinline__ int p_place(int row, int chunk) {
+  if constexpr (!kRowsL) return row * 128 + (chunk ^ (row & 15)) * 8;
+  const int sw = kRT == 8   ? (row & 3) | ((row >> 3) & 1) << 2
+                 : kRT == 4 ? ((row >> 1) & 1) | ((row >> 3) & 1) << 1
+                 : kRT == 2 ? (row >> 3) & 1
+                            : 0;
+  return row * (16 * kRT) + (((chunk >> 1) ^ sw) << 4) + (chunk & 1) * 8;
+}
+
+template <bool kRowsL, int kRT, int kWaves>
+__global__ __launch_bounds__(64 * kWaves) void quantize_project_kernel(
     const uint16_t* __restrict__ x, int64_t M, int64_t L, const uint16_t* __restrict__ P, int r,
     bool vec_p, int per_slice, uint8_t* __restrict__ codes, float* __restrict__ scale,
     float* __restrict__ part) {
-  const int lane = threadIdx.x & 63, li = lane & 15, lg = lane >> 4;
-  const int64_t row = (static_cast<int64_t>(blockIdx.x) * (blockDim.x >> 6) + (threadIdx.x >> 6)) * 16 + li;
+  constexpr int kThreads = 64 * kWaves;
+  constexpr int kLoads = kRT * 256 / kThreads;  // 16-byte chunks of P per thread and block
+  static_assert(kLoads * kThreads == kRT * 256, "P tile split");
+  __shared__ __attribute__((aligned(16))) uint16_t sP[2][kRT * 16 * 128];
+  const int t = threadIdx.x, lane = t & 63, li = lane & 15, lg = lane >> 4;
+  const int64_t row = (static_cast<int64_t>(blockIdx.x) * kWaves + (t >> 6)) * 16 + li;
   const int64_t m = row < M ? row : M - 1;
   const int64_t blocks = (L + 127) / 128;
   const int64_t b0 = static_cast<int64_t>(blockIdx.y) * per_slice;
   const int64_t b1 = b0 + per_slice < blocks ? b0 + per_slice : blocks;
-  f32x4_t acc[kRT];
-#pragma unroll
-  for (int i = 0; i < kRT; ++i) acc[i] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-  for (int64_t b = b0; b < b1; ++b) {
-    uint4 w[4];
+  uint4 w[4], p[kLoads];
+  auto load_x = [&](int64_t b) {
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
       const int64_t k = b * 128 + 32 * c + 8 * lg;
       w[c] = k < L ? *reinterpret_cast<const uint4*>(x + m * L + k) : make_uint4(0, 0, 0, 0);
     }
+  };
+  auto load_p = [&](int64_t b) {
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) {
+      const int q = i * kThreads + t;
+      if constexpr (kRowsL) {
+        const int64_t l = b * 128 + q / (2 * kRT);
+        const int j = q % (2 * kRT) * 8;
+        p[i] = load_bf16x8(P + l * r + j, l < L ? r - j : 0, vec_p);
+      } else {
+        const int64_t k = b * 128 + q % 16 * 8;
+        const int j = q / 16;
+        p[i] = load_bf16x8(P + j * L + k, j < r && k < L ? 8 : 0, vec_p);
+      }
+    }
+  };
+  f32x4_t acc[kRT];
+#pragma unroll
+  for (int i = 0; i < kRT; ++i) acc[i] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+  load_x(b0);
+  load_p(b0);
+  for (int64_t b = b0; b < b1; ++b) {
+    uint16_t* sp = sP[(b - b0) & 1];
+    uint4 cur[4];
+#pragma unroll
+    for (int c = 0; c < 4; ++c) cur[c] = w[c];
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) {
+      const int q = i * kThreads + t;
+      const int at = kRowsL ? p_place<kRowsL, kRT>(q / (2 * kRT), q % (2 * kRT))
+                            : p_place<kRowsL, kRT>(q / 16, q % 16);
+      *reinterpret_cast<uint4*>(sp + at) = p[i];
+    }
+    __syncthreads();
+    if (b + 1 < b1) {
+      load_x(b + 1);
+      load_p(b + 1);
+    }
     float v[4][8], am = 0.0f;
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
-      bf16x8_to_f32(w[c], v[c]);
+      bf16x8_to_f32(cur[c], v[c]);
       am = fmaxf(am, absmax8(v[c]));
     }
     am = fmaxf(am, __shfl_xor(am, 16, 64));
@@ -134,42 +195,75 @@ __global__ __launch_bounds__(kT) void quantize_project_kernel(
       }
     }
 #pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      const int64_t k = b * 128 + 32 * c + 8 * lg;
+    for (int c = 0; c < 4; ++c)
 #pragma unroll
       for (int i = 0; i < kRT; ++i) {
-        const int j = 16 * i + li;
-        uint4 pf = make_uint4(0, 0, 0, 0);
-        if (j < r && k < L)
-          pf = kRowsL ? load_bf16x8_strided(P + k * r + j, r, 8) : load_bf16x8(P + j * L + k, 8, vec_p);
-        acc[i] = mfma_bf16_32(pf, w[c], acc[i]);
+        uint4 pf;
+        if constexpr (kRowsL) {
+          uint2 h[2];
+#pragma unroll
+          for (int q = 0; q < 2; ++q) {
+            // lane 4 a + e of a group points at row a, ranks 4 e .. + 3
+            const int l = 32 * c + 8 * lg + 4 * q + (li >> 2);
+            const i16x4_t d = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                (lds_i16x4_t*)(lds_u16_t*)(sp + p_place<kRowsL, kRT>(l, 2 * i + ((li >> 1) & 1)) +
+                                           (li & 1) * 4));
+            h[q] = __builtin_bit_cast(uint2, d);
+          }
+          pf = make_uint4(h[0].x, h[0].y, h[1].x, h[1].y);
+        } else {
+          pf = *reinterpret_cast<const uint4*>(sp + p_place<kRowsL, kRT>(16 * i + li, 4 * c + lg));
+        }
+        acc[i] = mfma_bf16_32(pf, cur[c], acc[i]);
       }
-    }
   }
   if (row >= M) return;
   // lane (li, lg): ranks 16 i + 4 lg .. + 3 of token li
   float* out = part + (static_cast<int64_t>(blockIdx.y) * M + row) * r;
 #pragma unroll
-  for (int i = 0; i < kRT; ++i)
+  for (int i = 0; i < kRT; ++i) {
+    const int j = 16 * i + 4 * lg;
+    if ((r & 3) == 0) {
+      if (j < r) *reinterpret_cast<f32x4_t*>(out + j) = acc[i];
+    } else {
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const int j = 16 * i + 4 * lg + e;
-      if (j < r) out[j] = acc[i][e];
+      for (int e = 0; e < 4; ++e)
+        if (j + e < r) out[j + e] = acc[i][e];
     }
+  }
 }
 
-// Sum of the slices, in slice order: bf16(scale sum) for the LoRA-up term
-// and bf16(sum) for the caller.
+// The LoRA term's token side for the tile kernel: act[M][ld] = bf16(scale u),
+// u the slices' sum in slice order, rows zero-padded to ld = 64 or 128 values
+// so that a row is one or two 128-byte runs, like the codes of a block; bf16(u)
+// also to `plain` [M, r] for the caller.  Two values per thread, whose loads
+// go out without waiting for each other.
 __global__ __launch_bounds__(kT) void project_sum_kernel(const float* __restrict__ part, int slices,
-                                                         int64_t n, float scale,
-                                                         uint16_t* __restrict__ scaled,
+                                                         int64_t M, int r, int ld, float scale,
+                                                         uint16_t* __restrict__ act,
                                                          uint16_t* __restrict__ plain) {
-  const int64_t i = static_cast<int64_t>(blockIdx.x) * kT + threadIdx.x;
-  if (i >= n) return;
-  float s = 0.0f;
-  for (int q = 0; q < slices; ++q) s += part[q * n + i];
-  scaled[i] = static_cast<uint16_t>(pack_bf16x2(s * scale, 0.f) & 0xFFFF);
-  if (plain) plain[i] = static_cast<uint16_t>(pack_bf16x2(s, 0.f) & 0xFFFF);
+  const int64_t i = (static_cast<int64_t>(blockIdx.x) * kT + threadIdx.x) * 2;
+  const int64_t m = i / ld;
+  const int j = static_cast<int>(i % ld);
+  if (m >= M) return;
+  float s[2] = {0.0f, 0.0f};
+  if (j < r) {
+    const float* p = part + m * r + j;
+    const int two = j + 1 < r ? 1 : 0;
+    const int64_t step = M * r;
+#pragma unroll 8
+    for (int k = 0; k < slices; ++k) {
+      s[0] += p[k * step];
+      s[1] += p[k * step + two];
+    }
+    if (!two) s[1] = 0.0f;
+    if (plain) {
+      const uint32_t u = pack_bf16x2(s[0], s[1]);
+      plain[m * r + j] = static_cast<uint16_t>(u & 0xFFFF);
+      if (two) plain[m * r + j + 1] = static_cast<uint16_t>(u >> 16);
+    }
+  }
+  *reinterpret_cast<uint32_t*>(act + i) = pack_bf16x2(s[0] * scale, s[1] * scale);
 }
 
 // 16 codes per thread.
@@ -250,32 +344,40 @@ hipError_t launch_fp8_quantize_project(const uint16_t* x, int64_t M, int64_t L, 
                                        int r, bool rows_l, uint8_t* codes, float* scale,
                                        float* part, hipStream_t st) {
   if (M == 0) return hipSuccess;
-  const int waves = M > 48 ? 4 : static_cast<int>((M + 15) / 16);
+  const int waves = M > 16 ? 4 : 1;
   const dim3 grid(static_cast<uint32_t>((M + 16 * waves - 1) / (16 * waves)),
                   static_cast<uint32_t>(fp8_project_slices(M, L)));
-  const bool vec_p = (reinterpret_cast<uintptr_t>(P) & 15) == 0;
+  // rows of P can be read 16 bytes at a time (a row of A has L values, a
+  // multiple of 16; a row of B has r)
+  const bool vec_p = (reinterpret_cast<uintptr_t>(P) & 15) == 0 && (!rows_l || (r & 7) == 0);
   const int per = blocks_per_slice(M, L);
   auto go = [&](auto k) {
     hipLaunchKernelGGL(k, grid, dim3(64 * waves), 0, st, x, M, L, P, r, vec_p, per, codes, scale,
                        part);
     return hipGetLastError();
   };
+  auto by_rank = [&](auto rows, auto w) {
+    constexpr bool kR = decltype(rows)::value;
+    constexpr int kW = decltype(w)::value;
+    return r <= 16   ? go(quantize_project_kernel<kR, 1, kW>)
+           : r <= 32 ? go(quantize_project_kernel<kR, 2, kW>)
+           : r <= 64 ? go(quantize_project_kernel<kR, 4, kW>)
+                     : go(quantize_project_kernel<kR, 8, kW>);
+  };
+  using One = std::integral_constant<int, 1>;
+  using Four = std::integral_constant<int, 4>;
   if (rows_l)
-    return r <= 16   ? go(quantize_project_kernel<true, 1>)
-           : r <= 32 ? go(quantize_project_kernel<true, 2>)
-           : r <= 64 ? go(quantize_project_kernel<true, 4>)
-                     : go(quantize_project_kernel<true, 8>);
-  return r <= 16   ? go(quantize_project_kernel<false, 1>)
-         : r <= 32 ? go(quantize_project_kernel<false, 2>)
-         : r <= 64 ? go(quantize_project_kernel<false, 4>)
-                   : go(quantize_project_kernel<false, 8>);
+    return waves == 1 ? by_rank(std::true_type{}, One{}) : by_rank(std::true_type{}, Four{});
+  return waves == 1 ? by_rank(std::false_type{}, One{}) : by_rank(std::false_type{}, Four{});
 }
 
-hipError_t launch_fp8_project_sum(const float* part, int slices, int64_t n, float scale,
-                                  uint16_t* scaled, uint16_t* plain, hipStream_t st) {
-  if (n == 0) return hipSuccess;
-  hipLaunchKernelGGL(project_sum_kernel, dim3(static_cast<uint32_t>((n + kT - 1) / kT)), dim3(kT),
-                     0, st, part, slices, n, scale, scaled, plain);
+hipError_t launch_fp8_project_sum(const float* part, int slices, int64_t M, int r, float scale,
+                                  uint16_t* act, uint16_t* plain, hipStream_t st) {
+  if (M == 0 || r == 0) return hipSuccess;
+  const int ld = fp8_lora_pitch(r);
+  const int64_t threads = M * ld / 2;
+  hipLaunchKernelGGL(project_sum_kernel, dim3(static_cast<uint32_t>((threads + kT - 1) / kT)),
+                     dim3(kT), 0, st, part, slices, M, r, ld, scale, act, plain);
   return hipGetLastError();
 }
 

@@ -146,9 +146,6 @@ int fp8_project_slices(int64_t M, int64_t L);
 hipError_t launch_fp8_quantize_project(const uint16_t* x, int64_t M, int64_t L, const uint16_t* P,
                                        int r, bool rows_l, uint8_t* codes, float* scale,
                                        float* part, hipStream_t st);
-// bf16(scale sum over the slices) of n values, and bf16(sum) if plain.
-hipError_t launch_fp8_project_sum(const float* part, int slices, int64_t n, float scale,
-                                  uint16_t* scaled, uint16_t* plain, hipStream_t st);
 // y [M, N] for M <= kFp8DecodeM tokens: x W^T + (lora_scale u) B^T, u given
 // as slices partial sums [slices][M][r]; bf16(u) to u_out if not null.
 constexpr int kFp8DecodeM = 16;
@@ -156,10 +153,18 @@ hipError_t launch_fp8_decode(const Fp8View& w, const uint8_t* x, const float* xs
                              const float* part, int slices, const uint16_t* B, int r,
                              float lora_scale, uint16_t* y, uint16_t* u_out, hipStream_t st);
 hipError_t launch_fp8_dequant(const Fp8View& w, bool out_bf16, void* out, hipStream_t st);
-// out = x W^T + lact lw^T (x [M, K], lact [M, r], lw [N, r]), or with bwd
-// out = x W + lact lw (x [M, N], lw [r, K]); x in codes with row scales.
+// The LoRA term's token side for launch_fp8_gemm: act[M], rows of
+// fp8_lora_pitch(r) = 64 or 128 bf16 values padded with zeros, = scale * the
+// sum of the slices of part; its bf16 without the scale to plain [M, r] if
+// not null.
+inline int fp8_lora_pitch(int r) { return r <= 64 ? 64 : 128; }
+hipError_t launch_fp8_project_sum(const float* part, int slices, int64_t M, int r, float scale,
+                                  uint16_t* act, uint16_t* plain, hipStream_t st);
+// out = x W^T + act lw^T (x [M, K], lw = B [N, r]), or with bwd
+// out = x W + act lw (x [M, N], lw = A [r, K]); x in codes with row scales
+// (r == 0: no LoRA term).
 hipError_t launch_fp8_gemm(const Fp8View& w, const uint8_t* x, const float* xs, int64_t M,
-                           const uint16_t* lact, const uint16_t* lw, int r, bool bwd, uint16_t* out,
+                           const uint16_t* act, const uint16_t* lw, int r, bool bwd, uint16_t* out,
                            hipStream_t st);
 
 // LoRA merge: out[N, K] = bf16(dequant(W) + s B A) (A [r, K], B [N, r]).
