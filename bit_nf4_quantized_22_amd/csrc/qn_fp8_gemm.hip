@@ -63,7 +63,7 @@ struct Tile {
   static constexpr int kDmaA = kA / 1024 / kWaves, kDmaB = kB / 1024 / kWaves;
   static constexpr int kDmaS = kBM / 64;                  // waves that fetch 64 scales each
   static constexpr int kTI = kWTM / 16, kTJ = 4;          // MFMA tiles of a wave
-  static constexpr int kShare = kTI == 8 ? 2 : 4;         // DMAs issued at a time
+  static constexpr int kShare = 4;                             // DMAs issued at a time
   static_assert(kDmaA * 1024 * kWaves == kA && kDmaB * 1024 * kWaves == kB && kDmaS <= kWaves,
                 "tile split");
   static_assert(kDmaS < kWaves, "a wave is left for the weight's scales");
@@ -111,16 +111,20 @@ __device__ __forceinline__ uint32_t lds_addr(const void* p) {
       reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) const uint8_t*)p));
 }
 
-// Output tile of workgroup bid: the workgroups of one XCD (bid % 8) take a
-// contiguous run of the tile order, bands of kBandRows row tiles, column by
-// column within a band, so that the tiles an XCD works on at a time share
-// their rows of x and columns of W in its L2.
+// Place in the tile order of workgroup bid of total: the workgroups of one
+// XCD (bid % 8) take a contiguous run of it.
+__device__ __forceinline__ int xcd_run(int bid, int total) {
+  const int x = bid & 7, base = total >> 3, rem = total & 7;
+  return x * base + (x < rem ? x : rem) + (bid >> 3);
+}
+
+// Tile q of nr x nc in the tile order: bands of kBandRows row tiles, column
+// by column within a band, so that the tiles an XCD works on at a time share
+// their rows of x and columns of W in its L2 (2 and 16 rows: 4-10% slower at
+// 2048 x 11008 x 4096 and 4096 x 22016 x 8192; 8 the same).
 constexpr int kBandRows = 4;
 
-__device__ __forceinline__ void fp8_tile_of(int bid, int nc, int nr, int& row, int& col) {
-  const int total = nc * nr, x = bid & 7;
-  const int base = total >> 3, rem = total & 7;
-  const int q = x * base + (x < rem ? x : rem) + (bid >> 3);
+__device__ __forceinline__ void fp8_tile_of(int q, int nc, int nr, int& row, int& col) {
   const int band = q / (kBandRows * nc);
   const int local = q - band * kBandRows * nc;
   const int rows = nr - band * kBandRows < kBandRows ? nr - band * kBandRows : kBandRows;
@@ -201,19 +205,14 @@ __device__ __forceinline__ void add_pending(const Pending<T>& p, int j, f32x4_t&
   for (int e = 0; e < 4; ++e) acc[e] = fmaf(p.c[j][e], p.f, acc[e]);
 }
 
+// One output tile: rows from m0, columns from c0.
 template <typename T, bool kBwd>
-__global__ __launch_bounds__(T::kThreads, 2) void fp8_gemm_kernel(Fp8Args g) {
-  __shared__ __attribute__((aligned(1024))) uint8_t smem[2 * T::kStage];
+__device__ __forceinline__ void fp8_tile(const Fp8Args& g, uint8_t* smem, int64_t m0, int64_t c0) {
   const int t = threadIdx.x, lane = t & 63;
   const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
   const int wm = wave / T::kGN, wn = wave % T::kGN;
   const int li = lane & 15, lg = lane >> 4;
   const int64_t ncols = kBwd ? g.K : g.N, L = kBwd ? g.N : g.K;
-  int trow, tcol;
-  fp8_tile_of(blockIdx.x, static_cast<int>((ncols + T::kBN - 1) / T::kBN),
-              static_cast<int>((g.M + T::kBM - 1) / T::kBM), trow, tcol);
-  const int64_t m0 = static_cast<int64_t>(trow) * T::kBM;
-  const int64_t c0 = static_cast<int64_t>(tcol) * T::kBN;
   const int nfull = static_cast<int>(L / 128), tail = static_cast<int>(L % 128);
   const int64_t kb = (g.K + 127) / 128;
   // byte offsets of this lane's DMA sources; rows and columns past the edge
@@ -504,16 +503,45 @@ Ahead<T> f;
   }
 }
 
-template <typename T>
-hipError_t run(const Fp8Args& g, bool bwd, hipStream_t st) {
-  const int64_t ncols = bwd ? g.K : g.N;
-  const dim3 grid(static_cast<uint32_t>(((ncols + T::kBN - 1) / T::kBN) *
-                                        ((g.M + T::kBM - 1) / T::kBM)));
-  if (bwd)
-    hipLaunchKernelGGL((fp8_gemm_kernel<T, true>), grid, dim3(T::kThreads), 0, st, g);
-  else
-    hipLaunchKernelGGL((fp8_gemm_kernel<T, false>), grid, dim3(T::kThreads), 0, st, g);
-  return hipGetLastError();
+using Big = Tile<128, 2, 4>;    // 256 x 256, 8 waves
+using Half = Tile<64, 2, 4>;    // 128 x 256, 8 waves
+using Small = Tile<64, 2, 2>;   // 128 x 128, 4 waves, two workgroups per CU
+
+// Workgroups below nbig take one 256 x 256 tile each, the others half of one
+// of the remaining tiles: 256-row tiles halve the LDS reads per product, but
+// a last round that fills less than half of the 256 CUs with them costs as
+// much as a full one, and as halves it takes about 0.6 of that.
+template <bool kBwd>
+__global__ __launch_bounds__(Big::kThreads, 2) void fp8_gemm_kernel(Fp8Args g, int nbig) {
+  static_assert(Big::kThreads == Half::kThreads && Big::kBN == Half::kBN &&
+                    Big::kBM == 2 * Half::kBM && Big::kStage > Half::kStage,
+                "a half tile has the same workgroup");
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[2 * Big::kStage];
+  const int nc = static_cast<int>(((kBwd ? g.K : g.N) + Big::kBN - 1) / Big::kBN);
+  const int nr = static_cast<int>((g.M + Big::kBM - 1) / Big::kBM);
+  const int bid = blockIdx.x;
+  int row, col;
+  if (bid < nbig) {
+    fp8_tile_of(xcd_run(bid, nbig), nc, nr, row, col);
+    fp8_tile<Big, kBwd>(g, smem, static_cast<int64_t>(row) * Big::kBM,
+                        static_cast<int64_t>(col) * Big::kBN);
+  } else {
+    const int q = xcd_run(bid - nbig, 2 * (nc * nr - nbig));
+    fp8_tile_of(nbig + (q >> 1), nc, nr, row, col);
+    const int64_t m0 = static_cast<int64_t>(row) * Big::kBM + (q & 1) * Half::kBM;
+    if (m0 < g.M) fp8_tile<Half, kBwd>(g, smem, m0, static_cast<int64_t>(col) * Half::kBN);
+  }
+}
+
+template <bool kBwd>
+__global__ __launch_bounds__(Small::kThreads, 2) void fp8_gemm_small_kernel(Fp8Args g) {
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[2 * Small::kStage];
+  const int nc = static_cast<int>(((kBwd ? g.K : g.N) + Small::kBN - 1) / Small::kBN);
+  const int nr = static_cast<int>((g.M + Small::kBM - 1) / Small::kBM);
+  int row, col;
+  fp8_tile_of(xcd_run(blockIdx.x, nc * nr), nc, nr, row, col);
+  fp8_tile<Small, kBwd>(g, smem, static_cast<int64_t>(row) * Small::kBM,
+                        static_cast<int64_t>(col) * Small::kBN);
 }
 
 }  // namespace
@@ -526,10 +554,28 @@ hipError_t launch_fp8_gemm(const Fp8View& w, const uint8_t* x, const float* xs, 
   const bool vec_w = (reinterpret_cast<uintptr_t>(lw) & 15) == 0 && (bwd || (r & 7) == 0);
   Fp8Args g{w.codes, w.scale, x, xs, M, w.N, w.K, act, lw, r, fp8_lora_pitch(r), vec_w, out};
   const int64_t ncols = bwd ? w.K : w.N;
-  const int64_t big = ((ncols + 255) / 256) * ((M + 255) / 256);
-  if (big >= 256) return run<Tile<128, 2, 4>>(g, bwd, st);
-  if (big >= 64) return run<Tile<64, 2, 4>>(g, bwd, st);
-  return run<Tile<64, 2, 2>>(g, bwd, st);
+  const int64_t tiles = ((ncols + Big::kBN - 1) / Big::kBN) * ((M + Big::kBM - 1) / Big::kBM);
+  if (tiles >= 64) {
+    // whole rounds of the 256 CUs in large tiles, a remainder of up to half
+    // a round in halves
+    const int64_t rest = tiles % 256;
+    const int64_t nbig = rest <= 128 ? tiles - rest : tiles;
+    const dim3 grid(static_cast<uint32_t>(nbig + 2 * (tiles - nbig)));
+    if (bwd)
+      hipLaunchKernelGGL(fp8_gemm_kernel<true>, grid, dim3(Big::kThreads), 0, st, g,
+                         static_cast<int>(nbig));
+    else
+      hipLaunchKernelGGL(fp8_gemm_kernel<false>, grid, dim3(Big::kThreads), 0, st, g,
+                         static_cast<int>(nbig));
+    return hipGetLastError();
+  }
+  const dim3 grid(static_cast<uint32_t>(((ncols + Small::kBN - 1) / Small::kBN) *
+                                        ((M + Small::kBM - 1) / Small::kBM)));
+  if (bwd)
+    hipLaunchKernelGGL(fp8_gemm_small_kernel<true>, grid, dim3(Small::kThreads), 0, st, g);
+  else
+    hipLaunchKernelGGL(fp8_gemm_small_kernel<false>, grid, dim3(Small::kThreads), 0, st, g);
+  return hipGetLastError();
 }
 
 }  // namespace qn
