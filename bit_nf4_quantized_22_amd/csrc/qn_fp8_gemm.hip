@@ -17,7 +17,7 @@
 // first operand, so a lane's four results are four columns of one token and
 // the token's scale is one register.  Both operand tiles (128 bytes of the
 // contraction per step) and their scales are brought in by direct-to-LDS DMA,
-// one step ahead in the other of two buffers; 16-byte chunks of a row are
+// one or two steps ahead in two or three buffers; 16-byte chunks of a row are
 // XOR-swizzled by the choice of each lane's source address, so that the
 // fragment reads hit all banks.  The loop holds no other vector-memory
 // instruction: one scale loaded to a register made the compiler wait for all
@@ -51,9 +51,10 @@ struct Fp8Args {
   uint16_t* out;
 };
 
-template <int kWTM_, int kGM_, int kGN_>
+template <int kWTM_, int kGM_, int kGN_, int kBuf_>
 struct Tile {
   static constexpr int kWTM = kWTM_, kGM = kGM_, kGN = kGN_;
+  static constexpr int kBuf = kBuf_;                      // blocks held in LDS
   static constexpr int kBM = kWTM * kGM, kBN = 64 * kGN;
   static constexpr int kWaves = kGM * kGN, kThreads = 64 * kWaves;
   static constexpr int kA = kBM * 128, kB = kBN * 128;    // bytes of an operand tile
@@ -275,13 +276,12 @@ __device__ __forceinline__ void fp8_tile(const Fp8Args& g, uint8_t* smem, int64_
 #pragma unroll
     for (int j = 0; j < T::kTJ; ++j) acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
 
-  // Step b multiplies block b (buffer b & 1).  Its MFMAs of tokens 16 i run
+  // Step b multiplies block b (buffer b % kBuf).  Its MFMAs of tokens 16 i run
   // while the fragment of tokens 16 (i + 1) is read and the results of tokens
   // 16 (i - 1) are scaled and added.  Before the last i comes the turn: this
-  // wave's reads of buffer b & 1 have returned and block b + 1 has landed,
-  // for all waves after the barrier; from there on block b + 1's first
-  // fragments are read under the last MFMAs, and the DMAs of block b + 2 go
-  // out, a share per i (a DMA takes the address unit 16 cycles, so all at
+  // wave's reads of the buffer have returned and block b + 1 has landed, for
+  // all waves after the barrier; from there on block b + 1's first fragments
+  // are read under the last MFMAs, and the DMAs of block b + kBuf go out, a share per i (a DMA takes the address unit 16 cycles, so all at
   // once would hold the reads up; too late and the next turn waits for
   // them).  Blocks past the end are the last one again: a branch would cut the
   // step into pieces, and the last steps compiled apart without those DMAs
@@ -289,28 +289,36 @@ __device__ __forceinline__ void fp8_tile(const Fp8Args& g, uint8_t* smem, int64_
   if (nfull > 0) {
     constexpr int kShares = (kDma + T::kShare - 1) / T::kShare;
     constexpr int kEnd = T::kTI - 1;
-    static_assert(kShares <= T::kTI, "the DMAs of a block go out within a step");
+    static_assert(kShares < T::kTI, "the DMAs of a block go out before the next turn");
     const int last = nfull - 1;
+    auto upto = [&](int b) { return b < last ? b : last; };
 #pragma unroll
-    for (int q = 0; q < kShares; ++q) issue(0, 0, q);
-    asm volatile("s_waitcnt vmcnt(0)\n\ts_barrier" ::: "memory");
-    issue(last < 1 ? last : 1, 1, 0);
+    for (int b = 0; b < T::kBuf - 1; ++b)
+#pragma unroll
+      for (int q = 0; q < kShares; ++q) issue(upto(b), b, q);
+    // all DMAs but those of the kBuf - 2 youngest blocks have landed
+    asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"((T::kBuf - 2) * (kDma + 1)) : "memory");
+    issue(upto(T::kBuf - 1), T::kBuf - 1, 0);
     Ahead<T> f;
     Pending<T> p;
 #pragma unroll
     for (int j = 0; j < T::kTJ; ++j) p.c[j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
     p.f = 0.0f;
     read_ahead<T, kBwd>(smem, wm, wn, li, lg, f);
+    int buf = 0;
     for (int b = 0; b <= last; ++b) {
-      const uint8_t* cur = smem + (b & 1) * T::kStage;
-      const uint8_t* nxt = smem + ((b & 1) ^ 1) * T::kStage;
-      const int b1 = b + 1 < last ? b + 1 : last, b2 = b + 2 < last ? b + 2 : last;
+      const int bnext = buf + 1 == T::kBuf ? 0 : buf + 1;
+      const int bprev = buf == 0 ? T::kBuf - 1 : buf - 1;
+      const uint8_t* cur = smem + buf * T::kStage;
+      const uint8_t* nxt = smem + bnext * T::kStage;
 #pragma unroll
       for (int i = 0; i < T::kTI; ++i) {
         if (i < kEnd) {
           f.a[(i + 1) & 1] = token_frag<T>(cur, wm, i + 1, li, lg);
         } else {
-          asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+          asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"((T::kBuf - 2) *
+                                                                          (kDma + 1))
+                       : "memory");
           f.a[0] = token_frag<T>(nxt, wm, 0, li, lg);
         }
 #pragma unroll
@@ -322,12 +330,13 @@ __device__ __forceinline__ void fp8_tile(const Fp8Args& g, uint8_t* smem, int64_
         p.f = f.s[i] * f.sw;
         if (i == kEnd) {
           read_scales<T>(nxt, wm, wn, li, f);
-          issue(b2, b & 1, 0);
+          issue(upto(b + T::kBuf), buf, 0);
         } else if (i + 1 < kShares) {
-          issue(b1, (b & 1) ^ 1, i + 1);
+          issue(upto(b + T::kBuf - 1), bprev, i + 1);
         }
         __builtin_amdgcn_sched_barrier(0);
       }
+      buf = bnext;
     }
 #pragma unroll
     for (int j = 0; j < T::kTJ; ++j) add_pending<T>(p, j, acc[kEnd][j]);
@@ -503,9 +512,12 @@ Ahead<T> f;
   }
 }
 
-using Big = Tile<128, 2, 4>;    // 256 x 256, 8 waves
-using Half = Tile<64, 2, 4>;    // 128 x 256, 8 waves
-using Small = Tile<64, 2, 2>;   // 128 x 128, 4 waves, two workgroups per CU
+using Big = Tile<128, 2, 4, 2>;    // 256 x 256, 8 waves
+using Half = Tile<64, 2, 4, 3>;    // 128 x 256, 8 waves
+using Small = Tile<64, 2, 2, 2>;   // 128 x 128, 4 waves, two workgroups per CU
+constexpr int kMixedLds = Big::kBuf * Big::kStage > Half::kBuf * Half::kStage
+                              ? Big::kBuf * Big::kStage
+                              : Half::kBuf * Half::kStage;
 
 // Workgroups below nbig take one 256 x 256 tile each, the others half of one
 // of the remaining tiles: 256-row tiles halve the LDS reads per product, but
@@ -514,9 +526,9 @@ using Small = Tile<64, 2, 2>;   // 128 x 128, 4 waves, two workgroups per CU
 template <bool kBwd>
 __global__ __launch_bounds__(Big::kThreads, 2) void fp8_gemm_kernel(Fp8Args g, int nbig) {
   static_assert(Big::kThreads == Half::kThreads && Big::kBN == Half::kBN &&
-                    Big::kBM == 2 * Half::kBM && Big::kStage > Half::kStage,
+                    Big::kBM == 2 * Half::kBM,
                 "a half tile has the same workgroup");
-  __shared__ __attribute__((aligned(1024))) uint8_t smem[2 * Big::kStage];
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[kMixedLds];
   const int nc = static_cast<int>(((kBwd ? g.K : g.N) + Big::kBN - 1) / Big::kBN);
   const int nr = static_cast<int>((g.M + Big::kBM - 1) / Big::kBM);
   const int bid = blockIdx.x;
@@ -535,7 +547,7 @@ __global__ __launch_bounds__(Big::kThreads, 2) void fp8_gemm_kernel(Fp8Args g, i
 
 template <bool kBwd>
 __global__ __launch_bounds__(Small::kThreads, 2) void fp8_gemm_small_kernel(Fp8Args g) {
-  __shared__ __attribute__((aligned(1024))) uint8_t smem[2 * Small::kStage];
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[Small::kBuf * Small::kStage];
   const int nc = static_cast<int>(((kBwd ? g.K : g.N) + Small::kBN - 1) / Small::kBN);
   const int nr = static_cast<int>((g.M + Small::kBM - 1) / Small::kBM);
   int row, col;
