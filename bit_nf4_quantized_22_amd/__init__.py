@@ -623,28 +623,31 @@ def lora_adamw_step(p, g, m, v, step, lr=2e-4, betas=(0.9, 0.999), eps=1e-8, wei
 # --- block-scaled FP8 ------------------------------------------------------
 
 
-def _all_on(dev, *tensors):
-    """Every tensor given lies on dev; the calls below run there, whichever
-    device is current."""
-    for t in tensors:
-        if t is not None and t.device != dev:
-            raise ValueError(f"tensors on {t.device} and {dev}: all must be on one device")
+def _fit(t, dtype, numel, dev, name):
+    """_dev, and on the device dev (one pass: these checks run on every call of
+    a decode step)."""
+    if t.dtype is not dtype or t.numel() != numel or t.device != dev or not t.is_contiguous():
+        _dev(t, dtype, numel, name)
+        raise ValueError(f"{name}: on {t.device}, other tensors of the call on {dev}")
 
 
 def _call(fn, dev, stream, *args):
-    """Call a library function on dev, on the given stream of dev or on its
-    current one."""
+    """Call a library function with dev current, on the given stream of dev
+    or on its current one."""
     torch = _torch()
     f = getattr(load_library(), fn)
-    if stream is not None and stream.device != dev:
+    at = dev.index
+    if stream is None:
+        s = torch._C._cuda_getCurrentRawStream(at)
+    elif stream.device != dev:
         raise ValueError(f"{fn}: the stream belongs to {stream.device}, the tensors to {dev}")
-    if torch.cuda.current_device() == dev.index:
-        s = torch.cuda.current_stream() if stream is None else stream
-        status = f(*args, s.cuda_stream)
+    else:
+        s = stream.cuda_stream
+    if torch._C._cuda_getDevice() == at:
+        status = f(*args, s)
     else:
         with torch.cuda.device(dev):
-            s = torch.cuda.current_stream() if stream is None else stream
-            status = f(*args, s.cuda_stream)
+            status = f(*args, s)
     if status != QN_OK:
         _check(fn, status)
 
@@ -661,10 +664,10 @@ class Fp8Weight:
         torch = _torch()
         if codes.dim() != 2:
             raise ValueError("codes: need a matrix [N, K]")
-        self.N, self.K = codes.shape
+        N, K = self.N, self.K = codes.shape
+        dev = self.device = codes.device
         _dev(codes, torch.float8_e4m3fn, name="codes")
-        _dev(scale, torch.float32, -(-self.N // FP8_BLOCK) * -(-self.K // FP8_BLOCK), "scale")
-        _all_on(codes.device, scale)
+        _fit(scale, torch.float32, -(-N // FP8_BLOCK) * -(-K // FP8_BLOCK), dev, "scale")
         self.codes, self.scale = codes, scale
 
     def c_struct(self):
@@ -684,9 +687,8 @@ def fp8_quantize_blocks(w, codes=None, scale=None, stream=None):
         codes = torch.empty((N, K), dtype=torch.float8_e4m3fn, device=w.device)
     if scale is None:
         scale = torch.empty((nb, kb), dtype=torch.float32, device=w.device)
-    _dev(codes, torch.float8_e4m3fn, N * K, "codes")
-    _dev(scale, torch.float32, nb * kb, "scale")
-    _all_on(w.device, codes, scale)
+    _fit(codes, torch.float8_e4m3fn, N * K, w.device, "codes")
+    _fit(scale, torch.float32, nb * kb, w.device, "scale")
     _call("fp8_quantize_blocks", w.device, stream, w.data_ptr(),
           QN_F32 if w.dtype == torch.float32 else QN_BF16, N, K, codes.data_ptr(),
           scale.data_ptr())
@@ -711,9 +713,8 @@ def fp8_quantize_rows(x, codes=None, scale=None, stream=None):
         codes = torch.empty((M, K), dtype=torch.float8_e4m3fn, device=x.device)
     if scale is None:
         scale = torch.empty((kb, M), dtype=torch.float32, device=x.device)
-    _dev(codes, torch.float8_e4m3fn, M * K, "codes")
-    _dev(scale, torch.float32, kb * M, "scale")
-    _all_on(x.device, codes, scale)
+    _fit(codes, torch.float8_e4m3fn, M * K, x.device, "codes")
+    _fit(scale, torch.float32, kb * M, x.device, "scale")
     _call("fp8_quantize_rows", x.device, stream, x.data_ptr(), M, K, codes.data_ptr(),
           scale.data_ptr())
     return codes, scale
@@ -725,12 +726,11 @@ def fp8_dequant(fw, out_dtype=None, out=None, stream=None):
     out_dtype = out_dtype or torch.bfloat16
     if out_dtype not in (torch.float32, torch.bfloat16):
         raise ValueError("fp8_dequant: out_dtype must be float32 or bfloat16")
-    dev = fw.codes.device
+    dev = fw.device
     if out is None:
         out = torch.empty((fw.N, fw.K), dtype=out_dtype, device=dev)
-    _dev(out, out_dtype, fw.N * fw.K, "out")
-    _all_on(dev, out)
-    _call("fp8_dequant", dev, stream, ctypes.byref(fw.c_struct()),
+    _fit(out, out_dtype, fw.N * fw.K, dev, "out")
+    _call("fp8_dequant", dev, stream, fw.c_struct(),
           QN_BF16 if out_dtype == torch.bfloat16 else QN_F32, out.data_ptr())
     return out
 
@@ -743,13 +743,13 @@ def fp8_matmul(fw, codes, scale, transposed=False, out=None, stream=None):
     if codes.dim() != 2 or codes.shape[1] != L:
         raise ValueError(f"codes: need [M, {L}]")
     M = codes.shape[0]
-    _dev(codes, torch.float8_e4m3fn, name="codes")
-    _dev(scale, torch.float32, -(-L // FP8_BLOCK) * M, "scale")
+    dev = fw.device
+    _fit(codes, torch.float8_e4m3fn, M * L, dev, "codes")
+    _fit(scale, torch.float32, -(-L // FP8_BLOCK) * M, dev, "scale")
     if out is None:
-        out = torch.empty((M, n), dtype=torch.bfloat16, device=codes.device)
-    _dev(out, torch.bfloat16, M * n, "out")
-    _all_on(codes.device, fw.codes, scale, out)
-    _call("fp8_matmul", codes.device, stream, ctypes.byref(fw.c_struct()), codes.data_ptr(),
+        out = torch.empty((M, n), dtype=torch.bfloat16, device=dev)
+    _fit(out, torch.bfloat16, M * n, dev, "out")
+    _call("fp8_matmul", dev, stream, fw.c_struct(), codes.data_ptr(),
           scale.data_ptr(), M, int(bool(transposed)), out.data_ptr())
     return out
 
@@ -768,24 +768,27 @@ def fp8_linear_bwd_dx(fw, dy, A, B, r, alpha, dx=None, t_out=None, ws=None, stre
 
 def _fp8_linear(fn, op, fw, x, L, n, A, B, r, alpha, out, low, ws, stream):
     torch = _torch()
-    bf16, dev = torch.bfloat16, x.device
+    bf16, dev = torch.bfloat16, fw.device
     M = x.shape[0]
-    _dev(x, bf16, M * L, "x" if op == QN_OP_FP8_FWD else "dy")
+    fwd = op == QN_OP_FP8_FWD
+    _fit(x, bf16, M * L, dev, "x" if fwd else "dy")
+    a = b = None
     if r:
-        _dev(A, bf16, r * fw.K, "A")
-        _dev(B, bf16, fw.N * r, "B")
-    else:
-        A = B = None
+        _fit(A, bf16, r * fw.K, dev, "A")
+        _fit(B, bf16, fw.N * r, dev, "B")
+        a, b = A.data_ptr(), B.data_ptr()
     if out is None:
         out = torch.empty((M, n), dtype=bf16, device=dev)
-    _dev(out, bf16, M * n, "y" if op == QN_OP_FP8_FWD else "dx")
-    _dev(low, bf16, M * r, "u_out" if op == QN_OP_FP8_FWD else "t_out")
+    else:
+        _fit(out, bf16, M * n, dev, "y" if fwd else "dx")
+    if low is not None:
+        _fit(low, bf16, M * r, dev, "u_out" if fwd else "t_out")
     if ws is None:
         ws = workspace(qn_workspace_bytes(op, M, fw.N, fw.K, r), dev)
-    _dev(ws, torch.uint8, name="ws")
-    _all_on(dev, fw.codes, A, B, out, low, ws)
-    _call(fn, dev, stream, ctypes.byref(fw.c_struct()), x.data_ptr(), M, _addr(A), _addr(B), r,
-          alpha, out.data_ptr(), _addr(low), ws.data_ptr(), ws.numel())
+    else:
+        _fit(ws, torch.uint8, ws.numel(), dev, "ws")
+    _call(fn, dev, stream, fw.c_struct(), x.data_ptr(), M, a, b, r, alpha, out.data_ptr(),
+          _addr(low), ws.data_ptr(), ws.numel())
     return out
 
 
@@ -839,8 +842,9 @@ def lora_adamw_table(ps, gs, ms, vs, m_scales=None, v_scales=None, p_bf16s=None)
                 raise ValueError(f"{name}: missing")
             if t is None and eight and name in ("m_scale", "v_scale"):
                 raise ValueError(f"{name}: missing")
-            _dev(t, dt, size, name)
-        _all_on(dev, *row)
+            if t is not None:
+                _dev(t, dt, size, name)
+                _fit(t, dt, size, dev, name)
         arr[i] = qn_adamw_tensor(*[_addr(t) for t in row], k)
     size = lib.lora_adamw_table_bytes(arr, n)
     host = torch.empty(max(size, 1), dtype=torch.uint8)
@@ -852,7 +856,7 @@ def lora_adamw_table(ps, gs, ms, vs, m_scales=None, v_scales=None, p_bf16s=None)
 
 
 def lora_grad_norm_workspace_bytes(table):
-    return int(load_library().lora_grad_norm_workspace_bytes(ctypes.byref(table.plan)))
+    return int(load_library().lora_grad_norm_workspace_bytes(table.plan))
 
 
 def lora_grad_norm(table, max_norm, out=None, ws=None, stream=None):
@@ -862,12 +866,11 @@ def lora_grad_norm(table, max_norm, out=None, ws=None, stream=None):
     dev = table.device
     if out is None:
         out = torch.empty(2, dtype=torch.float32, device=dev)
-    _dev(out, torch.float32, 2, "out")
+    _fit(out, torch.float32, 2, dev, "out")
     if ws is None:
         ws = workspace(lora_grad_norm_workspace_bytes(table), dev)
-    _dev(ws, torch.uint8, name="ws")
-    _all_on(dev, out, ws)
-    _call("lora_grad_norm", dev, stream, ctypes.byref(table.plan), table.table.data_ptr(),
+    _fit(ws, torch.uint8, ws.numel(), dev, "ws")
+    _call("lora_grad_norm", dev, stream, table.plan, table.table.data_ptr(),
           max_norm, out.data_ptr(), ws.data_ptr(), ws.numel())
     return out
 
@@ -879,7 +882,7 @@ def lora_adamw_multi_step(table, step, lr=2e-4, betas=(0.9, 0.999), eps=1e-8, we
     step with one that is not finite does nothing."""
     torch = _torch()
     dev = table.device
-    _dev(grad_scale, torch.float32, 1, "grad_scale")
-    _all_on(dev, grad_scale)
-    _call("lora_adamw_multi_step", dev, stream, ctypes.byref(table.plan), table.table.data_ptr(),
+    if grad_scale is not None:
+        _fit(grad_scale, torch.float32, 1, dev, "grad_scale")
+    _call("lora_adamw_multi_step", dev, stream, table.plan, table.table.data_ptr(),
           _addr(grad_scale), lr, betas[0], betas[1], eps, weight_decay, step)

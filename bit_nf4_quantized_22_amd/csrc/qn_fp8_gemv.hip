@@ -74,6 +74,7 @@ __global__ __launch_bounds__(64 * kWaves) void fp8_decode_kernel(
     for (int i = t; i < (par > 1 ? par * mr : mr); i += kThreads) {
       const int e = i % mr, q0 = i / mr;
       float s = 0.0f;
+#pragma unroll 8
       for (int q = q0; q < slices; q += par) s += part[static_cast<int64_t>(q) * mr + e];
       s_u[i] = s;
     }
