@@ -122,7 +122,7 @@ def load_library():
         "fp8_quantize_blocks": (ctypes.c_int, [vp, i32, i64, i64, vp, vp, vp]),
         "fp8_quantize_rows": (ctypes.c_int, [vp, i64, i64, vp, vp, vp]),
         "fp8_dequant": (ctypes.c_int, [fp, i32, vp, vp]),
-        "fp8_matmul": (ctypes.c_int, [fp, vp, vp, i64, i32, vp, vp]),
+        "fp8_matmul": (ctypes.c_int, [fp, vp, vp, i64, i32, vp, vp, sz, vp]),
         "fp8_linear_fwd": (ctypes.c_int, lin),
         "fp8_linear_bwd_dx": (ctypes.c_int, lin),
         "lora_adamw_table_bytes": (sz, [ap, i32]),
@@ -735,7 +735,7 @@ def fp8_dequant(fw, out_dtype=None, out=None, stream=None):
     return out
 
 
-def fp8_matmul(fw, codes, scale, transposed=False, out=None, stream=None):
+def fp8_matmul(fw, codes, scale, transposed=False, out=None, ws=None, stream=None):
     """x W^T (bf16[M, N]) of x [M, K] from fp8_quantize_rows, or with
     transposed x W (bf16[M, K]) of x [M, N]."""
     torch = _torch()
@@ -749,8 +749,13 @@ def fp8_matmul(fw, codes, scale, transposed=False, out=None, stream=None):
     if out is None:
         out = torch.empty((M, n), dtype=torch.bfloat16, device=dev)
     _fit(out, torch.bfloat16, M * n, dev, "out")
-    _call("fp8_matmul", dev, stream, fw.c_struct(), codes.data_ptr(),
-          scale.data_ptr(), M, int(bool(transposed)), out.data_ptr())
+    if ws is None:
+        ws = workspace(qn_workspace_bytes(QN_OP_FP8_BWD_DX if transposed else QN_OP_FP8_FWD, M,
+                                          fw.N, fw.K, 0), dev)
+    else:
+        _fit(ws, torch.uint8, ws.numel(), dev, "ws")
+    _call("fp8_matmul", dev, stream, fw.c_struct(), codes.data_ptr(), scale.data_ptr(), M,
+          int(bool(transposed)), out.data_ptr(), ws.data_ptr(), ws.numel())
     return out
 
 

@@ -269,26 +269,31 @@ bool fp8_rows_ok(int64_t M, int64_t n) {
   return M >= 0 && M <= INT32_MAX && M * blocks128(n) <= INT32_MAX;
 }
 
-// Workspace of a quantised batch [M, L] and its LoRA projection: codes, row
-// scales, partial sums of the projection, and (but for the decode path) its
-// scaled bf16 sum in padded rows.
+// Workspace of a quantised batch [M, L] with `cols` output columns: codes, row
+// scales, partial sums of the LoRA projection and its scaled bf16 sum in
+// padded rows, partial sums of a split contraction.
 struct Fp8Ws {
-  size_t scale, part, act, total;
+  size_t scale, part, act, split, total;
 };
 
-Fp8Ws fp8_ws(bool bwd, int64_t M, int64_t L, int32_t r) {
+Fp8Ws fp8_ws(bool bwd, int64_t M, int64_t N, int64_t K, int32_t r) {
   Fp8Ws f{};
-  if (M <= 0 || L <= 0) return f;
+  if (M <= 0 || N <= 0 || K <= 0) return f;
+  const int64_t L = bwd ? N : K, cols = bwd ? K : N;
   const size_t m = static_cast<size_t>(M);
   f.scale = round_up(m * static_cast<size_t>(L), 256);
   f.part = f.scale + round_up(m * static_cast<size_t>(blocks128(L)) * 4, 256);
-  f.act = f.total = f.part;
-  if (r == 0) return f;
-  f.act += round_up(m * static_cast<size_t>(r) * 4 *
-                        static_cast<size_t>(qn::fp8_project_slices(M, L)), 256);
-  f.total = f.act;
-  if (bwd || M > qn::kFp8DecodeM)
-    f.total += round_up(m * static_cast<size_t>(qn::fp8_lora_pitch(r)) * 2, 256);
+  f.act = f.part;
+  if (r > 0)
+    f.act += round_up(m * static_cast<size_t>(r) * 4 *
+                          static_cast<size_t>(qn::fp8_project_slices(M, L)), 256);
+  f.split = f.act;
+  if (r > 0 && (bwd || M > qn::kFp8DecodeM))
+    f.split += round_up(m * static_cast<size_t>(qn::fp8_lora_pitch(r)) * 2, 256);
+  f.total = f.split;
+  const int splits = bwd || M > qn::kFp8FewM ? qn::fp8_gemm_splits(M, cols, L) : 1;
+  if (splits > 1)
+    f.total += m * static_cast<size_t>(cols) * 4 * static_cast<size_t>(splits);
   return f;
 }
 
@@ -309,27 +314,35 @@ int fp8_linear(bool bwd, const qn_fp8_weight* w, const qn_bf16* in, int64_t M, c
   if (!aligned(in, 16) || !aligned(out, 16) || (r > 0 && (!aligned(A, 2) || !aligned(B, 2))) ||
       !aligned(low_out, 2))
     return QN_ERR_ALIGN;
-  const Fp8Ws f = fp8_ws(bwd, M, L, r);
+  const Fp8Ws f = fp8_ws(bwd, M, v.N, v.K, r);
   if (!ws || ws_bytes < f.total) return QN_ERR_WORKSPACE;
   if (!aligned(ws, 16)) return QN_ERR_ALIGN;
   hipStream_t s = as_stream(stream);
   (void)hipGetLastError();
+  const float ls = r > 0 ? alpha / static_cast<float>(r) : 0.0f;
+  qn_bf16* low = r > 0 ? low_out : nullptr;
+  if (!bwd && M == 1 && qn::fp8_token_self_u(v, r))
+    return hip_status(qn::launch_fp8_token(v, in, A, B, r, ls, out, low, s));
   uint8_t* codes = static_cast<uint8_t*>(ws);
   float* scale = reinterpret_cast<float*>(codes + f.scale);
   float* part = reinterpret_cast<float*>(codes + f.part);
   uint16_t* act = reinterpret_cast<uint16_t*>(codes + f.act);
-  const float ls = r > 0 ? alpha / static_cast<float>(r) : 0.0f;
-  hipError_t e = r > 0 ? qn::launch_fp8_quantize_project(in, M, L, bwd ? B : A, r, bwd, codes,
-                                                         scale, part, s)
-                       : qn::launch_fp8_quantize_rows(in, M, L, codes, scale, s);
+  float* split = f.total > f.split ? reinterpret_cast<float*>(codes + f.split) : nullptr;
+  const bool decode = !bwd && M <= qn::kFp8DecodeM, few = !bwd && M <= qn::kFp8FewM;
+  const int m32 = static_cast<int>(few ? M : 0);
+  hipError_t e = r == 0   ? qn::launch_fp8_quantize_rows(in, M, L, codes, scale, s)
+                 : decode ? qn::launch_fp8_decode_project(in, m32, L, A, r, codes, scale, part, s)
+                          : qn::launch_fp8_quantize_project(in, M, L, bwd ? B : A, r, bwd, codes,
+                                                            scale, part, s);
   if (e != hipSuccess) return QN_ERR_HIP;
-  const int slices = r > 0 ? qn::fp8_project_slices(M, L) : 0;
-  if (!bwd && M <= qn::kFp8DecodeM)
-    return hip_status(qn::launch_fp8_decode(v, codes, scale, static_cast<int>(M), part, slices, B,
-                                            r, ls, out, r > 0 ? low_out : nullptr, s));
-  if (r > 0 && qn::launch_fp8_project_sum(part, slices, M, r, ls, act, low_out, s) != hipSuccess)
+  if (r > 0 && !decode &&
+      qn::launch_fp8_project_sum(part, qn::fp8_project_slices(M, L), M, r, ls, act, low, s) !=
+          hipSuccess)
     return QN_ERR_HIP;
-  return hip_status(qn::launch_fp8_gemm(v, codes, scale, M, act, bwd ? A : B, r, bwd, out, s));
+  if (few)
+    return hip_status(qn::launch_fp8_decode(v, codes, scale, m32, part, qn::fp8_decode_slices(L),
+                                            act, B, r, ls, out, low, s));
+  return hip_status(qn::launch_fp8_gemm(v, codes, scale, M, act, bwd ? A : B, r, bwd, out, split, s));
 }
 
 bool adamw_hyper_ok(float lr, float beta1, float beta2, float eps, float weight_decay) {
@@ -553,8 +566,8 @@ size_t qn_workspace_bytes(int32_t op, int64_t M, int64_t N, int64_t K, int32_t r
     case QN_OP_BWD_DX: return bwd_ws(M, N, r);
     case QN_OP_LORA_GRADS: return grads_ws(M, N, K, r);
     case QN_OP_BWD_DX_DROPOUT: return bwd_drop_ws(M, N, K, r);
-    case QN_OP_FP8_FWD: return fp8_ws(false, M, K, r).total;
-    case QN_OP_FP8_BWD_DX: return fp8_ws(true, M, N, r).total;
+    case QN_OP_FP8_FWD: return fp8_ws(false, M, N, K, r).total;
+    case QN_OP_FP8_BWD_DX: return fp8_ws(true, M, N, K, r).total;
     default: return 0;
   }
 }
@@ -678,7 +691,7 @@ int fp8_dequant(const qn_fp8_weight* w, int32_t out_dtype, void* out, void* stre
 }
 
 int fp8_matmul(const qn_fp8_weight* w, const uint8_t* x, const float* xscale, int64_t M,
-               int32_t transposed, qn_bf16* out, void* stream) {
+               int32_t transposed, qn_bf16* out, void* ws, size_t ws_bytes, void* stream) {
   qn::Fp8View v;
   if (int st = check_fp8_weight(w, v); st != QN_OK) return st;
   if (transposed != 0 && transposed != 1) return QN_ERR_UNSUPPORTED;
@@ -686,13 +699,18 @@ int fp8_matmul(const qn_fp8_weight* w, const uint8_t* x, const float* xscale, in
   if (M == 0) return QN_OK;
   if (!x || !xscale || !out) return QN_ERR_NULL;
   if (!aligned(x, 16) || !aligned(xscale, 4) || !aligned(out, 16)) return QN_ERR_ALIGN;
+  const Fp8Ws f = fp8_ws(transposed == 1, M, v.N, v.K, 0);
+  if (!ws || ws_bytes < f.total) return QN_ERR_WORKSPACE;
+  if (!aligned(ws, 16)) return QN_ERR_ALIGN;
+  float* split =
+      f.total > f.split ? reinterpret_cast<float*>(static_cast<char*>(ws) + f.split) : nullptr;
   (void)hipGetLastError();
   hipStream_t s = as_stream(stream);
-  if (!transposed && M <= qn::kFp8DecodeM)
+  if (!transposed && M <= qn::kFp8FewM)
     return hip_status(qn::launch_fp8_decode(v, x, xscale, static_cast<int>(M), nullptr, 0, nullptr,
-                                            0, 0.0f, out, nullptr, s));
+                                            nullptr, 0, 0.0f, out, nullptr, s));
   return hip_status(
-      qn::launch_fp8_gemm(v, x, xscale, M, nullptr, nullptr, 0, transposed == 1, out, s));
+      qn::launch_fp8_gemm(v, x, xscale, M, nullptr, nullptr, 0, transposed == 1, out, split, s));
 }
 
 int fp8_linear_fwd(const qn_fp8_weight* w, const qn_bf16* x, int64_t M, const qn_bf16* A,

@@ -49,6 +49,7 @@ struct Fp8Args {
   int r, pitch;
   bool vec_w;           // lw can be read 16 bytes at a time
   uint16_t* out;
+  float* part;          // [splits][M][ncols] fp32 instead of out, or nullptr
 };
 
 template <int kWTM_, int kGM_, int kGN_, int kBuf_>
@@ -206,15 +207,17 @@ __device__ __forceinline__ void add_pending(const Pending<T>& p, int j, f32x4_t&
   for (int e = 0; e < 4; ++e) acc[e] = fmaf(p.c[j][e], p.f, acc[e]);
 }
 
-// One output tile: rows from m0, columns from c0.
+// One output tile: rows from m0, columns from c0, the contraction's blocks
+// from b0, nfull whole ones and a tail of `tail` values behind them; the LoRA
+// term is added where first is set.
 template <typename T, bool kBwd>
-__device__ __forceinline__ void fp8_tile(const Fp8Args& g, uint8_t* smem, int64_t m0, int64_t c0) {
+__device__ __forceinline__ void fp8_tile(const Fp8Args& g, uint8_t* smem, int64_t m0, int64_t c0,
+                                         int b0, int nfull, int tail, bool first, int split) {
   const int t = threadIdx.x, lane = t & 63;
   const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
   const int wm = wave / T::kGN, wn = wave % T::kGN;
   const int li = lane & 15, lg = lane >> 4;
   const int64_t ncols = kBwd ? g.K : g.N, L = kBwd ? g.N : g.K;
-  const int nfull = static_cast<int>(L / 128), tail = static_cast<int>(L % 128);
   const int64_t kb = (g.K + 127) / 128;
   // byte offsets of this lane's DMA sources; rows and columns past the edge
   // re-read the last valid ones (they only feed outputs that are not stored)
@@ -249,9 +252,11 @@ __device__ __forceinline__ void fp8_tile(const Fp8Args& g, uint8_t* smem, int64_
       tok ? (m0 + srow < g.M ? srow : g.M - 1 - m0) * 4 : (cblk - c0 / 128) * (kBwd ? 1 : kb) * 4);
   const float* baseS = tok ? g.xs + m0 : kBwd ? g.ws + c0 / 128 : g.ws + c0 / 128 * kb;
   const int64_t stepS = tok ? g.M : kBwd ? kb : 1;
+  baseS += b0 * stepS;
   const uint32_t dstS = tok ? T::kScales + wave * 256 : T::kWScales;
-  const uint8_t* baseA = g.x + m0 * L;
-  const uint8_t* baseB = kBwd ? g.w + c0 : g.w + c0 * L;
+  const uint8_t* baseA = g.x + m0 * L + static_cast<int64_t>(b0) * 128;
+  const uint8_t* baseB = kBwd ? g.w + c0 + static_cast<int64_t>(b0) * 128 * g.K
+                              : g.w + c0 * L + static_cast<int64_t>(b0) * 128;
   const uint32_t lds0 = lds_addr(smem);
   // share q of the DMAs of block b, into buffer buf
   constexpr int kDma = T::kDmaA + T::kDmaB;
@@ -348,7 +353,7 @@ __device__ __forceinline__ void fp8_tile(const Fp8Args& g, uint8_t* smem, int64_
   // (padded rows of 128 bytes) by DMA, the adapter's from where it lies,
   // through registers: rows of B as the codes' rows, or A's 64 rows of kBN
   // columns, which the transposing LDS loads read.
-  for (int lb = 0; lb * 64 < g.r; ++lb) {
+  for (int lb = 0; first && lb * 64 < g.r; ++lb) {
     uint8_t* st = smem + (lb & 1) * T::kStage;
     const uint16_t* pa = g.act + m0 * g.pitch + lb * 64;
 #pragma unroll
@@ -435,7 +440,7 @@ __device__ __forceinline__ void fp8_tile(const Fp8Args& g, uint8_t* smem, int64_
   if (tail) {
     // the last, partial block: through registers, zeros behind its end
     uint8_t* st = smem + (nfull & 1) * T::kStage;
-    const int64_t l0 = static_cast<int64_t>(nfull) * 128;
+    const int64_t bt = b0 + nfull, l0 = bt * 128;
     auto row_tile = [&](uint8_t* dst, const uint8_t* src, int64_t row0, int64_t rows, int count) {
       for (int q = t; q < count * 8; q += T::kThreads) {
         const int row = q >> 3, c = q & 7;
@@ -461,10 +466,10 @@ __device__ __forceinline__ void fp8_tile(const Fp8Args& g, uint8_t* smem, int64_
     }
     float* sS = reinterpret_cast<float*>(st + T::kScales);
     for (int q = t; q < T::kBM; q += T::kThreads)
-      sS[q] = g.xs[nfull * g.M + (m0 + q < g.M ? m0 + q : g.M - 1)];
+      sS[q] = g.xs[bt * g.M + (m0 + q < g.M ? m0 + q : g.M - 1)];
     if (t < 4) {
       const int64_t c = c0 / 128 + t < cmax ? c0 / 128 + t : cmax;
-      reinterpret_cast<float*>(st + T::kWScales)[t] = g.ws[kBwd ? nfull * kb + c : c * kb + nfull];
+      reinterpret_cast<float*>(st + T::kWScales)[t] = g.ws[kBwd ? bt * kb + c : c * kb + bt];
     }
     __syncthreads();
 Ahead<T> f;
@@ -482,6 +487,17 @@ Ahead<T> f;
     }
   }
 
+  if (g.part) {
+    float* part = g.part + static_cast<int64_t>(split) * g.M * ncols;
+#pragma unroll
+    for (int i = 0; i < T::kTI; ++i)
+#pragma unroll
+      for (int j = 0; j < T::kTJ; ++j) {
+        const int64_t m = m0 + wm * T::kWTM + i * 16 + li, n = c0 + wn * 64 + j * 16 + 4 * lg;
+        if (m < g.M && n < ncols) *reinterpret_cast<f32x4_t*>(part + m * ncols + n) = acc[i][j];
+      }
+    return;
+  }
   // Epilogue: lane (li, lg) holds columns 16 j + 4 lg .. + 3 of token 16 i +
   // li.  Each wave turns its tile to bf16 through LDS, 64 tokens at a time,
   // and stores whole 128-byte row segments.
@@ -532,44 +548,74 @@ __global__ __launch_bounds__(Big::kThreads, 2) void fp8_gemm_kernel(Fp8Args g, i
   const int nc = static_cast<int>(((kBwd ? g.K : g.N) + Big::kBN - 1) / Big::kBN);
   const int nr = static_cast<int>((g.M + Big::kBM - 1) / Big::kBM);
   const int bid = blockIdx.x;
+  const int64_t L = kBwd ? g.N : g.K;
+  const int nfull = static_cast<int>(L / 128), tail = static_cast<int>(L % 128);
   int row, col;
   if (bid < nbig) {
     fp8_tile_of(xcd_run(bid, nbig), nc, nr, row, col);
     fp8_tile<Big, kBwd>(g, smem, static_cast<int64_t>(row) * Big::kBM,
-                        static_cast<int64_t>(col) * Big::kBN);
+                        static_cast<int64_t>(col) * Big::kBN, 0, nfull, tail, true, 0);
   } else {
     const int q = xcd_run(bid - nbig, 2 * (nc * nr - nbig));
     fp8_tile_of(nbig + (q >> 1), nc, nr, row, col);
     const int64_t m0 = static_cast<int64_t>(row) * Big::kBM + (q & 1) * Half::kBM;
-    if (m0 < g.M) fp8_tile<Half, kBwd>(g, smem, m0, static_cast<int64_t>(col) * Half::kBN);
+    if (m0 < g.M)
+      fp8_tile<Half, kBwd>(g, smem, m0, static_cast<int64_t>(col) * Half::kBN, 0, nfull, tail,
+                           true, 0);
   }
 }
 
+// Workgroup row z takes the blocks z per .. of the contraction; the last one
+// has the tail too.
 template <bool kBwd>
-__global__ __launch_bounds__(Small::kThreads, 2) void fp8_gemm_small_kernel(Fp8Args g) {
+__global__ __launch_bounds__(Small::kThreads, 2) void fp8_gemm_small_kernel(Fp8Args g, int per) {
   __shared__ __attribute__((aligned(1024))) uint8_t smem[Small::kBuf * Small::kStage];
   const int nc = static_cast<int>(((kBwd ? g.K : g.N) + Small::kBN - 1) / Small::kBN);
   const int nr = static_cast<int>((g.M + Small::kBM - 1) / Small::kBM);
+  const int64_t L = kBwd ? g.N : g.K;
+  const int whole = static_cast<int>(L / 128), b0 = static_cast<int>(blockIdx.y) * per;
+  const bool last = blockIdx.y + 1 == gridDim.y;
   int row, col;
   fp8_tile_of(xcd_run(blockIdx.x, nc * nr), nc, nr, row, col);
   fp8_tile<Small, kBwd>(g, smem, static_cast<int64_t>(row) * Small::kBM,
-                        static_cast<int64_t>(col) * Small::kBN);
+                        static_cast<int64_t>(col) * Small::kBN, b0, last ? whole - b0 : per,
+                        last ? static_cast<int>(L % 128) : 0, blockIdx.y == 0,
+                        static_cast<int>(blockIdx.y));
+}
+
+// Large tiles for this many outputs?
+bool large(int64_t M, int64_t ncols) {
+  return ((ncols + Big::kBN - 1) / Big::kBN) * ((M + Big::kBM - 1) / Big::kBM) >= 64;
 }
 
 }  // namespace
 
+int fp8_gemm_splits(int64_t M, int64_t ncols, int64_t L) {
+  if (M <= 0 || large(M, ncols)) return 1;
+  const int64_t tiles = ((ncols + Small::kBN - 1) / Small::kBN) *
+                        ((M + Small::kBM - 1) / Small::kBM);
+  // two workgroups per CU, at least 4 blocks each
+  int64_t s = 512 / tiles;
+  const int64_t most = L / 128 / 4;
+  s = s < most ? s : most;
+  if (s < 2) return 1;
+  const int64_t per = (L / 128 + s - 1) / s;
+  return static_cast<int>((L / 128 + per - 1) / per);
+}
+
 hipError_t launch_fp8_gemm(const Fp8View& w, const uint8_t* x, const float* xs, int64_t M,
                            const uint16_t* act, const uint16_t* lw, int r, bool bwd, uint16_t* out,
-                           hipStream_t st) {
+                           float* part, hipStream_t st) {
   if (M == 0) return hipSuccess;
   // rows of B have r values, those of A K, a multiple of 16
   const bool vec_w = (reinterpret_cast<uintptr_t>(lw) & 15) == 0 && (bwd || (r & 7) == 0);
-  Fp8Args g{w.codes, w.scale, x, xs, M, w.N, w.K, act, lw, r, fp8_lora_pitch(r), vec_w, out};
-  const int64_t ncols = bwd ? w.K : w.N;
-  const int64_t tiles = ((ncols + Big::kBN - 1) / Big::kBN) * ((M + Big::kBM - 1) / Big::kBM);
-  if (tiles >= 64) {
+  const int64_t ncols = bwd ? w.K : w.N, L = bwd ? w.N : w.K;
+  Fp8Args g{w.codes, w.scale, x, xs, M, w.N, w.K, act, lw, r, fp8_lora_pitch(r), vec_w, out,
+            nullptr};
+  if (large(M, ncols)) {
     // whole rounds of the 256 CUs in large tiles, a remainder of up to half
     // a round in halves
+    const int64_t tiles = ((ncols + Big::kBN - 1) / Big::kBN) * ((M + Big::kBM - 1) / Big::kBM);
     const int64_t rest = tiles % 256;
     const int64_t nbig = rest <= 128 ? tiles - rest : tiles;
     const dim3 grid(static_cast<uint32_t>(nbig + 2 * (tiles - nbig)));
@@ -581,13 +627,18 @@ hipError_t launch_fp8_gemm(const Fp8View& w, const uint8_t* x, const float* xs, 
                          static_cast<int>(nbig));
     return hipGetLastError();
   }
+  const int splits = part ? fp8_gemm_splits(M, ncols, L) : 1;
+  const int per = static_cast<int>((L / 128 + splits - 1) / splits);
+  if (splits > 1) g.part = part;
   const dim3 grid(static_cast<uint32_t>(((ncols + Small::kBN - 1) / Small::kBN) *
-                                        ((M + Small::kBM - 1) / Small::kBM)));
+                                        ((M + Small::kBM - 1) / Small::kBM)),
+                  static_cast<uint32_t>(splits));
   if (bwd)
-    hipLaunchKernelGGL(fp8_gemm_small_kernel<true>, grid, dim3(Small::kThreads), 0, st, g);
+    hipLaunchKernelGGL(fp8_gemm_small_kernel<true>, grid, dim3(Small::kThreads), 0, st, g, per);
   else
-    hipLaunchKernelGGL(fp8_gemm_small_kernel<false>, grid, dim3(Small::kThreads), 0, st, g);
-  return hipGetLastError();
+    hipLaunchKernelGGL(fp8_gemm_small_kernel<false>, grid, dim3(Small::kThreads), 0, st, g, per);
+  const hipError_t e = hipGetLastError();
+  return splits > 1 && e == hipSuccess ? launch_fp8_split_sum(part, splits, M * ncols, out, st) : e;
 }
 
 }  // namespace qn

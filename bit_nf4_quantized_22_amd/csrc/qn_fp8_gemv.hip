@@ -1,15 +1,20 @@
-// Block-scaled FP8 product for up to 16 tokens (gfx950).
+// Block-scaled FP8 products for up to 64 tokens (gfx950).
 //
 //   y[m, n] = sum_b xs[b, m] ws[n / 128, b] (xq_b[m] . wq_b[n]) + (s u) B^T
 //
 // Bound by reading the weight once (N K bytes).  A workgroup owns 16 output
 // columns and the whole contraction: its waves take the blocks of 128 in
 // turn, each block one 16x16x128 FP8 MFMA with the weight's rows as the first
-// operand and the tokens (padded to 16 by re-reading the last) as the second.
+// operand and 16 tokens (the last one again past the end) as the second.
 // Every lane loads 32 consecutive bytes of its row straight into its
-// fragment, kDepth blocks ahead of their products, so the weight needs
-// neither LDS nor a second pass.  The waves' fp32 sums meet in LDS and are
-// added in wave order, so results are bit-reproducible.
+// fragment, some blocks ahead of their products, so the weight needs neither
+// LDS nor a second pass.  The waves' fp32 sums meet in LDS and are added in
+// wave order, so results are bit-reproducible.
+//
+// One token: the same launch quantises x and, where the adapter is small,
+// computes u = x A^T, each wave for its own blocks: at 4096 x 4096 the whole
+// call is one launch.  More tokens: x's codes and u's partial sums come from
+// a launch before.
 
 #include "qn_fp8.h"
 #include "qn_launch.h"
@@ -18,127 +23,317 @@ namespace qn {
 
 namespace {
 
-constexpr int kDepth = 4;  // blocks in flight per wave
 constexpr int kMaxRank = 128;
 
-struct Block {
-  uint4 w0, w1, x0, x1;
-  float s;
+// This lane's 32 bytes of block b of a row, zeros behind the row's end.
+struct Bytes32 {
+  uint4 lo, hi;
 };
 
-template <int kWaves>
-__global__ __launch_bounds__(64 * kWaves) void fp8_decode_kernel(
+__device__ __forceinline__ Bytes32 row_bytes(const uint8_t* row, int64_t b, int64_t K, int lg) {
+  const int64_t k = b * 128 + 32 * lg;
+  Bytes32 v{make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
+  if (k < K) v.lo = *reinterpret_cast<const uint4*>(row + k);
+  if (k + 16 < K) v.hi = *reinterpret_cast<const uint4*>(row + k + 16);
+  return v;
+}
+
+// LoRA-up term of 16 tokens: acc += B[n rows] us^T, us rows of `pitch` bf16
+// (zero past r) at sus, B's fragments already in registers.
+template <int kFrags>
+__device__ __forceinline__ f32x4_t lora_up(f32x4_t acc, const uint4 (&bf)[kFrags],
+                                           const uint16_t* sus, int pitch, int r, int li, int lg) {
+#pragma unroll
+  for (int q = 0; q < kFrags; ++q)
+    if (32 * q < r)
+      acc = mfma_bf16_32(bf[q], *reinterpret_cast<const uint4*>(sus + li * pitch + 32 * q + 8 * lg),
+                         acc);
+  return acc;
+}
+
+__device__ __forceinline__ void store_columns(uint16_t* y, f32x4_t acc) {
+  *reinterpret_cast<uint2*>(y) =
+      make_uint2(pack_bf16x2(acc[0], acc[1]), pack_bf16x2(acc[2], acc[3]));
+}
+
+// One token.  kRT: 16-rank tiles of the projection computed here; with kRT ==
+// 0 and r > 0 u comes as `slices` partial sums.
+template <int kRT>
+__global__ __launch_bounds__(1024) void fp8_token_kernel(
     const uint8_t* __restrict__ w, const float* __restrict__ ws, int64_t N, int64_t K,
-    const uint8_t* __restrict__ x, const float* __restrict__ xs, int M,
-    const float* __restrict__ part, int slices, const uint16_t* __restrict__ B, int r, bool vec_b,
-    float lora_scale, uint16_t* __restrict__ y, uint16_t* __restrict__ u_out) {
-  constexpr int kThreads = 64 * kWaves;
-  __shared__ f32x4_t s_acc[kWaves][64];
-  __shared__ float s_u[kFp8DecodeM * kMaxRank];                     // slices of u, then u
-  __shared__ __attribute__((aligned(16))) uint16_t s_us[16 * kMaxRank];  // bf16(s u), [16][rp]
+    const uint16_t* __restrict__ x, const uint16_t* __restrict__ A, bool vec_a,
+    const uint16_t* __restrict__ B, int r, bool vec_b, float lora_scale, uint16_t* __restrict__ y,
+    uint16_t* __restrict__ u_out) {
+  constexpr int kWaves = 16, kAhead = 2;
+  constexpr int kR = kRT > 0 ? kRT : 1;
+  __shared__ f32x4_t s_acc[kWaves][4];
+  __shared__ f32x4_t s_u[kR][kWaves][4];
+  __shared__ __attribute__((aligned(16))) uint16_t s_us[16 * kR + 16];
+  __shared__ __attribute__((aligned(16))) uint32_t s_x[kWaves][kAhead][64];   // bf16 pairs
+  __shared__ __attribute__((aligned(16))) uint16_t s_q[kWaves][kAhead][64];   // code pairs
   const int t = threadIdx.x, lane = t & 63;
   const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
   const int li = lane & 15, lg = lane >> 4;
   const int64_t n0 = static_cast<int64_t>(blockIdx.x) * 16;  // N is a multiple of 16
   const int64_t kb = (K + 127) / 128;
-  const int m = li < M ? li : M - 1;
   const uint8_t* wr = w + (n0 + li) * K;
-  const uint8_t* xr = x + static_cast<int64_t>(m) * K;
   const float* wsr = ws + (n0 / 128) * kb;
 
-  auto load = [&](int64_t b, Block& d) {
-    const int64_t k = b * 128 + 32 * lg;
-    const uint4 z = make_uint4(0, 0, 0, 0);
-    d.w0 = d.w1 = d.x0 = d.x1 = z;
-    d.s = 0.0f;
-    if (b >= kb) return;
-    if (k < K) {
-      d.w0 = *reinterpret_cast<const uint4*>(wr + k);
-      d.x0 = *reinterpret_cast<const uint4*>(xr + k);
-    }
-    if (k + 16 < K) {
-      d.w1 = *reinterpret_cast<const uint4*>(wr + k + 16);
-      d.x1 = *reinterpret_cast<const uint4*>(xr + k + 16);
-    }
-    d.s = xs[b * M + m] * wsr[b];
-  };
-  Block blk[kDepth];
+  uint4 bf[(kR + 1) / 2];
+  if (kRT > 0 && wave == 0) {
 #pragma unroll
-  for (int d = 0; d < kDepth; ++d) load(wave + d * kWaves, blk[d]);
-
-  // u = sum of its slices: as many slices at a time as there are threads,
-  // then the partial sums, in a fixed order
-  const int mr = M * r;
-  if (r > 0) {
-    const int par = mr <= kThreads ? kThreads / mr : 1;
-    for (int i = t; i < (par > 1 ? par * mr : mr); i += kThreads) {
-      const int e = i % mr, q0 = i / mr;
-      float s = 0.0f;
-#pragma unroll 8
-      for (int q = q0; q < slices; q += par) s += part[static_cast<int64_t>(q) * mr + e];
-      s_u[i] = s;
-    }
-    __syncthreads();
-    const int rp = (r + 31) & ~31;
-    for (int i = t; i < 16 * rp; i += kThreads) {
-      const int row = i / rp, j = i % rp;
-      float s = 0.0f;
-      if (row < M && j < r) {
-        for (int q = 0; q < par; ++q) s += s_u[q * mr + row * r + j];
-        if (u_out && blockIdx.x == 0)
-          u_out[row * r + j] = static_cast<uint16_t>(pack_bf16x2(s, 0.f) & 0xFFFF);
+    for (int q = 0; q < (kR + 1) / 2; ++q)
+      bf[q] = load_bf16x8(B + (n0 + li) * r + 32 * q + 8 * lg, r - 32 * q - 8 * lg, vec_b);
+  }
+  f32x4_t acc = f32x4_t{0.f, 0.f, 0.f, 0.f}, ua[kR];
+#pragma unroll
+  for (int i = 0; i < kR; ++i) ua[i] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+  for (int64_t bw = wave; bw < kb; bw += kAhead * kWaves) {
+    // everything that these blocks need is asked for first
+    Bytes32 wv[kAhead];
+    uint32_t xp[kAhead];
+    float sw[kAhead];
+    uint4 av[kAhead][kR][4];
+#pragma unroll
+    for (int d = 0; d < kAhead; ++d) {
+      const int64_t b = bw + d * kWaves;
+      const bool in = b < kb;
+      const int64_t k = b * 128 + 2 * lane;
+      xp[d] = in && k < K ? *reinterpret_cast<const uint32_t*>(x + k) : 0u;
+      wv[d] = row_bytes(wr, in ? b : kb, K, lg);
+      sw[d] = in ? wsr[b] : 0.0f;
+      if constexpr (kRT > 0) {
+#pragma unroll
+        for (int i = 0; i < kRT; ++i)
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            const int64_t ka = b * 128 + 32 * c + 8 * lg;
+            const int j = 16 * i + li;
+            av[d][i][c] = load_bf16x8(A + j * K + ka, j < r && in && ka < K ? 8 : 0, vec_a);
+          }
       }
-      s_us[i] = static_cast<uint16_t>(pack_bf16x2(s * lora_scale, 0.f) & 0xFFFF);
+    }
+#pragma unroll
+    for (int d = 0; d < kAhead; ++d) {
+      const float x0 = bf16_lo(xp[d]), x1 = bf16_hi(xp[d]);
+      const float s = fp8_scale(wave_max(fmaxf(fabsf(x0), fabsf(x1))));
+      const float inv = __fdiv_rn(1.0f, s);
+      s_x[wave][d][lane] = xp[d];
+      s_q[wave][d][lane] = static_cast<uint16_t>(__builtin_amdgcn_cvt_pk_fp8_f32(
+          fp8_ratio(x0, s, inv), fp8_ratio(x1, s, inv), 0, false));
+      sw[d] *= s;
+    }
+    // written and read by the same wave: its own LDS order suffices
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+#pragma unroll
+    for (int d = 0; d < kAhead; ++d) {
+      const uint4* q = reinterpret_cast<const uint4*>(&s_q[wave][d][16 * lg]);
+      const f32x4_t c =
+          mfma_fp8(frag8(wv[d].lo, wv[d].hi), frag8(q[0], q[1]), f32x4_t{0.f, 0.f, 0.f, 0.f});
+#pragma unroll
+      for (int e = 0; e < 4; ++e) acc[e] = fmaf(c[e], sw[d], acc[e]);
+      if constexpr (kRT > 0) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const uint4 xf = *reinterpret_cast<const uint4*>(&s_x[wave][d][16 * k + 4 * lg]);
+#pragma unroll
+          for (int i = 0; i < kRT; ++i) ua[i] = mfma_bf16_32(av[d][i][k], xf, ua[i]);
+        }
+      }
+    }
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // read before the next blocks' values
+  }
+  // all 16 result columns are the same token: keep column 0
+  if (li == 0) {
+    s_acc[wave][lg] = acc;
+    if constexpr (kRT > 0) {
+#pragma unroll
+      for (int i = 0; i < kRT; ++i) s_u[i][wave][lg] = ua[i];
     }
   }
-
-  f32x4_t acc = f32x4_t{0.f, 0.f, 0.f, 0.f};
-  for (int64_t b = wave; b < kb; b += kDepth * kWaves) {
-#pragma unroll
-    for (int d = 0; d < kDepth; ++d) {
-      const f32x4_t c = mfma_fp8(frag8(blk[d].w0, blk[d].w1), frag8(blk[d].x0, blk[d].x1),
-                                 f32x4_t{0.f, 0.f, 0.f, 0.f});
-      const float s = blk[d].s;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) acc[e] = fmaf(c[e], s, acc[e]);
-      load(b + (d + kDepth) * kWaves, blk[d]);
-    }
-  }
-  s_acc[wave][lane] = acc;
   __syncthreads();
   if (wave > 0) return;
 #pragma unroll
-  for (int q = 1; q < kWaves; ++q) acc += s_acc[q][lane];
-  if (r > 0) {
-    const int rp = (r + 31) & ~31;
-    for (int j0 = 0; j0 < r; j0 += 32) {
-      const int j = j0 + 8 * lg;
-      const uint4 bf = load_bf16x8(B + (n0 + li) * r + j, r - j, vec_b);
-      const uint4 uf = *reinterpret_cast<const uint4*>(s_us + li * rp + j);
-      acc = mfma_bf16_32(bf, uf, acc);
+  for (int q = 0; q < kWaves; ++q) acc = q == 0 ? s_acc[0][lg] : acc + s_acc[q][lg];
+  if constexpr (kRT > 0) {
+    if (lane < 16 * kRT) {
+      float s = 0.0f;
+#pragma unroll
+      for (int q = 0; q < kWaves; ++q) s += s_u[lane >> 4][q][(lane >> 2) & 3][lane & 3];
+      if (u_out && blockIdx.x == 0 && lane < r)
+        u_out[lane] = static_cast<uint16_t>(pack_bf16x2(s, 0.f) & 0xFFFF);
+      // ranks from r on are zero: their rows of A were read as zeros
+      s_us[lane] = static_cast<uint16_t>(pack_bf16x2(s * lora_scale, 0.f) & 0xFFFF);
+    } else if (lane < 16 * kRT + 16) {
+      s_us[lane] = 0;
+    }
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    acc = lora_up(acc, bf, s_us, 0, r, li, lg);
+  }
+  if (li == 0) store_columns(y + n0 + 4 * lg, acc);
+}
+
+// Up to 16 kMT tokens, codes and scales of x given; u as `slices` partial
+// sums (kMT == 1), or act = bf16(s u) in rows of `pitch` values.
+template <int kWaves, int kMT>
+__global__ __launch_bounds__(64 * kWaves) void fp8_decode_kernel(
+    const uint8_t* __restrict__ w, const float* __restrict__ ws, int64_t N, int64_t K,
+    const uint8_t* __restrict__ x, const float* __restrict__ xs, int M,
+    const float* __restrict__ part, int slices, const uint16_t* __restrict__ act, int pitch,
+    const uint16_t* __restrict__ B, int r, bool vec_b, float lora_scale, uint16_t* __restrict__ y,
+    uint16_t* __restrict__ u_out) {
+  constexpr int kThreads = 64 * kWaves;
+  constexpr int kAhead = kMT <= 2 ? 2 : 1;  // blocks in flight besides the one multiplied
+  static_assert(kMT <= kWaves, "a wave finishes 16 tokens");
+  __shared__ f32x4_t s_acc[kWaves][kMT][64];
+  __shared__ float s_u[kMT == 1 ? kFp8DecodeM * kMaxRank : 1];
+  __shared__ __attribute__((aligned(16))) uint16_t s_us[kMT == 1 ? 16 * kMaxRank : 8];
+  const int t = threadIdx.x, lane = t & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
+  const int li = lane & 15, lg = lane >> 4;
+  const int64_t n0 = static_cast<int64_t>(blockIdx.x) * 16;  // N is a multiple of 16
+  const int64_t kb = (K + 127) / 128;
+  const uint8_t* wr = w + (n0 + li) * K;
+  const float* wsr = ws + (n0 / 128) * kb;
+  int m[kMT];
+#pragma unroll
+  for (int i = 0; i < kMT; ++i) m[i] = 16 * i + li < M ? 16 * i + li : M - 1;
+
+  struct Block {
+    Bytes32 w, x[kMT];
+    float sw, sx[kMT];
+  };
+  auto load = [&](int64_t b, Block& d) {
+    const bool in = b < kb;
+    d.w = row_bytes(wr, in ? b : kb, K, lg);
+    d.sw = in ? wsr[b] : 0.0f;
+#pragma unroll
+    for (int i = 0; i < kMT; ++i) {
+      d.x[i] = row_bytes(x + m[i] * K, in ? b : kb, K, lg);
+      d.sx[i] = in ? xs[b * M + m[i]] : 0.0f;
+    }
+  };
+  Block blk[kAhead + 1];
+#pragma unroll
+  for (int d = 0; d <= kAhead; ++d) load(wave + d * kWaves, blk[d]);
+  uint4 bf[kMaxRank / 32];
+  if (wave < kMT) {
+#pragma unroll
+    for (int q = 0; q < kMaxRank / 32; ++q) {
+      bf[q] = make_uint4(0, 0, 0, 0);
+      if (32 * q < r)
+        bf[q] = load_bf16x8(B + (n0 + li) * r + 32 * q + 8 * lg, r - 32 * q - 8 * lg, vec_b);
     }
   }
-  // lane (li, lg): columns n0 + 4 lg .. + 3 of token li
-  if (li < M)
-    *reinterpret_cast<uint2*>(y + static_cast<int64_t>(li) * N + n0 + 4 * lg) =
-        make_uint2(pack_bf16x2(acc[0], acc[1]), pack_bf16x2(acc[2], acc[3]));
+
+  if constexpr (kMT == 1) {
+    // u = sum of its slices: as many slices at a time as there are threads,
+    // then the partial sums, in a fixed order
+    if (r > 0) {
+      const int mr = M * r, rp = (r + 31) & ~31;
+      const int par = mr <= kThreads ? kThreads / mr : 1;
+      for (int i = t; i < (par > 1 ? par * mr : mr); i += kThreads) {
+        const int e = i % mr, q0 = i / mr;
+        float s = 0.0f;
+#pragma unroll 8
+        for (int q = q0; q < slices; q += par) s += part[static_cast<int64_t>(q) * mr + e];
+        s_u[i] = s;
+      }
+      __syncthreads();
+      for (int i = t; i < 16 * rp; i += kThreads) {
+        const int row = i / rp, j = i % rp;
+        float s = 0.0f;
+        if (row < M && j < r) {
+          for (int q = 0; q < par; ++q) s += s_u[q * mr + row * r + j];
+          if (u_out && blockIdx.x == 0)
+            u_out[row * r + j] = static_cast<uint16_t>(pack_bf16x2(s, 0.f) & 0xFFFF);
+        }
+        s_us[i] = static_cast<uint16_t>(pack_bf16x2(s * lora_scale, 0.f) & 0xFFFF);
+      }
+    }
+  }
+
+  f32x4_t acc[kMT];
+#pragma unroll
+  for (int i = 0; i < kMT; ++i) acc[i] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+  for (int64_t b = wave; b < kb; b += (kAhead + 1) * kWaves) {
+#pragma unroll
+    for (int d = 0; d <= kAhead; ++d) {
+      const i32x8_t wf = frag8(blk[d].w.lo, blk[d].w.hi);
+#pragma unroll
+      for (int i = 0; i < kMT; ++i) {
+        const f32x4_t c = mfma_fp8(wf, frag8(blk[d].x[i].lo, blk[d].x[i].hi),
+                                   f32x4_t{0.f, 0.f, 0.f, 0.f});
+        const float s = blk[d].sx[i] * blk[d].sw;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[i][e] = fmaf(c[e], s, acc[i][e]);
+      }
+      load(b + (d + kAhead + 1) * kWaves, blk[d]);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < kMT; ++i) s_acc[wave][i][lane] = acc[i];
+  __syncthreads();
+  if (wave >= kMT) return;
+  f32x4_t sum = s_acc[0][wave][lane];
+#pragma unroll
+  for (int q = 1; q < kWaves; ++q) sum += s_acc[q][wave][lane];
+  const int row = 16 * wave + li;
+  if (r > 0) {
+    if constexpr (kMT == 1)
+      sum = lora_up(sum, bf, s_us, (r + 31) & ~31, r, li, lg);
+    else
+      sum = lora_up(sum, bf, act + static_cast<int64_t>(row < M ? row - li : M - 1 - li) * pitch,
+                    pitch, r, li, lg);
+  }
+  // lane (li, lg): columns n0 + 4 lg .. + 3 of token 16 wave + li
+  if (row < M) store_columns(y + row * N + n0 + 4 * lg, sum);
 }
 
 }  // namespace
 
+bool fp8_token_self_u(const Fp8View& w, int r) {
+  // A is read by every workgroup: past about 40 MB in all (from the caches)
+  // a projection launch of its own costs less
+  return r <= 16 && w.N / 16 * r * w.K * 2 <= (int64_t{40} << 20);
+}
+
+hipError_t launch_fp8_token(const Fp8View& w, const uint16_t* x, const uint16_t* A,
+                            const uint16_t* B, int r, float lora_scale, uint16_t* y,
+                            uint16_t* u_out, hipStream_t st) {
+  const dim3 grid(static_cast<uint32_t>(w.N / 16));
+  const bool vec_a = (reinterpret_cast<uintptr_t>(A) & 15) == 0;
+  const bool vec_b = (r & 7) == 0 && (reinterpret_cast<uintptr_t>(B) & 15) == 0;
+  auto go = [&](auto k) {
+    hipLaunchKernelGGL(k, grid, dim3(1024), 0, st, w.codes, w.scale, w.N, w.K, x, A, vec_a, B, r,
+                       vec_b, lora_scale, y, u_out);
+    return hipGetLastError();
+  };
+  return r == 0 ? go(fp8_token_kernel<0>) : go(fp8_token_kernel<1>);
+}
+
 hipError_t launch_fp8_decode(const Fp8View& w, const uint8_t* x, const float* xs, int M,
-                             const float* part, int slices, const uint16_t* B, int r,
-                             float lora_scale, uint16_t* y, uint16_t* u_out, hipStream_t st) {
+                             const float* part, int slices, const uint16_t* act,
+                             const uint16_t* B, int r, float lora_scale, uint16_t* y,
+                             uint16_t* u_out, hipStream_t st) {
   if (M == 0) return hipSuccess;
   const dim3 grid(static_cast<uint32_t>(w.N / 16));
   const bool vec_b = (r & 7) == 0 && (reinterpret_cast<uintptr_t>(B) & 15) == 0;
   const int64_t kb = (w.K + 127) / 128;
   auto go = [&](auto k, int waves) {
     hipLaunchKernelGGL(k, grid, dim3(64 * waves), 0, st, w.codes, w.scale, w.N, w.K, x, xs, M, part,
-                       slices, B, r, vec_b, lora_scale, y, u_out);
+                       slices, act, fp8_lora_pitch(r), B, r, vec_b, lora_scale, y, u_out);
     return hipGetLastError();
   };
-  return kb <= 8 ? go(fp8_decode_kernel<4>, 4) : go(fp8_decode_kernel<16>, 16);
+  // few columns: all 16 waves on one workgroup per CU; many: smaller
+  // workgroups, so that all of them run at once
+  if (M <= 16)
+    return kb <= 8        ? go(fp8_decode_kernel<4, 1>, 4)
+           : grid.x > 512 ? go(fp8_decode_kernel<8, 1>, 8)
+                          : go(fp8_decode_kernel<16, 1>, 16);
+  // more tokens need the registers of 8 waves
+  if (M <= 32) return kb <= 8 ? go(fp8_decode_kernel<4, 2>, 4) : go(fp8_decode_kernel<8, 2>, 8);
+  return kb <= 8 ? go(fp8_decode_kernel<4, 4>, 4) : go(fp8_decode_kernel<8, 4>, 8);
 }
 
 }  // namespace qn

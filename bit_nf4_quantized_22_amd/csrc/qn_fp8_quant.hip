@@ -6,8 +6,6 @@
 // nearest to fl32(x / s), ties to even.  All three are one pass over the
 // data: a block's values stay in registers between its maximum and its codes.
 
-#include <type_traits>
-
 #include "qn_fp8.h"
 #include "qn_launch.h"
 
@@ -233,6 +231,67 @@ __global__ __launch_bounds__(64 * kWaves) void quantize_project_kernel(
   }
 }
 
+// The same for the decode path (up to 16 tokens, P = A): a wave takes one
+// block, with A's fragments straight in registers, everything asked for at
+// once; the four waves' sums are added in LDS, so that the product's
+// workgroups, which all add up the slices, find a quarter as many.
+template <int kRT>
+__global__ __launch_bounds__(kT) void decode_project_kernel(
+    const uint16_t* __restrict__ x, int M, int64_t L, const uint16_t* __restrict__ A, int r,
+    bool vec_a, uint8_t* __restrict__ codes, float* __restrict__ scale, float* __restrict__ part) {
+  __shared__ f32x4_t s_part[4][kRT][64];
+  const int t = threadIdx.x, lane = t & 63, li = lane & 15, lg = lane >> 4, wave = t >> 6;
+  const int64_t b = static_cast<int64_t>(blockIdx.x) * 4 + wave;
+  const int m = li < M ? li : M - 1;
+  uint4 w[4], a[kRT][4];
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    const int64_t k = b * 128 + 32 * c + 8 * lg;
+    w[c] = k < L ? *reinterpret_cast<const uint4*>(x + m * L + k) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+    for (int i = 0; i < kRT; ++i) {
+      const int j = 16 * i + li;
+      a[i][c] = load_bf16x8(A + j * L + k, j < r && k < L ? 8 : 0, vec_a);
+    }
+  }
+  float v[4][8], am = 0.0f;
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    bf16x8_to_f32(w[c], v[c]);
+    am = fmaxf(am, absmax8(v[c]));
+  }
+  am = fmaxf(am, __shfl_xor(am, 16, 64));
+  am = fmaxf(am, __shfl_xor(am, 32, 64));
+  const float s = fp8_scale(am), inv = __fdiv_rn(1.0f, s);
+  if (li < M && b * 128 < L) {
+    if (lg == 0) scale[b * M + li] = s;
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      const int64_t k = b * 128 + 32 * c + 8 * lg;
+      if (k < L) *reinterpret_cast<uint2*>(codes + li * L + k) = fp8_codes8(v[c], s, inv);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < kRT; ++i) {
+    f32x4_t acc = f32x4_t{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int c = 0; c < 4; ++c) acc = mfma_bf16_32(a[i][c], w[c], acc);
+    s_part[wave][i][lane] = acc;
+  }
+  __syncthreads();
+  // lane (li, lg): ranks 16 i + 4 lg .. + 3 of token li; wave i's tiles
+  for (int i = wave; i < kRT; i += 4) {
+    const f32x4_t u = s_part[0][i][lane] + s_part[1][i][lane] + s_part[2][i][lane] +
+                      s_part[3][i][lane];
+    float* out = part + (static_cast<int64_t>(blockIdx.x) * M + li) * r;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int j = 16 * i + 4 * lg + e;
+      if (li < M && j < r) out[j] = u[e];
+    }
+  }
+}
+
 // The LoRA term's token side for the tile kernel: act[M][ld] = bf16(scale u),
 // u the slices' sum in slice order, rows zero-padded to ld = 64 or 128 values
 // so that a row is one or two 128-byte runs, like the codes of a block; bf16(u)
@@ -264,6 +323,22 @@ __global__ __launch_bounds__(kT) void project_sum_kernel(const float* __restrict
     }
   }
   *reinterpret_cast<uint32_t*>(act + i) = pack_bf16x2(s[0] * scale, s[1] * scale);
+}
+
+// out = bf16 of the sum of `splits` fp32 parts [splits][n], in their order; 8
+// values per thread (n is a multiple of 16).
+__global__ __launch_bounds__(kT) void split_sum_kernel(const float* __restrict__ part, int splits,
+                                                       int64_t n, uint16_t* __restrict__ out) {
+  const int64_t i = (static_cast<int64_t>(blockIdx.x) * kT + threadIdx.x) * 8;
+  if (i >= n) return;
+  f32x4_t a = f32x4_t{0.f, 0.f, 0.f, 0.f}, b = a;
+#pragma unroll 4
+  for (int q = 0; q < splits; ++q) {
+    a += *reinterpret_cast<const f32x4_t*>(part + q * n + i);
+    b += *reinterpret_cast<const f32x4_t*>(part + q * n + i + 4);
+  }
+  *reinterpret_cast<uint4*>(out + i) = make_uint4(pack_bf16x2(a[0], a[1]), pack_bf16x2(a[2], a[3]),
+                                                  pack_bf16x2(b[0], b[1]), pack_bf16x2(b[2], b[3]));
 }
 
 // 16 codes per thread.
@@ -344,7 +419,7 @@ hipError_t launch_fp8_quantize_project(const uint16_t* x, int64_t M, int64_t L, 
                                        int r, bool rows_l, uint8_t* codes, float* scale,
                                        float* part, hipStream_t st) {
   if (M == 0) return hipSuccess;
-  const int waves = M > 16 ? 4 : 1;
+  const int waves = rows_l && M <= 16 ? 1 : 4;
   const dim3 grid(static_cast<uint32_t>((M + 16 * waves - 1) / (16 * waves)),
                   static_cast<uint32_t>(fp8_project_slices(M, L)));
   // rows of P can be read 16 bytes at a time (a row of A has L values, a
@@ -356,19 +431,36 @@ hipError_t launch_fp8_quantize_project(const uint16_t* x, int64_t M, int64_t L, 
                        part);
     return hipGetLastError();
   };
-  auto by_rank = [&](auto rows, auto w) {
-    constexpr bool kR = decltype(rows)::value;
-    constexpr int kW = decltype(w)::value;
-    return r <= 16   ? go(quantize_project_kernel<kR, 1, kW>)
-           : r <= 32 ? go(quantize_project_kernel<kR, 2, kW>)
-           : r <= 64 ? go(quantize_project_kernel<kR, 4, kW>)
-                     : go(quantize_project_kernel<kR, 8, kW>);
+  if (!rows_l)
+    return r <= 16   ? go(quantize_project_kernel<false, 1, 4>)
+           : r <= 32 ? go(quantize_project_kernel<false, 2, 4>)
+           : r <= 64 ? go(quantize_project_kernel<false, 4, 4>)
+                     : go(quantize_project_kernel<false, 8, 4>);
+  if (waves == 1)
+    return r <= 16   ? go(quantize_project_kernel<true, 1, 1>)
+           : r <= 32 ? go(quantize_project_kernel<true, 2, 1>)
+           : r <= 64 ? go(quantize_project_kernel<true, 4, 1>)
+                     : go(quantize_project_kernel<true, 8, 1>);
+  return r <= 16   ? go(quantize_project_kernel<true, 1, 4>)
+         : r <= 32 ? go(quantize_project_kernel<true, 2, 4>)
+         : r <= 64 ? go(quantize_project_kernel<true, 4, 4>)
+                   : go(quantize_project_kernel<true, 8, 4>);
+}
+
+int fp8_decode_slices(int64_t L) { return static_cast<int>(((L + 127) / 128 + 3) / 4); }
+
+hipError_t launch_fp8_decode_project(const uint16_t* x, int M, int64_t L, const uint16_t* A, int r,
+                                     uint8_t* codes, float* scale, float* part, hipStream_t st) {
+  const dim3 grid(static_cast<uint32_t>(fp8_decode_slices(L)));
+  const bool vec_a = (reinterpret_cast<uintptr_t>(A) & 15) == 0;
+  auto go = [&](auto k) {
+    hipLaunchKernelGGL(k, grid, dim3(kT), 0, st, x, M, L, A, r, vec_a, codes, scale, part);
+    return hipGetLastError();
   };
-  using One = std::integral_constant<int, 1>;
-  using Four = std::integral_constant<int, 4>;
-  if (rows_l)
-    return waves == 1 ? by_rank(std::true_type{}, One{}) : by_rank(std::true_type{}, Four{});
-  return waves == 1 ? by_rank(std::false_type{}, One{}) : by_rank(std::false_type{}, Four{});
+  return r <= 16   ? go(decode_project_kernel<1>)
+         : r <= 32 ? go(decode_project_kernel<2>)
+         : r <= 64 ? go(decode_project_kernel<4>)
+                   : go(decode_project_kernel<8>);
 }
 
 hipError_t launch_fp8_project_sum(const float* part, int slices, int64_t M, int r, float scale,
@@ -378,6 +470,14 @@ hipError_t launch_fp8_project_sum(const float* part, int slices, int64_t M, int 
   const int64_t threads = M * ld / 2;
   hipLaunchKernelGGL(project_sum_kernel, dim3(static_cast<uint32_t>((threads + kT - 1) / kT)),
                      dim3(kT), 0, st, part, slices, M, r, ld, scale, act, plain);
+  return hipGetLastError();
+}
+
+hipError_t launch_fp8_split_sum(const float* part, int splits, int64_t n, uint16_t* out,
+                                hipStream_t st) {
+  const int64_t threads = n / 8;
+  hipLaunchKernelGGL(split_sum_kernel, dim3(static_cast<uint32_t>((threads + kT - 1) / kT)),
+                     dim3(kT), 0, st, part, splits, n, out);
   return hipGetLastError();
 }
 

@@ -146,12 +146,28 @@ int fp8_project_slices(int64_t M, int64_t L);
 hipError_t launch_fp8_quantize_project(const uint16_t* x, int64_t M, int64_t L, const uint16_t* P,
                                        int r, bool rows_l, uint8_t* codes, float* scale,
                                        float* part, hipStream_t st);
-// y [M, N] for M <= kFp8DecodeM tokens: x W^T + (lora_scale u) B^T, u given
-// as slices partial sums [slices][M][r]; bf16(u) to u_out if not null.
-constexpr int kFp8DecodeM = 16;
+// y [M, N] = x W^T + (lora_scale u) B^T for M <= kFp8FewM tokens, u given as
+// slices partial sums [slices][M][r] (M <= kFp8DecodeM; bf16(u) to u_out if
+// not null) or as act (see launch_fp8_project_sum).
+constexpr int kFp8DecodeM = 16, kFp8FewM = 64;
 hipError_t launch_fp8_decode(const Fp8View& w, const uint8_t* x, const float* xs, int M,
-                             const float* part, int slices, const uint16_t* B, int r,
-                             float lora_scale, uint16_t* y, uint16_t* u_out, hipStream_t st);
+                             const float* part, int slices, const uint16_t* act,
+                             const uint16_t* B, int r, float lora_scale, uint16_t* y,
+                             uint16_t* u_out, hipStream_t st);
+// launch_fp8_quantize_project of M <= kFp8DecodeM tokens with P = A, into
+// fp8_decode_slices(L) slices.
+int fp8_decode_slices(int64_t L);
+hipError_t launch_fp8_decode_project(const uint16_t* x, int M, int64_t L, const uint16_t* A, int r,
+                                     uint8_t* codes, float* scale, float* part, hipStream_t st);
+// One token in one launch: x quantised and u = x A^T computed by the product's
+// workgroups; for r == 0 or where fp8_token_self_u holds.
+bool fp8_token_self_u(const Fp8View& w, int r);
+hipError_t launch_fp8_token(const Fp8View& w, const uint16_t* x, const uint16_t* A,
+                            const uint16_t* B, int r, float lora_scale, uint16_t* y,
+                            uint16_t* u_out, hipStream_t st);
+// out = bf16(sum of `splits` fp32 parts of n values).
+hipError_t launch_fp8_split_sum(const float* part, int splits, int64_t n, uint16_t* out,
+                                hipStream_t st);
 hipError_t launch_fp8_dequant(const Fp8View& w, bool out_bf16, void* out, hipStream_t st);
 // The LoRA term's token side for launch_fp8_gemm: act[M], rows of
 // fp8_lora_pitch(r) = 64 or 128 bf16 values padded with zeros, = scale * the
@@ -162,10 +178,13 @@ hipError_t launch_fp8_project_sum(const float* part, int slices, int64_t M, int 
                                   uint16_t* act, uint16_t* plain, hipStream_t st);
 // out = x W^T + act lw^T (x [M, K], lw = B [N, r]), or with bwd
 // out = x W + act lw (x [M, N], lw = A [r, K]); x in codes with row scales
-// (r == 0: no LoRA term).
+// (r == 0: no LoRA term).  The contraction (L) is split over
+// fp8_gemm_splits(M, ncols, L) workgroups where the tiles are few and part,
+// fp32 [splits][M][ncols], is given.
+int fp8_gemm_splits(int64_t M, int64_t ncols, int64_t L);
 hipError_t launch_fp8_gemm(const Fp8View& w, const uint8_t* x, const float* xs, int64_t M,
                            const uint16_t* act, const uint16_t* lw, int r, bool bwd, uint16_t* out,
-                           hipStream_t st);
+                           float* part, hipStream_t st);
 
 // LoRA merge: out[N, K] = bf16(dequant(W) + s B A) (A [r, K], B [N, r]).
 hipError_t launch_merge(const WeightView& w, const uint16_t* A, const uint16_t* B, int r, float s,

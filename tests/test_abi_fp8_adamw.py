@@ -44,21 +44,27 @@ def test_fp8_weight_checks(lib):  # noqa: F811
            (fp8_w(N=(1 << 23) + 16), qn.QN_ERR_SHAPE), (None, qn.QN_ERR_NULL)]
     for w, status in bad:
         assert lib.fp8_dequant(w, qn.QN_F32, FAKE, None) == status
-        assert lib.fp8_matmul(w, FAKE, FAKE, 1, 0, FAKE, None) == status
+        assert lib.fp8_matmul(w, FAKE, FAKE, 1, 0, FAKE, FAKE, need, None) == status
         for f in (lib.fp8_linear_fwd, lib.fp8_linear_bwd_dx):
             assert f(w, FAKE, 32, FAKE, FAKE, 8, 16.0, FAKE, None, FAKE, need, None) == status
 
 
 def test_fp8_product_argument_errors(lib):  # noqa: F811
-    f = lib.fp8_matmul
-    assert f(fp8_w(), FAKE, FAKE, 1, 2, FAKE, None) == qn.QN_ERR_UNSUPPORTED
-    assert f(fp8_w(), FAKE, FAKE, -1, 0, FAKE, None) == qn.QN_ERR_SHAPE
-    assert f(fp8_w(), FAKE, FAKE, BIG, 0, FAKE, None) == qn.QN_ERR_SHAPE
-    assert f(fp8_w(), None, None, 0, 0, None, None) == qn.QN_OK
-    for a in ((None, FAKE, FAKE), (FAKE, None, FAKE), (FAKE, FAKE, None)):
-        assert f(fp8_w(), a[0], a[1], 1, 1, a[2], None) == qn.QN_ERR_NULL
-    for a in ((ODD, FAKE, FAKE), (FAKE, ODD, FAKE), (FAKE, FAKE, ODD)):
-        assert f(fp8_w(), a[0], a[1], 1, 1, a[2], None) == qn.QN_ERR_ALIGN
+    need = qn.qn_workspace_bytes(qn.QN_OP_FP8_BWD_DX, 80, 128, 128, 0)
+
+    def f(x=FAKE, s=FAKE, M=80, tr=1, out=FAKE, ws=FAKE, n=need):
+        return lib.fp8_matmul(fp8_w(), x, s, M, tr, out, ws, n, None)
+
+    assert f(tr=2) == qn.QN_ERR_UNSUPPORTED
+    assert f(M=-1) == qn.QN_ERR_SHAPE
+    assert f(M=BIG) == qn.QN_ERR_SHAPE
+    assert f(x=None, s=None, M=0, out=None, ws=None, n=0) == qn.QN_OK
+    for k in ("x", "s", "out"):
+        assert f(**{k: None}) == qn.QN_ERR_NULL
+    for k in ("x", "s", "out", "ws"):
+        assert f(**{k: ODD}) == qn.QN_ERR_ALIGN
+    assert f(ws=None) == qn.QN_ERR_WORKSPACE
+    assert f(n=need - 1) == qn.QN_ERR_WORKSPACE
     assert lib.fp8_dequant(fp8_w(), 2, FAKE, None) == qn.QN_ERR_UNSUPPORTED
     assert lib.fp8_dequant(fp8_w(), qn.QN_F32, None, None) == qn.QN_ERR_NULL
     assert lib.fp8_dequant(fp8_w(), qn.QN_F32, ODD, None) == qn.QN_ERR_ALIGN

@@ -145,7 +145,13 @@ def test_borders_between_codes_and_the_ends_of_the_range():
 LAYERS = [(1, 16, 16, 0), (1, 144, 272, 16), (3, 128, 1040, 5), (16, 272, 2112, 64),
           (17, 16, 16, 1), (17, 144, 272, 16), (64, 128, 128, 0), (65, 1088, 2112, 64),
           (127, 272, 144, 128), (300, 784, 656, 24), (129, 2064, 48, 33), (1, 4096, 4096, 16),
-          (9, 1024, 11008, 16)]
+          (9, 1024, 11008, 16),
+          # one token: in one launch with A (r <= 16) and without, at the
+          # border of its rule, and in two; the largest of each decode size
+          (1, 272, 4112, 3), (1, 1040, 528, 0), (1, 528, 1040, 17), (1, 144, 208, 128),
+          (2, 9216, 512, 16), (32, 144, 1296, 16), (33, 144, 400, 24), (64, 272, 1296, 64),
+          # contractions split over workgroups, with and without a tail
+          (65, 160, 1024, 16), (66, 400, 2064, 0), (5, 2064, 400, 8), (200, 1040, 1552, 40)]
 
 
 @pytest.mark.parametrize("M,N,K,r", LAYERS)
@@ -189,10 +195,14 @@ def test_linear_layer_against_the_oracle(M, N, K, r):
     assert rel_to_bound(to_np(dx[:M]), ref_dx, bd) <= 1
     check(f"fp8 y {M}x{N}x{K} r={r}", to_np(y[:M]), ref_y)
     check(f"fp8 dx {M}x{N}x{K} r={r}", to_np(dx[:M]), ref_dx)
-    # the product of given rows is the layer without an adapter
+    # the product of given rows is the layer without an adapter: the same
+    # bits, but for one token, whose one launch adds the blocks in another order
     if r == 0:
         c, sc = qn.fp8_quantize_rows(x)
-        assert torch.equal(qn.fp8_matmul(fw, c, sc).view(torch.int16), y[:M].view(torch.int16))
+        got = qn.fp8_matmul(fw, c, sc)
+        assert rel_to_bound(to_np(got), ref_y, by) <= 1
+        if M > 1:
+            assert torch.equal(got.view(torch.int16), y[:M].view(torch.int16))
         c, sc = qn.fp8_quantize_rows(dy)
         got = qn.fp8_matmul(fw, c, sc, transposed=True)
         assert torch.equal(got.view(torch.int16), dx[:M].view(torch.int16))
