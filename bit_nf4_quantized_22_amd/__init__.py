@@ -68,8 +68,7 @@ class qn_adamw_tensor(ctypes.Structure):
 
 class qn_adamw_plan(ctypes.Structure):
     _fields_ = [("chunks", ctypes.c_int64), ("bytes", ctypes.c_int64),
-                ("tensors", ctypes.c_int32), ("grad_dtype", ctypes.c_int32),
-                ("state", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+                ("grad_dtype", ctypes.c_int32), ("state", ctypes.c_int32)]
 
 
 _lib = None

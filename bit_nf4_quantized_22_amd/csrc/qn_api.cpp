@@ -350,24 +350,20 @@ bool adamw_hyper_ok(float lr, float beta1, float beta2, float eps, float weight_
          eps > 0.0f && weight_decay >= 0.0f;
 }
 
-// Chunks of the matrices of an AdamW table, -1 for sizes out of range;
-// `used` counts the matrices that have elements.
-int64_t adamw_chunks(const qn_adamw_tensor* t, int32_t count, int32_t& used) {
+// Chunks of the matrices of an AdamW table, -1 for sizes out of range.
+int64_t adamw_chunks(const qn_adamw_tensor* t, int32_t count) {
   int64_t chunks = 0;
-  used = 0;
   for (int32_t i = 0; i < count; ++i) {
     if (t[i].n < 0) return -1;
     if (t[i].n == 0) continue;
-    ++used;
     chunks += (t[i].n - 1) / qn::kAdamChunk + 1;
     if (chunks > INT32_MAX) return -1;
   }
   return chunks;
 }
 
-size_t adamw_table_size(int32_t used, int64_t chunks) {
-  return static_cast<size_t>(used) * sizeof(qn::AdamTensor) +
-         static_cast<size_t>(chunks) * sizeof(uint2);
+size_t adamw_table_size(int64_t chunks) {
+  return static_cast<size_t>(chunks) * sizeof(qn::AdamChunk);
 }
 
 // Whether memory that a step writes overlaps anything else of the table.
@@ -412,20 +408,16 @@ int check_adamw_plan(const qn_adamw_plan* plan, const void* table) {
   if ((plan->grad_dtype != QN_F32 && plan->grad_dtype != QN_BF16) ||
       (plan->state != QN_STATE_F32 && plan->state != QN_STATE_8BIT))
     return QN_ERR_UNSUPPORTED;
-  if (plan->tensors < 0 || plan->chunks < plan->tensors || plan->chunks > INT32_MAX ||
-      plan->bytes != static_cast<int64_t>(adamw_table_size(plan->tensors, plan->chunks)))
+  if (plan->chunks < 0 || plan->chunks > INT32_MAX ||
+      plan->bytes != static_cast<int64_t>(adamw_table_size(plan->chunks)))
     return QN_ERR_SHAPE;
   if (plan->chunks > 0 && !table) return QN_ERR_NULL;
   if (!aligned(table, 16)) return QN_ERR_ALIGN;
   return QN_OK;
 }
 
-const qn::AdamTensor* adamw_tensors(const void* table) {
-  return static_cast<const qn::AdamTensor*>(table);
-}
-
-const uint2* adamw_map(const qn_adamw_plan* plan, const void* table) {
-  return reinterpret_cast<const uint2*>(adamw_tensors(table) + plan->tensors);
+const qn::AdamChunk* adamw_table(const void* table) {
+  return static_cast<const qn::AdamChunk*>(table);
 }
 
 }  // namespace
@@ -727,9 +719,8 @@ int fp8_linear_bwd_dx(const qn_fp8_weight* w, const qn_bf16* dy, int64_t M, cons
 
 size_t lora_adamw_table_bytes(const qn_adamw_tensor* t, int32_t count) {
   if (!t || count < 0) return 0;
-  int32_t used = 0;
-  const int64_t chunks = adamw_chunks(t, count, used);
-  return chunks < 0 ? 0 : adamw_table_size(used, chunks);
+  const int64_t chunks = adamw_chunks(t, count);
+  return chunks < 0 ? 0 : adamw_table_size(chunks);
 }
 
 int lora_adamw_table(const qn_adamw_tensor* t, int32_t count, int32_t grad_dtype, int32_t state,
@@ -739,8 +730,7 @@ int lora_adamw_table(const qn_adamw_tensor* t, int32_t count, int32_t grad_dtype
       (state != QN_STATE_F32 && state != QN_STATE_8BIT))
     return QN_ERR_UNSUPPORTED;
   if (count < 0) return QN_ERR_SHAPE;
-  int32_t used = 0;
-  const int64_t chunks = adamw_chunks(t, count, used);
+  const int64_t chunks = adamw_chunks(t, count);
   if (chunks < 0) return QN_ERR_SHAPE;
   const bool state8 = state == QN_STATE_8BIT;
   for (int32_t i = 0; i < count; ++i) {
@@ -753,7 +743,7 @@ int lora_adamw_table(const qn_adamw_tensor* t, int32_t count, int32_t grad_dtype
         (state8 && (!aligned(a.m_scale, 4) || !aligned(a.v_scale, 4))))
       return QN_ERR_ALIGN;
   }
-  const size_t need = adamw_table_size(used, chunks);
+  const size_t need = adamw_table_size(chunks);
   if (need > 0 && (!table || bytes < need)) return QN_ERR_WORKSPACE;
   if (!aligned(table, 8)) return QN_ERR_ALIGN;
   try {
@@ -761,18 +751,21 @@ int lora_adamw_table(const qn_adamw_tensor* t, int32_t count, int32_t grad_dtype
   } catch (...) {  // no host memory for the ranges
     return QN_ERR_WORKSPACE;
   }
-  *plan = qn_adamw_plan{chunks, static_cast<int64_t>(need), used, grad_dtype, state, 0};
-  qn::AdamTensor* d = static_cast<qn::AdamTensor*>(table);
-  uint2* map = reinterpret_cast<uint2*>(d + used);
-  uint32_t k = 0;
+  *plan = qn_adamw_plan{chunks, static_cast<int64_t>(need), grad_dtype, state};
+  qn::AdamChunk* d = static_cast<qn::AdamChunk*>(table);
   for (int32_t i = 0; i < count; ++i) {
     const qn_adamw_tensor& a = t[i];
-    if (a.n == 0) continue;
-    d[k] = qn::AdamTensor{a.p, a.g, a.m, a.v, state8 ? a.m_scale : nullptr,
-                          state8 ? a.v_scale : nullptr, a.p_bf16, a.n};
-    const int64_t c = (a.n - 1) / qn::kAdamChunk + 1;
-    for (int64_t j = 0; j < c; ++j) *map++ = uint2{k, static_cast<uint32_t>(j)};
-    ++k;
+    for (int64_t e = 0; e < a.n; e += qn::kAdamChunk) {
+      const int64_t blk = e / qn::kAdamStateBlock, state = state8 ? e : e * 4;
+      *d++ = qn::AdamChunk{a.p + e,
+                           static_cast<const char*>(a.g) + e * (grad_dtype == QN_BF16 ? 2 : 4),
+                           static_cast<char*>(a.m) + state,
+                           static_cast<char*>(a.v) + state,
+                           state8 ? a.m_scale + blk : nullptr,
+                           state8 ? a.v_scale + blk : nullptr,
+                           a.p_bf16 ? a.p_bf16 + e : nullptr,
+                           std::min<int64_t>(a.n - e, qn::kAdamChunk)};
+    }
   }
   return QN_OK;
 }
@@ -792,8 +785,8 @@ int lora_grad_norm(const qn_adamw_plan* plan, const void* table, float max_norm,
   if (need > 0 && (!ws || ws_bytes < need)) return QN_ERR_WORKSPACE;
   if (!aligned(ws, 8)) return QN_ERR_ALIGN;
   (void)hipGetLastError();
-  return hip_status(qn::launch_grad_norm(adamw_tensors(table), adamw_map(plan, table),
-                                         plan->chunks, plan->grad_dtype == QN_BF16, max_norm,
+  return hip_status(qn::launch_grad_norm(adamw_table(table), plan->chunks,
+                                         plan->grad_dtype == QN_BF16, max_norm,
                                          static_cast<double*>(ws), out, as_stream(stream)));
 }
 
@@ -805,7 +798,7 @@ int lora_adamw_multi_step(const qn_adamw_plan* plan, const void* table, const fl
   if (step < 1 || !adamw_hyper_ok(lr, beta1, beta2, eps, weight_decay)) return QN_ERR_SHAPE;
   (void)hipGetLastError();
   return hip_status(qn::launch_adamw_multi(
-      adamw_tensors(table), adamw_map(plan, table), plan->chunks, plan->state == QN_STATE_8BIT,
+      adamw_table(table), plan->chunks, plan->state == QN_STATE_8BIT,
       plan->grad_dtype == QN_BF16, grad_scale, lr, beta1, beta2, eps, weight_decay, step,
       as_stream(stream)));
 }

@@ -196,9 +196,9 @@ hipError_t launch_adamw(float* p, const float* g, float* m, float* v, uint16_t* 
                         hipStream_t st);
 
 // AdamW over many matrices (see lora_adamw_multi_step in the C ABI): the
-// device table is the descriptors, then the chunk map: entry b names the
-// descriptor and the chunk of kAdamChunk elements that workgroup b takes.
-struct AdamTensor {
+// device table holds one entry per workgroup, a chunk of up to kAdamChunk
+// elements of one matrix with the addresses of its first element.
+struct AdamChunk {
   float* p;
   const void* g;  // fp32 or bf16
   void* m;        // fp32, or E4M3 codes
@@ -212,14 +212,13 @@ constexpr int kAdamChunk = 2048;
 constexpr int kAdamStateBlock = 256;  // elements per scale of the 8-bit states
 constexpr int kGradNormBlocks = 2048;  // most partial sums of the gradient norm
 int grad_norm_blocks(int64_t chunks);
-hipError_t launch_adamw_multi(const AdamTensor* tab, const uint2* map, int64_t chunks, bool state8,
-                              bool bf16_grad, const float* grad_scale, float lr, float beta1,
-                              float beta2, float eps, float weight_decay, int step,
-                              hipStream_t st);
+hipError_t launch_adamw_multi(const AdamChunk* tab, int64_t chunks, bool state8, bool bf16_grad,
+                              const float* grad_scale, float lr, float beta1, float beta2,
+                              float eps, float weight_decay, int step, hipStream_t st);
 // part: grad_norm_blocks(chunks) doubles; out[0] = norm, out[1] = clip
 // coefficient.
-hipError_t launch_grad_norm(const AdamTensor* tab, const uint2* map, int64_t chunks, bool bf16_grad,
-                            float max_norm, double* part, float* out, hipStream_t st);
+hipError_t launch_grad_norm(const AdamChunk* tab, int64_t chunks, bool bf16_grad, float max_norm,
+                            double* part, float* out, hipStream_t st);
 
 // LoRA dropout on the adapter branch (see lora_dropout in the C ABI):
 // threshold = floor(p 2^32) on the 32-bit Philox halves, inv_keep =

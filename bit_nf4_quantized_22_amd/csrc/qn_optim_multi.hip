@@ -4,8 +4,9 @@
 // [rkmt "QLORA技术解析" §3.5], [czcl "QLoRA技術解析" §3.2]: the adapter is
 // trained with AdamW, its states in 32 or 8 bits.  A 7B model has 448 LoRA
 // matrices of 64 K - 176 K elements, so one call per matrix is launch-bound;
-// here a workgroup takes one chunk of 2048 elements of one matrix, found in
-// a table of descriptors and a chunk map that the caller keeps on the device.
+// here a workgroup takes one chunk of 2048 elements of one matrix, whose
+// addresses it finds in one 64-byte entry of a table that the caller keeps on
+// the device.
 //
 // Per element, fp32, each operation rounded on its own (no fused
 // multiply-add, so that the 8-bit codes are a pure function of the inputs):
@@ -89,21 +90,19 @@ __device__ __forceinline__ float state_scale(float most, float top) {
 
 template <bool kState8, bool kBf16Grad>
 __global__ __launch_bounds__(kThreads) void adamw_multi_kernel(
-    const AdamTensor* __restrict__ tab, const uint2* __restrict__ map,
-    const float* __restrict__ grad_scale, MultiArgs a) {
+    const AdamChunk* __restrict__ tab, const float* __restrict__ grad_scale, MultiArgs a) {
 #pragma clang fp contract(off)
-  const uint2 at = map[blockIdx.x];
-  const AdamTensor d = tab[at.x];
+  const AdamChunk d = tab[blockIdx.x];
   float c = 1.0f;
   if (grad_scale) {
     c = *grad_scale;
     if (!(fabsf(c) < __builtin_inff())) return;  // norm not finite: no step
   }
-  const int64_t e0 = static_cast<int64_t>(at.y) * kAdamChunk + threadIdx.x * kPer;
-  const int left = d.n - e0 >= kPer ? kPer : d.n > e0 ? static_cast<int>(d.n - e0) : 0;
+  const int e0 = threadIdx.x * kPer, n = static_cast<int>(d.n);
+  const int left = n - e0 >= kPer ? kPer : n > e0 ? n - e0 : 0;
   float p[kPer], g[kPer], m[kPer], v[kPer];
   uint32_t m8[2] = {0, 0}, v8[2] = {0, 0};
-  const int64_t blk = e0 / kAdamStateBlock;
+  const int blk = e0 / kAdamStateBlock;
   float ms = 0.0f, vs = 0.0f;
   if (left == kPer) {
     const f4_t p0 = *reinterpret_cast<const f4_t*>(d.p + e0);
@@ -264,39 +263,47 @@ __device__ __forceinline__ double block_sum64(double x) {
 // reads of g need, and no gradient's square overflows): workgroup b takes
 // chunks b, b + gridDim.x, ..., a fixed order.
 template <bool kBf16Grad>
-__global__ __launch_bounds__(kThreads) void grad_sq_kernel(const AdamTensor* __restrict__ tab,
-                                                           const uint2* __restrict__ map,
+__global__ __launch_bounds__(kThreads) void grad_sq_kernel(const AdamChunk* __restrict__ tab,
                                                            int64_t chunks,
                                                            double* __restrict__ part) {
+  constexpr int kAhead = 4;  // chunks in flight
+  const int e0 = threadIdx.x * kPer;
   double s = 0.0;
-  for (int64_t q = blockIdx.x; q < chunks; q += gridDim.x) {
-    const uint2 at = map[q];
-    const void* gp = tab[at.x].g;
-    const int64_t n = tab[at.x].n;
-    const int64_t e0 = static_cast<int64_t>(at.y) * kAdamChunk + threadIdx.x * kPer;
-    float g[kPer];
-    if (e0 + kPer <= n) {
-      if constexpr (kBf16Grad) {
-        const u4_t w = *reinterpret_cast<const u4_t*>(static_cast<const uint16_t*>(gp) + e0);
+  for (int64_t q = blockIdx.x; q < chunks; q += kAhead * static_cast<int64_t>(gridDim.x)) {
+    float g[kAhead][kPer];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) g[2 * j] = bf16_lo(w[j]), g[2 * j + 1] = bf16_hi(w[j]);
+    for (int k = 0; k < kAhead; ++k) {
+      const int64_t c = q + k * static_cast<int64_t>(gridDim.x);
+      const void* gp = tab[c < chunks ? c : q].g;
+      const int n = c < chunks ? static_cast<int>(tab[c].n) : 0;
+      if (e0 + kPer <= n) {
+        if constexpr (kBf16Grad) {
+          const u4_t w = *reinterpret_cast<const u4_t*>(static_cast<const uint16_t*>(gp) + e0);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) g[k][2 * j] = bf16_lo(w[j]), g[k][2 * j + 1] = bf16_hi(w[j]);
+        } else {
+          const f4_t g0 = *reinterpret_cast<const f4_t*>(static_cast<const float*>(gp) + e0);
+          const f4_t g1 = *reinterpret_cast<const f4_t*>(static_cast<const float*>(gp) + e0 + 4);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) g[k][j] = g0[j], g[k][4 + j] = g1[j];
+        }
       } else {
-        const f4_t g0 = *reinterpret_cast<const f4_t*>(static_cast<const float*>(gp) + e0);
-        const f4_t g1 = *reinterpret_cast<const f4_t*>(static_cast<const float*>(gp) + e0 + 4);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) g[j] = g0[j], g[4 + j] = g1[j];
-      }
-    } else {
-#pragma unroll
-      for (int j = 0; j < kPer; ++j) {
-        if constexpr (kBf16Grad)
-          g[j] = e0 + j < n ? bf16_to_f32(static_cast<const uint16_t*>(gp)[e0 + j]) : 0.0f;
-        else
-          g[j] = e0 + j < n ? static_cast<const float*>(gp)[e0 + j] : 0.0f;
+        for (int j = 0; j < kPer; ++j) {
+          if constexpr (kBf16Grad)
+            g[k][j] = e0 + j < n ? bf16_to_f32(static_cast<const uint16_t*>(gp)[e0 + j]) : 0.0f;
+          else
+            g[k][j] = e0 + j < n ? static_cast<const float*>(gp)[e0 + j] : 0.0f;
+        }
       }
     }
 #pragma unroll
-    for (int j = 0; j < kPer; ++j) s = fma(static_cast<double>(g[j]), static_cast<double>(g[j]), s);
+    for (int k = 0; k < kAhead; ++k)
+#pragma unroll
+      for (int j = 0; j < kPer; ++j) {
+        const double v = static_cast<double>(g[k][j]);
+        s = fma(v, v, s);
+      }
   }
   const double t = block_sum64<kThreads / 64>(s);
   if (threadIdx.x == 0) part[blockIdx.x] = t;
@@ -325,10 +332,9 @@ int grad_norm_blocks(int64_t chunks) {
   return static_cast<int>(chunks < kGradNormBlocks ? chunks : kGradNormBlocks);
 }
 
-hipError_t launch_adamw_multi(const AdamTensor* tab, const uint2* map, int64_t chunks, bool state8,
-                              bool bf16_grad, const float* grad_scale, float lr, float beta1,
-                              float beta2, float eps, float weight_decay, int step,
-                              hipStream_t st) {
+hipError_t launch_adamw_multi(const AdamChunk* tab, int64_t chunks, bool state8, bool bf16_grad,
+                              const float* grad_scale, float lr, float beta1, float beta2,
+                              float eps, float weight_decay, int step, hipStream_t st) {
   if (chunks == 0) return hipSuccess;
   MultiArgs a;
   a.beta1 = beta1;
@@ -345,16 +351,16 @@ hipError_t launch_adamw_multi(const AdamTensor* tab, const uint2* map, int64_t c
   const dim3 grid(static_cast<uint32_t>(chunks));
   auto k = state8 ? (bf16_grad ? adamw_multi_kernel<true, true> : adamw_multi_kernel<true, false>)
                   : (bf16_grad ? adamw_multi_kernel<false, true> : adamw_multi_kernel<false, false>);
-  hipLaunchKernelGGL(k, grid, dim3(kThreads), 0, st, tab, map, grad_scale, a);
+  hipLaunchKernelGGL(k, grid, dim3(kThreads), 0, st, tab, grad_scale, a);
   return hipGetLastError();
 }
 
-hipError_t launch_grad_norm(const AdamTensor* tab, const uint2* map, int64_t chunks, bool bf16_grad,
-                            float max_norm, double* part, float* out, hipStream_t st) {
+hipError_t launch_grad_norm(const AdamChunk* tab, int64_t chunks, bool bf16_grad, float max_norm,
+                            double* part, float* out, hipStream_t st) {
   const int blocks = grad_norm_blocks(chunks);
   if (blocks > 0) {
     auto k = bf16_grad ? grad_sq_kernel<true> : grad_sq_kernel<false>;
-    hipLaunchKernelGGL(k, dim3(static_cast<uint32_t>(blocks)), dim3(kThreads), 0, st, tab, map,
+    hipLaunchKernelGGL(k, dim3(static_cast<uint32_t>(blocks)), dim3(kThreads), 0, st, tab,
                        chunks, part);
     if (hipError_t e = hipGetLastError(); e != hipSuccess) return e;
   }

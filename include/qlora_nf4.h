@@ -574,10 +574,8 @@ typedef struct qn_adamw_tensor {
 typedef struct qn_adamw_plan {
   int64_t chunks;      /* workgroups of a step */
   int64_t bytes;       /* bytes of the table */
-  int32_t tensors;     /* matrices with n > 0 */
   int32_t grad_dtype;  /* QN_F32 or QN_BF16 */
   int32_t state;       /* QN_STATE_F32 or QN_STATE_8BIT */
-  int32_t reserved;
 } qn_adamw_plan;
 
 /*
