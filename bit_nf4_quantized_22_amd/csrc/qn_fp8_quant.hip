@@ -295,34 +295,44 @@ __global__ __launch_bounds__(kT) void decode_project_kernel(
 // The LoRA term's token side for the tile kernel: act[M][ld] = bf16(scale u),
 // u the slices' sum in slice order, rows zero-padded to ld = 64 or 128 values
 // so that a row is one or two 128-byte runs, like the codes of a block; bf16(u)
-// also to `plain` [M, r] for the caller.  Two values per thread, whose loads
-// go out without waiting for each other.
+// also to `plain` [M, r] for the caller.  Four values per thread; kSlices
+// loads go out before the first is added.
 __global__ __launch_bounds__(kT) void project_sum_kernel(const float* __restrict__ part, int slices,
                                                          int64_t M, int r, int ld, float scale,
                                                          uint16_t* __restrict__ act,
                                                          uint16_t* __restrict__ plain) {
-  const int64_t i = (static_cast<int64_t>(blockIdx.x) * kT + threadIdx.x) * 2;
+  const int64_t i = (static_cast<int64_t>(blockIdx.x) * kT + threadIdx.x) * 4;
   const int64_t m = i / ld;
   const int j = static_cast<int>(i % ld);
   if (m >= M) return;
-  float s[2] = {0.0f, 0.0f};
-  if (j < r) {
-    const float* p = part + m * r + j;
-    const int two = j + 1 < r ? 1 : 0;
-    const int64_t step = M * r;
-#pragma unroll 8
-    for (int k = 0; k < slices; ++k) {
-      s[0] += p[k * step];
-      s[1] += p[k * step + two];
+  f32x4_t s = f32x4_t{0.f, 0.f, 0.f, 0.f};
+  const int64_t step = M * r;
+  const float* p = part + m * r + j;
+  if (j < r && (r & 3) == 0) {
+    constexpr int kSlices = 16;
+    for (int k0 = 0; k0 < slices; k0 += kSlices) {
+      f32x4_t v[kSlices];
+#pragma unroll
+      for (int k = 0; k < kSlices; ++k)  // past the end: the last one again, not added
+        v[k] = *reinterpret_cast<const f32x4_t*>(p + (k0 + k < slices ? k0 + k : slices - 1) * step);
+#pragma unroll
+      for (int k = 0; k < kSlices; ++k)
+        if (k0 + k < slices) s += v[k];
     }
-    if (!two) s[1] = 0.0f;
-    if (plain) {
-      const uint32_t u = pack_bf16x2(s[0], s[1]);
-      plain[m * r + j] = static_cast<uint16_t>(u & 0xFFFF);
-      if (two) plain[m * r + j + 1] = static_cast<uint16_t>(u >> 16);
-    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (j + e < r)
+        for (int k = 0; k < slices; ++k) s[e] += p[k * step + e];
   }
-  *reinterpret_cast<uint32_t*>(act + i) = pack_bf16x2(s[0] * scale, s[1] * scale);
+  *reinterpret_cast<uint2*>(act + i) = make_uint2(pack_bf16x2(s[0] * scale, s[1] * scale),
+                                                  pack_bf16x2(s[2] * scale, s[3] * scale));
+  if (plain) {
+    const uint32_t u[2] = {pack_bf16x2(s[0], s[1]), pack_bf16x2(s[2], s[3])};
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (j + e < r) plain[m * r + j + e] = static_cast<uint16_t>(u[e >> 1] >> (16 * (e & 1)));
+  }
 }
 
 // out = bf16 of the sum of `splits` fp32 parts [splits][n], in their order; 8
@@ -467,7 +477,7 @@ hipError_t launch_fp8_project_sum(const float* part, int slices, int64_t M, int 
                                   uint16_t* act, uint16_t* plain, hipStream_t st) {
   if (M == 0 || r == 0) return hipSuccess;
   const int ld = fp8_lora_pitch(r);
-  const int64_t threads = M * ld / 2;
+  const int64_t threads = M * ld / 4;
   hipLaunchKernelGGL(project_sum_kernel, dim3(static_cast<uint32_t>((threads + kT - 1) / kT)),
                      dim3(kT), 0, st, part, slices, M, r, ld, scale, act, plain);
   return hipGetLastError();
