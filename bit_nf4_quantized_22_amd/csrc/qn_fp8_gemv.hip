@@ -213,6 +213,21 @@ __global__ __launch_bounds__(64 * kWaves) void fp8_decode_kernel(
       d.sx[i] = in ? xs[b * M + m[i]] : 0.0f;
     }
   };
+  // u = sum of its slices: `par` threads per value, thread (q0, e) takes the
+  // slices q0, q0 + par, ...; the first kEarly of them are asked for before
+  // anything else and added while the weight is on its way, the sums over q0
+  // (in order) follow behind the product.
+  constexpr int kEarly = 8;
+  const int mr = M * r, par = kMT == 1 && r > 0 && mr <= kThreads ? kThreads / mr : 1;
+  float early[kEarly];
+  if (kMT == 1 && r > 0) {
+    const int e = t % mr, q0 = t / mr;
+#pragma unroll
+    for (int k = 0; k < kEarly; ++k) {
+      const int q = q0 + k * par;
+      early[k] = part[static_cast<int64_t>(q < slices ? q : slices - 1) * mr + e];
+    }
+  }
   Block blk[kAhead + 1];
 #pragma unroll
   for (int d = 0; d <= kAhead; ++d) load(wave + d * kWaves, blk[d]);
@@ -225,32 +240,13 @@ __global__ __launch_bounds__(64 * kWaves) void fp8_decode_kernel(
         bf[q] = load_bf16x8(B + (n0 + li) * r + 32 * q + 8 * lg, r - 32 * q - 8 * lg, vec_b);
     }
   }
-
-  if constexpr (kMT == 1) {
-    // u = sum of its slices: as many slices at a time as there are threads,
-    // then the partial sums, in a fixed order
-    if (r > 0) {
-      const int mr = M * r, rp = (r + 31) & ~31;
-      const int par = mr <= kThreads ? kThreads / mr : 1;
-      for (int i = t; i < (par > 1 ? par * mr : mr); i += kThreads) {
-        const int e = i % mr, q0 = i / mr;
-        float s = 0.0f;
-#pragma unroll 8
-        for (int q = q0; q < slices; q += par) s += part[static_cast<int64_t>(q) * mr + e];
-        s_u[i] = s;
-      }
-      __syncthreads();
-      for (int i = t; i < 16 * rp; i += kThreads) {
-        const int row = i / rp, j = i % rp;
-        float s = 0.0f;
-        if (row < M && j < r) {
-          for (int q = 0; q < par; ++q) s += s_u[q * mr + row * r + j];
-          if (u_out && blockIdx.x == 0)
-            u_out[row * r + j] = static_cast<uint16_t>(pack_bf16x2(s, 0.f) & 0xFFFF);
-        }
-        s_us[i] = static_cast<uint16_t>(pack_bf16x2(s * lora_scale, 0.f) & 0xFFFF);
-      }
-    }
+  if (kMT == 1 && r > 0) {
+    const int q0 = t / mr;
+    float s = 0.0f;
+#pragma unroll
+    for (int k = 0; k < kEarly; ++k)
+      if (q0 + k * par < slices) s += early[k];
+    if (t < par * mr) s_u[t] = s;
   }
 
   f32x4_t acc[kMT];
@@ -273,6 +269,31 @@ __global__ __launch_bounds__(64 * kWaves) void fp8_decode_kernel(
   }
 #pragma unroll
   for (int i = 0; i < kMT; ++i) s_acc[wave][i][lane] = acc[i];
+  if constexpr (kMT == 1) {
+    if (r > 0) {
+      // the slices past the early ones, and the values past the first kThreads
+      for (int i = t; i < (par > 1 ? par * mr : mr); i += kThreads) {
+        const int e = i % mr, q0 = i / mr;
+        float s = i == t ? s_u[i] : 0.0f;
+#pragma unroll 8
+        for (int q = q0 + (i == t ? kEarly * par : 0); q < slices; q += par)
+          s += part[static_cast<int64_t>(q) * mr + e];
+        s_u[i] = s;
+      }
+      __syncthreads();
+      const int rp = (r + 31) & ~31;
+      for (int i = t; i < 16 * rp; i += kThreads) {
+        const int row = i / rp, j = i % rp;
+        float s = 0.0f;
+        if (row < M && j < r) {
+          for (int q = 0; q < par; ++q) s += s_u[q * mr + row * r + j];
+          if (u_out && blockIdx.x == 0)
+            u_out[row * r + j] = static_cast<uint16_t>(pack_bf16x2(s, 0.f) & 0xFFFF);
+        }
+        s_us[i] = static_cast<uint16_t>(pack_bf16x2(s * lora_scale, 0.f) & 0xFFFF);
+      }
+    }
+  }
   __syncthreads();
   if (wave >= kMT) return;
   f32x4_t sum = s_acc[0][wave][lane];
