@@ -321,13 +321,19 @@ int fp8_linear(bool bwd, const qn_fp8_weight* w, const qn_bf16* in, int64_t M, c
   (void)hipGetLastError();
   const float ls = r > 0 ? alpha / static_cast<float>(r) : 0.0f;
   qn_bf16* low = r > 0 ? low_out : nullptr;
-  if (!bwd && M == 1 && qn::fp8_token_self_u(v, r))
-    return hip_status(qn::launch_fp8_token(v, in, A, B, r, ls, out, low, s));
   uint8_t* codes = static_cast<uint8_t*>(ws);
   float* scale = reinterpret_cast<float*>(codes + f.scale);
   float* part = reinterpret_cast<float*>(codes + f.part);
   uint16_t* act = reinterpret_cast<uint16_t*>(codes + f.act);
   float* split = f.total > f.split ? reinterpret_cast<float*>(codes + f.split) : nullptr;
+  if (!bwd && M == 1) {
+    const bool own_u = qn::fp8_token_self_u(v, r);
+    if (!own_u && qn::launch_fp8_decode_project(in, 1, L, A, r, nullptr, nullptr, part, s) !=
+                      hipSuccess)
+      return QN_ERR_HIP;
+    return hip_status(qn::launch_fp8_token(v, in, A, own_u ? nullptr : part,
+                                           qn::fp8_decode_slices(L), B, r, ls, out, low, s));
+  }
   const bool decode = !bwd && M <= qn::kFp8DecodeM, few = !bwd && M <= qn::kFp8FewM;
   const int m32 = static_cast<int>(few ? M : 0);
   hipError_t e = r == 0   ? qn::launch_fp8_quantize_rows(in, M, L, codes, scale, s)

@@ -11,8 +11,8 @@
 // LDS nor a second pass.  The waves' fp32 sums meet in LDS and are added in
 // wave order, so results are bit-reproducible.
 //
-// One token: the same launch quantises x and, where the adapter is small,
-// computes u = x A^T, each wave for its own blocks: at 4096 x 4096 the whole
+// One token: the same launch quantises x, each wave for its own blocks, and,
+// where the adapter is small, computes u = x A^T: at 4096 x 4096 the whole
 // call is one launch.  More tokens: x's codes and u's partial sums come from
 // a launch before.
 
@@ -56,19 +56,21 @@ __device__ __forceinline__ void store_columns(uint16_t* y, f32x4_t acc) {
       make_uint2(pack_bf16x2(acc[0], acc[1]), pack_bf16x2(acc[2], acc[3]));
 }
 
-// One token.  kRT: 16-rank tiles of the projection computed here; with kRT ==
-// 0 and r > 0 u comes as `slices` partial sums.
-template <int kRT>
+// Where one token's u comes from: no adapter, x A^T computed here (r <= 16),
+// or `slices` partial sums of it.
+enum TokenU { kNoAdapter, kOwnU, kGivenU };
+
+template <int kU>
 __global__ __launch_bounds__(1024) void fp8_token_kernel(
     const uint8_t* __restrict__ w, const float* __restrict__ ws, int64_t N, int64_t K,
     const uint16_t* __restrict__ x, const uint16_t* __restrict__ A, bool vec_a,
-    const uint16_t* __restrict__ B, int r, bool vec_b, float lora_scale, uint16_t* __restrict__ y,
-    uint16_t* __restrict__ u_out) {
-  constexpr int kWaves = 16, kAhead = 2;
-  constexpr int kR = kRT > 0 ? kRT : 1;
+    const float* __restrict__ part, int slices, const uint16_t* __restrict__ B, int r, bool vec_b,
+    float lora_scale, uint16_t* __restrict__ y, uint16_t* __restrict__ u_out) {
+  constexpr int kWaves = 16, kThreads = 64 * kWaves, kAhead = 2;
+  constexpr int kFrags = kU == kGivenU ? kMaxRank / 32 : 1;
   __shared__ f32x4_t s_acc[kWaves][4];
-  __shared__ f32x4_t s_u[kR][kWaves][4];
-  __shared__ __attribute__((aligned(16))) uint16_t s_us[16 * kR + 16];
+  __shared__ float s_u[kU == kNoAdapter ? 1 : kThreads];  // kOwnU: [wave][16 ranks]
+  __shared__ __attribute__((aligned(16))) uint16_t s_us[32 * kFrags];
   __shared__ __attribute__((aligned(16))) uint32_t s_x[kWaves][kAhead][64];   // bf16 pairs
   __shared__ __attribute__((aligned(16))) uint16_t s_q[kWaves][kAhead][64];   // code pairs
   const int t = threadIdx.x, lane = t & 63;
@@ -79,21 +81,32 @@ __global__ __launch_bounds__(1024) void fp8_token_kernel(
   const uint8_t* wr = w + (n0 + li) * K;
   const float* wsr = ws + (n0 / 128) * kb;
 
-  uint4 bf[(kR + 1) / 2];
-  if (kRT > 0 && wave == 0) {
+  uint4 bf[kFrags];
+  if (kU != kNoAdapter && wave == 0) {
 #pragma unroll
-    for (int q = 0; q < (kR + 1) / 2; ++q)
-      bf[q] = load_bf16x8(B + (n0 + li) * r + 32 * q + 8 * lg, r - 32 * q - 8 * lg, vec_b);
+    for (int q = 0; q < kFrags; ++q) {
+      bf[q] = make_uint4(0, 0, 0, 0);
+      if (32 * q < r)
+        bf[q] = load_bf16x8(B + (n0 + li) * r + 32 * q + 8 * lg, r - 32 * q - 8 * lg, vec_b);
+    }
   }
-  f32x4_t acc = f32x4_t{0.f, 0.f, 0.f, 0.f}, ua[kR];
-#pragma unroll
-  for (int i = 0; i < kR; ++i) ua[i] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+  if constexpr (kU == kGivenU) {
+    // thread (q0, j) adds the slices q0, q0 + par, ... of rank j
+    const int par = kThreads / r, j = t % r, q0 = t / r;
+    float s = 0.0f;
+    if (q0 < par) {
+#pragma unroll 4
+      for (int q = q0; q < slices; q += par) s += part[static_cast<int64_t>(q) * r + j];
+    }
+    s_u[t] = s;
+  }
+  f32x4_t acc = f32x4_t{0.f, 0.f, 0.f, 0.f}, ua = acc;
   for (int64_t bw = wave; bw < kb; bw += kAhead * kWaves) {
     // everything that these blocks need is asked for first
     Bytes32 wv[kAhead];
     uint32_t xp[kAhead];
     float sw[kAhead];
-    uint4 av[kAhead][kR][4];
+    uint4 av[kAhead][4];
 #pragma unroll
     for (int d = 0; d < kAhead; ++d) {
       const int64_t b = bw + d * kWaves;
@@ -102,15 +115,12 @@ __global__ __launch_bounds__(1024) void fp8_token_kernel(
       xp[d] = in && k < K ? *reinterpret_cast<const uint32_t*>(x + k) : 0u;
       wv[d] = row_bytes(wr, in ? b : kb, K, lg);
       sw[d] = in ? wsr[b] : 0.0f;
-      if constexpr (kRT > 0) {
+      if constexpr (kU == kOwnU) {
 #pragma unroll
-        for (int i = 0; i < kRT; ++i)
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            const int64_t ka = b * 128 + 32 * c + 8 * lg;
-            const int j = 16 * i + li;
-            av[d][i][c] = load_bf16x8(A + j * K + ka, j < r && in && ka < K ? 8 : 0, vec_a);
-          }
+        for (int c = 0; c < 4; ++c) {
+          const int64_t ka = b * 128 + 32 * c + 8 * lg;
+          av[d][c] = load_bf16x8(A + li * K + ka, li < r && in && ka < K ? 8 : 0, vec_a);
+        }
       }
     }
 #pragma unroll
@@ -118,7 +128,7 @@ __global__ __launch_bounds__(1024) void fp8_token_kernel(
       const float x0 = bf16_lo(xp[d]), x1 = bf16_hi(xp[d]);
       const float s = fp8_scale(wave_max(fmaxf(fabsf(x0), fabsf(x1))));
       const float inv = __fdiv_rn(1.0f, s);
-      s_x[wave][d][lane] = xp[d];
+      if constexpr (kU == kOwnU) s_x[wave][d][lane] = xp[d];
       s_q[wave][d][lane] = static_cast<uint16_t>(__builtin_amdgcn_cvt_pk_fp8_f32(
           fp8_ratio(x0, s, inv), fp8_ratio(x1, s, inv), 0, false));
       sw[d] *= s;
@@ -132,13 +142,11 @@ __global__ __launch_bounds__(1024) void fp8_token_kernel(
           mfma_fp8(frag8(wv[d].lo, wv[d].hi), frag8(q[0], q[1]), f32x4_t{0.f, 0.f, 0.f, 0.f});
 #pragma unroll
       for (int e = 0; e < 4; ++e) acc[e] = fmaf(c[e], sw[d], acc[e]);
-      if constexpr (kRT > 0) {
+      if constexpr (kU == kOwnU) {
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const uint4 xf = *reinterpret_cast<const uint4*>(&s_x[wave][d][16 * k + 4 * lg]);
-#pragma unroll
-          for (int i = 0; i < kRT; ++i) ua[i] = mfma_bf16_32(av[d][i][k], xf, ua[i]);
-        }
+        for (int k = 0; k < 4; ++k)
+          ua = mfma_bf16_32(
+              av[d][k], *reinterpret_cast<const uint4*>(&s_x[wave][d][16 * k + 4 * lg]), ua);
       }
     }
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // read before the next blocks' values
@@ -146,26 +154,26 @@ __global__ __launch_bounds__(1024) void fp8_token_kernel(
   // all 16 result columns are the same token: keep column 0
   if (li == 0) {
     s_acc[wave][lg] = acc;
-    if constexpr (kRT > 0) {
-#pragma unroll
-      for (int i = 0; i < kRT; ++i) s_u[i][wave][lg] = ua[i];
-    }
+    if constexpr (kU == kOwnU) *reinterpret_cast<f32x4_t*>(&s_u[16 * wave + 4 * lg]) = ua;
   }
   __syncthreads();
   if (wave > 0) return;
 #pragma unroll
   for (int q = 0; q < kWaves; ++q) acc = q == 0 ? s_acc[0][lg] : acc + s_acc[q][lg];
-  if constexpr (kRT > 0) {
-    if (lane < 16 * kRT) {
+  if constexpr (kU != kNoAdapter) {
+    const int pitch = kU == kOwnU ? 16 : r;
+    const int sums = kU == kOwnU          ? kWaves
+                     : kThreads / r < slices ? kThreads / r
+                                             : slices;
+    for (int j = lane; j < 32 * kFrags && j < ((r + 31) & ~31); j += 64) {
       float s = 0.0f;
-#pragma unroll
-      for (int q = 0; q < kWaves; ++q) s += s_u[lane >> 4][q][(lane >> 2) & 3][lane & 3];
-      if (u_out && blockIdx.x == 0 && lane < r)
-        u_out[lane] = static_cast<uint16_t>(pack_bf16x2(s, 0.f) & 0xFFFF);
-      // ranks from r on are zero: their rows of A were read as zeros
-      s_us[lane] = static_cast<uint16_t>(pack_bf16x2(s * lora_scale, 0.f) & 0xFFFF);
-    } else if (lane < 16 * kRT + 16) {
-      s_us[lane] = 0;
+      if (j < r) {
+#pragma unroll 8
+        for (int q = 0; q < sums; ++q) s += s_u[q * pitch + j];
+      }
+      if (u_out && blockIdx.x == 0 && j < r)
+        u_out[j] = static_cast<uint16_t>(pack_bf16x2(s, 0.f) & 0xFFFF);
+      s_us[j] = static_cast<uint16_t>(pack_bf16x2(s * lora_scale, 0.f) & 0xFFFF);
     }
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
     acc = lora_up(acc, bf, s_us, 0, r, li, lg);
@@ -286,7 +294,7 @@ __global__ __launch_bounds__(64 * kWaves) void fp8_decode_kernel(
         const int row = i / rp, j = i % rp;
         float s = 0.0f;
         if (row < M && j < r) {
-          for (int q = 0; q < par; ++q) s += s_u[q * mr + row * r + j];
+          for (int q = 0; q < par && q < slices; ++q) s += s_u[q * mr + row * r + j];
           if (u_out && blockIdx.x == 0)
             u_out[row * r + j] = static_cast<uint16_t>(pack_bf16x2(s, 0.f) & 0xFFFF);
         }
@@ -314,23 +322,26 @@ __global__ __launch_bounds__(64 * kWaves) void fp8_decode_kernel(
 }  // namespace
 
 bool fp8_token_self_u(const Fp8View& w, int r) {
-  // A is read by every workgroup: past about 40 MB in all (from the caches)
-  // a projection launch of its own costs less
+  // A is read by every workgroup, from the caches: past about 40 MB in all a
+  // projection launch of its own costs less (one token, r = 16: 4096 x 4096,
+  // 34 MB, 9.1 us against 10.9; 11008 x 4096, 90 MB, 23.6 against 18.3)
   return r <= 16 && w.N / 16 * r * w.K * 2 <= (int64_t{40} << 20);
 }
 
 hipError_t launch_fp8_token(const Fp8View& w, const uint16_t* x, const uint16_t* A,
-                            const uint16_t* B, int r, float lora_scale, uint16_t* y,
-                            uint16_t* u_out, hipStream_t st) {
+                            const float* part, int slices, const uint16_t* B, int r,
+                            float lora_scale, uint16_t* y, uint16_t* u_out, hipStream_t st) {
   const dim3 grid(static_cast<uint32_t>(w.N / 16));
   const bool vec_a = (reinterpret_cast<uintptr_t>(A) & 15) == 0;
   const bool vec_b = (r & 7) == 0 && (reinterpret_cast<uintptr_t>(B) & 15) == 0;
   auto go = [&](auto k) {
-    hipLaunchKernelGGL(k, grid, dim3(1024), 0, st, w.codes, w.scale, w.N, w.K, x, A, vec_a, B, r,
-                       vec_b, lora_scale, y, u_out);
+    hipLaunchKernelGGL(k, grid, dim3(1024), 0, st, w.codes, w.scale, w.N, w.K, x, A, vec_a, part,
+                       slices, B, r, vec_b, lora_scale, y, u_out);
     return hipGetLastError();
   };
-  return r == 0 ? go(fp8_token_kernel<0>) : go(fp8_token_kernel<1>);
+  return r == 0   ? go(fp8_token_kernel<kNoAdapter>)
+         : part   ? go(fp8_token_kernel<kGivenU>)
+                  : go(fp8_token_kernel<kOwnU>);
 }
 
 hipError_t launch_fp8_decode(const Fp8View& w, const uint8_t* x, const float* xs, int M,

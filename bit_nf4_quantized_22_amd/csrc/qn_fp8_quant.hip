@@ -263,7 +263,7 @@ __global__ __launch_bounds__(kT) void decode_project_kernel(
   am = fmaxf(am, __shfl_xor(am, 16, 64));
   am = fmaxf(am, __shfl_xor(am, 32, 64));
   const float s = fp8_scale(am), inv = __fdiv_rn(1.0f, s);
-  if (li < M && b * 128 < L) {
+  if (codes && li < M && b * 128 < L) {
     if (lg == 0) scale[b * M + li] = s;
 #pragma unroll
     for (int c = 0; c < 4; ++c) {

@@ -155,16 +155,17 @@ hipError_t launch_fp8_decode(const Fp8View& w, const uint8_t* x, const float* xs
                              const uint16_t* B, int r, float lora_scale, uint16_t* y,
                              uint16_t* u_out, hipStream_t st);
 // launch_fp8_quantize_project of M <= kFp8DecodeM tokens with P = A, into
-// fp8_decode_slices(L) slices.
+// fp8_decode_slices(L) slices; codes == nullptr: the projection alone.
 int fp8_decode_slices(int64_t L);
 hipError_t launch_fp8_decode_project(const uint16_t* x, int M, int64_t L, const uint16_t* A, int r,
                                      uint8_t* codes, float* scale, float* part, hipStream_t st);
-// One token in one launch: x quantised and u = x A^T computed by the product's
-// workgroups; for r == 0 or where fp8_token_self_u holds.
+// One token, x quantised by the product's workgroups; u = x A^T given as
+// slices partial sums, or (part == nullptr, where fp8_token_self_u holds)
+// computed by them too.
 bool fp8_token_self_u(const Fp8View& w, int r);
 hipError_t launch_fp8_token(const Fp8View& w, const uint16_t* x, const uint16_t* A,
-                            const uint16_t* B, int r, float lora_scale, uint16_t* y,
-                            uint16_t* u_out, hipStream_t st);
+                            const float* part, int slices, const uint16_t* B, int r,
+                            float lora_scale, uint16_t* y, uint16_t* u_out, hipStream_t st);
 // out = bf16(sum of `splits` fp32 parts of n values).
 hipError_t launch_fp8_split_sum(const float* part, int splits, int64_t n, uint16_t* out,
                                 hipStream_t st);
