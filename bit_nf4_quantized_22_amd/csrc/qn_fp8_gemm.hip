@@ -594,9 +594,11 @@ int fp8_gemm_splits(int64_t M, int64_t ncols, int64_t L) {
   if (M <= 0 || large(M, ncols)) return 1;
   const int64_t tiles = ((ncols + Small::kBN - 1) / Small::kBN) *
                         ((M + Small::kBM - 1) / Small::kBM);
-  // two workgroups per CU, at least 4 blocks each
-  int64_t s = 512 / tiles;
-  const int64_t most = L / 128 / 4;
+  // one workgroup per CU, at least 8 blocks each: adding the parts up costs a
+  // launch (333 x 1088 x 2112 backward, 8 blocks: whole 10.8 us, in two 14.8;
+  // 128 x 11008 x 4096, 86 blocks: whole 68 us, in eight 21)
+  int64_t s = 256 / tiles;
+  const int64_t most = L / 128 / 8;
   s = s < most ? s : most;
   if (s < 2) return 1;
   const int64_t per = (L / 128 + s - 1) / s;

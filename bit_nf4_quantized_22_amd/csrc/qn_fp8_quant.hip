@@ -123,7 +123,9 @@ __global__ __launch_bounds__(64 * kWaves) void quantize_project_kernel(
   constexpr int kThreads = 64 * kWaves;
   constexpr int kLoads = kRT * 256 / kThreads;  // 16-byte chunks of P per thread and block
   static_assert(kLoads * kThreads == kRT * 256, "P tile split");
+  constexpr int kQPitch = 128 + 16;
   __shared__ __attribute__((aligned(16))) uint16_t sP[2][kRT * 16 * 128];
+  __shared__ __attribute__((aligned(16))) uint8_t sQ[kWaves][16 * kQPitch];
   const int t = threadIdx.x, lane = t & 63, li = lane & 15, lg = lane >> 4;
   const int64_t row = (static_cast<int64_t>(blockIdx.x) * kWaves + (t >> 6)) * 16 + li;
   const int64_t m = row < M ? row : M - 1;
@@ -184,13 +186,20 @@ __global__ __launch_bounds__(64 * kWaves) void quantize_project_kernel(
     am = fmaxf(am, __shfl_xor(am, 16, 64));
     am = fmaxf(am, __shfl_xor(am, 32, 64));
     const float s = fp8_scale(am), inv = __fdiv_rn(1.0f, s);
-    if (row < M) {
-      if (lg == 0) scale[b * M + row] = s;
+    if (row < M && lg == 0) scale[b * M + row] = s;
+    // the codes leave as whole 128-byte rows, 8 of them per store (8 bytes of
+    // 16 rows per store took 40% longer for the whole kernel); the wave's own
+    // LDS order keeps the turns of sQ apart
+    uint8_t* sq = sQ[t >> 6];
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        const int64_t k = b * 128 + 32 * c + 8 * lg;
-        if (k < L) *reinterpret_cast<uint2*>(codes + row * L + k) = fp8_codes8(v[c], s, inv);
-      }
+    for (int c = 0; c < 4; ++c)
+      *reinterpret_cast<uint2*>(sq + li * kQPitch + 32 * c + 8 * lg) = fp8_codes8(v[c], s, inv);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int rr = 8 * h + (lane >> 3);
+      const int64_t to = row - li + rr, k = b * 128 + (lane & 7) * 16;
+      const uint4 q = *reinterpret_cast<const uint4*>(sq + rr * kQPitch + (lane & 7) * 16);
+      if (to < M && k < L) *reinterpret_cast<uint4*>(codes + to * L + k) = q;
     }
 #pragma unroll
     for (int c = 0; c < 4; ++c)
