@@ -777,10 +777,12 @@ def _fp8_linear(fn, op, fw, x, L, n, A, B, r, alpha, out, low, ws, stream):
     fwd = op == QN_OP_FP8_FWD
     _fit(x, bf16, M * L, dev, "x" if fwd else "dy")
     a = b = None
-    if r:
+    if r and A is not None:
         _fit(A, bf16, r * fw.K, dev, "A")
+        a = A.data_ptr()
+    if r and B is not None:
         _fit(B, bf16, fw.N * r, dev, "B")
-        a, b = A.data_ptr(), B.data_ptr()
+        b = B.data_ptr()
     if out is None:
         out = torch.empty((M, n), dtype=bf16, device=dev)
     else:

@@ -284,9 +284,10 @@ Fp8Ws fp8_ws(bool bwd, int64_t M, int64_t N, int64_t K, int32_t r) {
   f.scale = round_up(m * static_cast<size_t>(L), 256);
   f.part = f.scale + round_up(m * static_cast<size_t>(blocks128(L)) * 4, 256);
   f.act = f.part;
+  const int slices = !bwd && M <= qn::kFp8DecodeM ? qn::fp8_decode_slices(L)
+                                                  : qn::fp8_project_slices(M, L);
   if (r > 0)
-    f.act += round_up(m * static_cast<size_t>(r) * 4 *
-                          static_cast<size_t>(qn::fp8_project_slices(M, L)), 256);
+    f.act += round_up(m * static_cast<size_t>(r) * 4 * static_cast<size_t>(slices), 256);
   f.split = f.act;
   if (r > 0 && (bwd || M > qn::kFp8DecodeM))
     f.split += round_up(m * static_cast<size_t>(qn::fp8_lora_pitch(r)) * 2, 256);

@@ -522,9 +522,12 @@ QN_API int fp8_matmul(const qn_fp8_weight* w, const uint8_t* x, const float* xsc
  *   y = Q(x) * value(W)^T + (alpha/r) * (x * A^T) * B^T,
  * Q(x) the values of x's codes (fp8_quantize_rows).  The adapter reads the
  * unquantised x.  Arguments, shapes of x, A, B, y, u_out and the rules for r
- * and NULL adapters as qlora_linear_fwd; out bf16.
+ * and NULL adapters as qlora_linear_fwd; x and y 16-byte aligned, y not
+ * overlapping any operand (dx likewise below).
  *   ws  device workspace of ws_bytes >= qn_workspace_bytes(QN_OP_FP8_FWD,..)
  *       (needed for r == 0 too: x's codes lie there).
+ * A row of y is bit-reproducible for a given batch; batches of up to 16, up
+ * to 64 and more tokens add the blocks up in orders of their own.
  */
 QN_API int fp8_linear_fwd(const qn_fp8_weight* w, const qn_bf16* x, int64_t M, const qn_bf16* A,
                           const qn_bf16* B, int32_t r, float alpha, qn_bf16* y, qn_bf16* u_out,

@@ -327,3 +327,30 @@ def test_a_training_step_of_an_8_bit_layer():
     qd = fp8.row_values(*fp8.quantize_rows(dy))
     ref = qd @ wv + s * (dy.astype(np.float64) @ B0) @ A0
     assert np.linalg.norm(dx.float().cpu().numpy() - ref) <= 2.0 ** -8 * np.linalg.norm(ref)
+
+
+def test_table_refuses_the_same_matrix_twice():
+    t = upload(make([300], 32, 2, False, seed=1), 32, False)[0]
+    two = lambda k: [t[k], t[k]]
+    with pytest.raises(qn.QnError) as e:
+        qn.lora_adamw_table(two("p"), two("g"), two("m"), two("v"))
+    assert e.value.status == qn.QN_ERR_SHAPE
+    with pytest.raises(ValueError):
+        qn.lora_adamw_table([t["p"]], [t["g"]], [t["m"].cpu()], [t["v"]])
+    with pytest.raises(ValueError):
+        qn.lora_adamw_table([t["p"]], [t["g"]], [t["m"][:299]], [t["v"]])
+    with pytest.raises(qn.QnError) as e:
+        qn.lora_adamw_table([t["p"][1:]], [t["g"][1:]], [t["m"][1:]], [t["v"][1:]])
+    assert e.value.status == qn.QN_ERR_ALIGN
+
+
+def test_steps_on_another_stream():
+    state = make([5000, 70], 8, 3, False, seed=4)
+    t = upload(state, 8, False)
+    tab = table_of(t, 8)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    norm = qn.lora_grad_norm(tab, 1e9, stream=side)
+    qn.lora_adamw_multi_step(tab, 3, grad_scale=norm[1:], stream=side, **HYPER)
+    torch.cuda.synchronize()
+    check(state, t, 8, 3)

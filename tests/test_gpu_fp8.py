@@ -333,3 +333,77 @@ def test_empty_batch_writes_nothing():
     c, s = qn.fp8_quantize_rows(x)
     assert qn.fp8_matmul(fw, c, s).shape == (0, 32)
     torch.cuda.synchronize()
+
+
+def test_long_contraction_of_a_few_tokens():
+    """More blocks than any layer has: the decode projection's slices grow
+    with K and have to fit the workspace."""
+    M, N, K, r = 2, 16, 2 ** 18 + 8208, 4
+    rng = np.random.default_rng(1)
+    w = (rng.standard_normal((N, K)) * 0.02).astype(np.float32)
+    xb = acts(M, K, 5)
+    A, B = (bf16_of(rng.standard_normal(s) * 0.02) for s in ((r, K), (N, r)))
+    fw = qn.fp8_quantize_weight(torch.from_numpy(w).to(DEV))
+    wv = fp8.weight_values(*fp8.quantize_blocks(w))
+    xf, Af, Bf = f64(xb), f64(A), f64(B)
+    xv = fp8.row_values(*fp8.quantize_rows(xf.astype(np.float32)))
+    for m in (1, 2):
+        y = qn.fp8_linear_fwd(fw, bf16_dev(xb[:m]), bf16_dev(A), bf16_dev(B), r, 8.0)
+        torch.cuda.synchronize()
+        check(f"fp8 y {m}x{N}x{K}", to_np(y), xv[:m] @ wv.T + 2.0 * (xf[:m] @ Af.T) @ Bf.T)
+
+
+@pytest.mark.parametrize("M", [1, 40, 100])
+def test_missing_adapter_is_the_frozen_layer(M):
+    fw = qn.fp8_quantize_weight(torch.from_numpy(weights(144, 272, 3)).to(DEV))
+    x, dy = bf16_dev(acts(M, 272, 1)), bf16_dev(acts(M, 144, 2))
+    for f, v in ((qn.fp8_linear_fwd, x), (qn.fp8_linear_bwd_dx, dy)):
+        a, b = f(fw, v, None, None, 0, 1.0), f(fw, v, None, None, 8, 16.0)
+        assert torch.equal(a.view(torch.int16), b.view(torch.int16))
+    A = bf16_dev(bf16_of(np.zeros((8, 272))))
+    with pytest.raises(qn.QnError):
+        qn.fp8_linear_fwd(fw, x, A, None, 8, 16.0)
+
+
+def test_binding_refusals_on_the_device():
+    fw = qn.fp8_quantize_weight(torch.from_numpy(weights(32, 48, 3)).to(DEV))
+    x = bf16_dev(acts(4, 48, 1))
+    bad = [lambda: qn.fp8_linear_fwd(fw, x.float(), None, None, 0, 1.0),
+           lambda: qn.fp8_linear_fwd(fw, x[:, :32], None, None, 0, 1.0),
+           lambda: qn.fp8_linear_fwd(fw, bf16_dev(acts(48, 4, 1)).t(), None, None, 0, 1.0),
+           lambda: qn.fp8_linear_fwd(fw, x.cpu(), None, None, 0, 1.0),
+           lambda: qn.fp8_linear_bwd_dx(fw, x, None, None, 0, 1.0),
+           lambda: qn.fp8_matmul(fw, x, torch.zeros(1, 4, device=DEV)),
+           lambda: qn.Fp8Weight(fw.codes, fw.scale.flatten()[:0]),
+           lambda: qn.fp8_quantize_rows(x.float())]
+    for f in bad:
+        with pytest.raises(ValueError):
+            f()
+    with pytest.raises(qn.QnError) as e:      # 24 columns: not a multiple of 16
+        qn.fp8_quantize_rows(bf16_dev(acts(2, 24, 1)))
+    assert e.value.status == qn.QN_ERR_SHAPE
+    with pytest.raises(qn.QnError) as e:
+        qn.fp8_linear_fwd(fw, x, None, None, 0, 1.0,
+                          ws=torch.empty(64, dtype=torch.uint8, device=DEV))
+    assert e.value.status == qn.QN_ERR_WORKSPACE
+
+
+# grids of the tile kernels: halves alone, whole tiles alone, both (the large
+# test above), rows that end inside a half and inside a whole tile
+@pytest.mark.parametrize("M,N", [(1100, 4096), (1000, 12000), (2100, 8000)])
+def test_tile_grids_on_some_rows(M, N):
+    K, r = 400, 8
+    w = weights(N, K, M)
+    rng = np.random.default_rng(N)
+    xb = acts(M, K, 3)
+    A, B = (bf16_of(rng.standard_normal(sh) * 0.02) for sh in ((r, K), (N, r)))
+    fw = qn.fp8_quantize_weight(torch.from_numpy(w).to(DEV))
+    wv = fp8.weight_values(*fp8.quantize_blocks(w))
+    y = torch.full((M + 1, N), 7.0, dtype=torch.bfloat16, device=DEV)
+    qn.fp8_linear_fwd(fw, bf16_dev(xb), bf16_dev(A), bf16_dev(B), r, 16.0, y=y[:M])
+    torch.cuda.synchronize()
+    assert torch.all(y[M] == 7.0)
+    rows = np.unique(np.concatenate([np.arange(0, M, 97), [127, 128, 255, 256, M - 1]]))
+    v, Af, Bf = f64(xb[rows]), f64(A), f64(B)
+    qv = fp8.row_values(*fp8.quantize_rows(v.astype(np.float32)))
+    check(f"fp8 y {M}x{N}x{K}", to_np(y)[rows], qv @ wv.T + 2.0 * (v @ Af.T) @ Bf.T)
