@@ -211,7 +211,7 @@ struct AdamChunk {
 };
 constexpr int kAdamChunk = 2048;
 constexpr int kAdamStateBlock = 256;  // elements per scale of the 8-bit states
-constexpr int kGradNormBlocks = 2048;  // most partial sums of the gradient norm
+constexpr int kGradNormBlocks = 1024;  // most partial sums of the gradient norm
 int grad_norm_blocks(int64_t chunks);
 hipError_t launch_adamw_multi(const AdamChunk* tab, int64_t chunks, bool state8, bool bf16_grad,
                               const float* grad_scale, float lr, float beta1, float beta2,
