@@ -684,10 +684,12 @@ def fp8_quantize_blocks(w, codes=None, scale=None, stream=None):
     nb, kb = -(-N // FP8_BLOCK), -(-K // FP8_BLOCK)
     if codes is None:
         codes = torch.empty((N, K), dtype=torch.float8_e4m3fn, device=w.device)
+    else:
+        _fit(codes, torch.float8_e4m3fn, N * K, w.device, "codes")
     if scale is None:
         scale = torch.empty((nb, kb), dtype=torch.float32, device=w.device)
-    _fit(codes, torch.float8_e4m3fn, N * K, w.device, "codes")
-    _fit(scale, torch.float32, nb * kb, w.device, "scale")
+    else:
+        _fit(scale, torch.float32, nb * kb, w.device, "scale")
     _call("fp8_quantize_blocks", w.device, stream, w.data_ptr(),
           QN_F32 if w.dtype == torch.float32 else QN_BF16, N, K, codes.data_ptr(),
           scale.data_ptr())
@@ -710,10 +712,12 @@ def fp8_quantize_rows(x, codes=None, scale=None, stream=None):
     _dev(x, torch.bfloat16, name="x")
     if codes is None:
         codes = torch.empty((M, K), dtype=torch.float8_e4m3fn, device=x.device)
+    else:
+        _fit(codes, torch.float8_e4m3fn, M * K, x.device, "codes")
     if scale is None:
         scale = torch.empty((kb, M), dtype=torch.float32, device=x.device)
-    _fit(codes, torch.float8_e4m3fn, M * K, x.device, "codes")
-    _fit(scale, torch.float32, kb * M, x.device, "scale")
+    else:
+        _fit(scale, torch.float32, kb * M, x.device, "scale")
     _call("fp8_quantize_rows", x.device, stream, x.data_ptr(), M, K, codes.data_ptr(),
           scale.data_ptr())
     return codes, scale
