@@ -651,6 +651,16 @@ def _call(fn, dev, stream, *args):
         _check(fn, status)
 
 
+def _new(shape, dtype, dev, stream):
+    """A tensor for a call on the given stream: in that stream's memory, so
+    that neither earlier nor later work of the current stream shares it."""
+    torch = _torch()
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=dev)
+
+
 def _addr(t):
     return None if t is None else t.data_ptr()
 
@@ -683,11 +693,11 @@ def fp8_quantize_blocks(w, codes=None, scale=None, stream=None):
     N, K = w.shape
     nb, kb = -(-N // FP8_BLOCK), -(-K // FP8_BLOCK)
     if codes is None:
-        codes = torch.empty((N, K), dtype=torch.float8_e4m3fn, device=w.device)
+        codes = _new((N, K), torch.float8_e4m3fn, w.device, stream)
     else:
         _fit(codes, torch.float8_e4m3fn, N * K, w.device, "codes")
     if scale is None:
-        scale = torch.empty((nb, kb), dtype=torch.float32, device=w.device)
+        scale = _new((nb, kb), torch.float32, w.device, stream)
     else:
         _fit(scale, torch.float32, nb * kb, w.device, "scale")
     _call("fp8_quantize_blocks", w.device, stream, w.data_ptr(),
@@ -711,11 +721,11 @@ def fp8_quantize_rows(x, codes=None, scale=None, stream=None):
     kb = -(-K // FP8_BLOCK)
     _dev(x, torch.bfloat16, name="x")
     if codes is None:
-        codes = torch.empty((M, K), dtype=torch.float8_e4m3fn, device=x.device)
+        codes = _new((M, K), torch.float8_e4m3fn, x.device, stream)
     else:
         _fit(codes, torch.float8_e4m3fn, M * K, x.device, "codes")
     if scale is None:
-        scale = torch.empty((kb, M), dtype=torch.float32, device=x.device)
+        scale = _new((kb, M), torch.float32, x.device, stream)
     else:
         _fit(scale, torch.float32, kb * M, x.device, "scale")
     _call("fp8_quantize_rows", x.device, stream, x.data_ptr(), M, K, codes.data_ptr(),
@@ -731,8 +741,9 @@ def fp8_dequant(fw, out_dtype=None, out=None, stream=None):
         raise ValueError("fp8_dequant: out_dtype must be float32 or bfloat16")
     dev = fw.device
     if out is None:
-        out = torch.empty((fw.N, fw.K), dtype=out_dtype, device=dev)
-    _fit(out, out_dtype, fw.N * fw.K, dev, "out")
+        out = _new((fw.N, fw.K), out_dtype, dev, stream)
+    else:
+        _fit(out, out_dtype, fw.N * fw.K, dev, "out")
     _call("fp8_dequant", dev, stream, fw.c_struct(),
           QN_BF16 if out_dtype == torch.bfloat16 else QN_F32, out.data_ptr())
     return out
@@ -750,11 +761,12 @@ def fp8_matmul(fw, codes, scale, transposed=False, out=None, ws=None, stream=Non
     _fit(codes, torch.float8_e4m3fn, M * L, dev, "codes")
     _fit(scale, torch.float32, -(-L // FP8_BLOCK) * M, dev, "scale")
     if out is None:
-        out = torch.empty((M, n), dtype=torch.bfloat16, device=dev)
-    _fit(out, torch.bfloat16, M * n, dev, "out")
+        out = _new((M, n), torch.bfloat16, dev, stream)
+    else:
+        _fit(out, torch.bfloat16, M * n, dev, "out")
     if ws is None:
-        ws = workspace(qn_workspace_bytes(QN_OP_FP8_BWD_DX if transposed else QN_OP_FP8_FWD, M,
-                                          fw.N, fw.K, 0), dev)
+        op = QN_OP_FP8_BWD_DX if transposed else QN_OP_FP8_FWD
+        ws = _new(qn_workspace_bytes(op, M, fw.N, fw.K, 0), torch.uint8, dev, stream)
     else:
         _fit(ws, torch.uint8, ws.numel(), dev, "ws")
     _call("fp8_matmul", dev, stream, fw.c_struct(), codes.data_ptr(), scale.data_ptr(), M,
@@ -788,13 +800,13 @@ def _fp8_linear(fn, op, fw, x, L, n, A, B, r, alpha, out, low, ws, stream):
         _fit(B, bf16, fw.N * r, dev, "B")
         b = B.data_ptr()
     if out is None:
-        out = torch.empty((M, n), dtype=bf16, device=dev)
+        out = _new((M, n), bf16, dev, stream)
     else:
         _fit(out, bf16, M * n, dev, "y" if fwd else "dx")
     if low is not None:
         _fit(low, bf16, M * r, dev, "u_out" if fwd else "t_out")
     if ws is None:
-        ws = workspace(qn_workspace_bytes(op, M, fw.N, fw.K, r), dev)
+        ws = _new(qn_workspace_bytes(op, M, fw.N, fw.K, r), torch.uint8, dev, stream)
     else:
         _fit(ws, torch.uint8, ws.numel(), dev, "ws")
     _call(fn, dev, stream, fw.c_struct(), x.data_ptr(), M, a, b, r, alpha, out.data_ptr(),
@@ -875,11 +887,13 @@ def lora_grad_norm(table, max_norm, out=None, ws=None, stream=None):
     torch = _torch()
     dev = table.device
     if out is None:
-        out = torch.empty(2, dtype=torch.float32, device=dev)
-    _fit(out, torch.float32, 2, dev, "out")
+        out = _new(2, torch.float32, dev, stream)
+    else:
+        _fit(out, torch.float32, 2, dev, "out")
     if ws is None:
-        ws = workspace(lora_grad_norm_workspace_bytes(table), dev)
-    _fit(ws, torch.uint8, ws.numel(), dev, "ws")
+        ws = _new(lora_grad_norm_workspace_bytes(table), torch.uint8, dev, stream)
+    else:
+        _fit(ws, torch.uint8, ws.numel(), dev, "ws")
     _call("lora_grad_norm", dev, stream, table.plan, table.table.data_ptr(),
           max_norm, out.data_ptr(), ws.data_ptr(), ws.numel())
     return out

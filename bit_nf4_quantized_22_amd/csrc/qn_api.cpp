@@ -264,9 +264,10 @@ int check_fp8_weight(const qn_fp8_weight* w, qn::Fp8View& v) {
   return QN_OK;
 }
 
-// Rows of a batch: every launch over M rows of n columns fits its grid.
+// Rows of a batch: every launch over M rows of n columns has less than 2^32
+// threads (at most 16 per run of 128 columns, 32 per row).
 bool fp8_rows_ok(int64_t M, int64_t n) {
-  return M >= 0 && M <= INT32_MAX && M * blocks128(n) <= INT32_MAX;
+  return M >= 0 && M <= (int64_t{1} << 26) && M * blocks128(n) <= (int64_t{1} << 27);
 }
 
 // Workspace of a quantised batch [M, L] with `cols` output columns: codes, row
@@ -357,6 +358,8 @@ bool adamw_hyper_ok(float lr, float beta1, float beta2, float eps, float weight_
          eps > 0.0f && weight_decay >= 0.0f;
 }
 
+constexpr int64_t kAdamMaxChunks = int64_t{1} << 24;  // 256 threads each, under 2^32
+
 // Chunks of the matrices of an AdamW table, -1 for sizes out of range.
 int64_t adamw_chunks(const qn_adamw_tensor* t, int32_t count) {
   int64_t chunks = 0;
@@ -364,7 +367,7 @@ int64_t adamw_chunks(const qn_adamw_tensor* t, int32_t count) {
     if (t[i].n < 0) return -1;
     if (t[i].n == 0) continue;
     chunks += (t[i].n - 1) / qn::kAdamChunk + 1;
-    if (chunks > INT32_MAX) return -1;
+    if (chunks >= kAdamMaxChunks) return -1;
   }
   return chunks;
 }
@@ -415,7 +418,7 @@ int check_adamw_plan(const qn_adamw_plan* plan, const void* table) {
   if ((plan->grad_dtype != QN_F32 && plan->grad_dtype != QN_BF16) ||
       (plan->state != QN_STATE_F32 && plan->state != QN_STATE_8BIT))
     return QN_ERR_UNSUPPORTED;
-  if (plan->chunks < 0 || plan->chunks > INT32_MAX ||
+  if (plan->chunks < 0 || plan->chunks >= kAdamMaxChunks ||
       plan->bytes != static_cast<int64_t>(adamw_table_size(plan->chunks)))
     return QN_ERR_SHAPE;
   if (plan->chunks > 0 && !table) return QN_ERR_NULL;
@@ -658,7 +661,7 @@ int fp8_quantize_blocks(const void* w, int32_t dtype, int64_t N, int64_t K, uint
                         float* scale, void* stream) {
   if (dtype != QN_F32 && dtype != QN_BF16) return QN_ERR_UNSUPPORTED;
   if (N < 0 || K < 0 || N % 16 != 0 || K % 16 != 0 || N > kFp8MaxDim || K > kFp8MaxDim ||
-      blocks128(N) * blocks128(K) > INT32_MAX)
+      blocks128(N) * blocks128(K) >= (int64_t{1} << 24))
     return QN_ERR_SHAPE;
   if (N == 0 || K == 0) return QN_OK;
   if (!w || !codes || !scale) return QN_ERR_NULL;
@@ -682,7 +685,7 @@ int fp8_dequant(const qn_fp8_weight* w, int32_t out_dtype, void* out, void* stre
   qn::Fp8View v;
   if (int st = check_fp8_weight(w, v); st != QN_OK) return st;
   if (out_dtype != QN_F32 && out_dtype != QN_BF16) return QN_ERR_UNSUPPORTED;
-  if (v.N * v.K / 16 > int64_t{INT32_MAX} * 256) return QN_ERR_SHAPE;
+  if (v.N * v.K / 16 > (int64_t{1} << 31)) return QN_ERR_SHAPE;
   if (!out) return QN_ERR_NULL;
   if (!aligned(out, 16)) return QN_ERR_ALIGN;
   (void)hipGetLastError();

@@ -7,11 +7,13 @@
 
 namespace qn {
 
-// Scale of a group whose largest magnitude is amax: fl32(amax / 448), at
-// least 2^-100, so that no group divides by zero and the residuals of
-// fp8_ratio stay normal numbers.
-__device__ __forceinline__ float fp8_scale(float amax) {
-  return fmaxf(__fdiv_rn(amax, 448.0f), 0x1p-100f);
+// Scale of a group whose largest magnitude has the fp32 bits amax: fl32(amax /
+// 448), at least 2^-100, so that no group divides by zero and the residuals of
+// fp8_ratio stay normal numbers; NaN for a group with an infinity or NaN, so
+// that every product with the group is NaN.
+__device__ __forceinline__ float fp8_scale(uint32_t amax) {
+  const float s = fmaxf(__fdiv_rn(__uint_as_float(amax), 448.0f), 0x1p-100f);
+  return amax < 0x7F800000u ? s : __builtin_nanf("");
 }
 
 // fl32(x / s) in the codes' range, inv = fl32(1 / s): one Newton step on
@@ -42,17 +44,33 @@ __device__ __forceinline__ void bf16x8_to_f32(const uint4& w, float (&v)[8]) {
   v[4] = bf16_lo(w.z), v[5] = bf16_hi(w.z), v[6] = bf16_lo(w.w), v[7] = bf16_hi(w.w);
 }
 
-__device__ __forceinline__ float absmax8(const float (&v)[8]) {
-  float m = 0.0f;
-#pragma unroll
-  for (int j = 0; j < 8; ++j) m = fmaxf(m, fabsf(v[j]));
-  return m;
+// Magnitudes are compared as integers: the bits of |x| are ordered as |x| is,
+// with infinities and NaN on top, where a maximum of floats drops a NaN.
+typedef unsigned short u16x2_t __attribute__((ext_vector_type(2)));
+
+// Two running maxima of bf16 magnitudes, of the even and the odd values.
+__device__ __forceinline__ u16x2_t absmax_pair(u16x2_t m, uint32_t pair) {
+  return __builtin_elementwise_max(m, __builtin_bit_cast(u16x2_t, pair & 0x7FFF7FFFu));
 }
 
-// Max over aligned runs of 16 lanes (every lane gets it).
-__device__ __forceinline__ float max16(float x) {
+__device__ __forceinline__ u16x2_t absmax_pair(u16x2_t m, const uint4& w) {
+  return absmax_pair(absmax_pair(absmax_pair(absmax_pair(m, w.x), w.y), w.z), w.w);
+}
+
+// The larger of the two, as fp32 bits.
+__device__ __forceinline__ uint32_t absmax_bits(u16x2_t m) {
+  return static_cast<uint32_t>(m[0] > m[1] ? m[0] : m[1]) << 16;
+}
+
+// Max over the lanes that differ in the bits from .. to of their number
+// (every lane gets it).
+template <int kFrom, int kTo>
+__device__ __forceinline__ uint32_t lanes_max(uint32_t x) {
 #pragma unroll
-  for (int off = 1; off <= 8; off <<= 1) x = fmaxf(x, __shfl_xor(x, off, 64));
+  for (int off = kFrom; off <= kTo; off <<= 1) {
+    const uint32_t y = static_cast<uint32_t>(__shfl_xor(static_cast<int>(x), off, 64));
+    x = x > y ? x : y;
+  }
   return x;
 }
 
@@ -81,18 +99,6 @@ __device__ __forceinline__ uint4 load_bf16x8(const uint16_t* p, int left, bool v
   for (int j = 0; j < 4; ++j) {
     const uint32_t lo = 2 * j < left ? p[2 * j] : 0u;
     const uint32_t hi = 2 * j + 1 < left ? p[2 * j + 1] : 0u;
-    w[j] = lo | hi << 16;
-  }
-  return make_uint4(w[0], w[1], w[2], w[3]);
-}
-
-// The same of 8 values a row pitch apart (a column of a row-major matrix).
-__device__ __forceinline__ uint4 load_bf16x8_strided(const uint16_t* p, int64_t pitch, int left) {
-  uint32_t w[4];
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const uint32_t lo = 2 * j < left ? p[(2 * j) * pitch] : 0u;
-    const uint32_t hi = 2 * j + 1 < left ? p[(2 * j + 1) * pitch] : 0u;
     w[j] = lo | hi << 16;
   }
   return make_uint4(w[0], w[1], w[2], w[3]);

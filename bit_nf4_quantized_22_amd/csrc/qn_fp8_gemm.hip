@@ -21,9 +21,10 @@
 // XOR-swizzled by the choice of each lane's source address, so that the
 // fragment reads hit all banks.  The loop holds no other vector-memory
 // instruction: one scale loaded to a register made the compiler wait for all
-// outstanding DMAs in every step (4096 x 22016 x 8192: 720 -> 656 us).  The backward's weight tile lies [n][k] in memory while a lane
-// needs 32 n of one k: it is read through the transposing LDS loads (8 rows
-// x 16 columns of bytes per 16 lanes).
+// outstanding DMAs in every step (4096 x 22016 x 8192: 720 -> 656 us).  The
+// backward's weight tile lies [n][k] in memory while a lane needs 32 n of one
+// k: it is read through the transposing LDS loads (8 rows x 16 columns of
+// bytes per 16 lanes).
 
 #include "qn_fp8.h"
 #include "qn_launch.h"
@@ -286,9 +287,10 @@ __device__ __forceinline__ void fp8_tile(const Fp8Args& g, uint8_t* smem, int64_
   // 16 (i - 1) are scaled and added.  Before the last i comes the turn: this
   // wave's reads of the buffer have returned and block b + 1 has landed, for
   // all waves after the barrier; from there on block b + 1's first fragments
-  // are read under the last MFMAs, and the DMAs of block b + kBuf go out, a share per i (a DMA takes the address unit 16 cycles, so all at
-  // once would hold the reads up; too late and the next turn waits for
-  // them).  Blocks past the end are the last one again: a branch would cut the
+  // are read under the last MFMAs, and the DMAs of block b + kBuf go out, a
+  // share per i (a DMA takes the address unit 16 cycles, so all at once would
+  // hold the reads up; too late and the next turn waits for them).  Blocks
+  // past the end are the last one again: a branch would cut the
   // step into pieces, and the last steps compiled apart without those DMAs
   // spilled registers (656 -> 745 us at 4096 x 22016 x 8192).
   if (nfull > 0) {
@@ -475,7 +477,7 @@ __device__ __forceinline__ void fp8_tile(const Fp8Args& g, uint8_t* smem, int64_
       reinterpret_cast<float*>(st + T::kWScales)[t] = g.ws[kBwd ? bt * kb + c : c * kb + bt];
     }
     __syncthreads();
-Ahead<T> f;
+    Ahead<T> f;
     read_ahead<T, kBwd>(st, wm, wn, li, lg, f);
 #pragma unroll
     for (int i = 0; i < T::kTI; ++i) {

@@ -126,7 +126,8 @@ __global__ __launch_bounds__(1024) void fp8_token_kernel(
 #pragma unroll
     for (int d = 0; d < kAhead; ++d) {
       const float x0 = bf16_lo(xp[d]), x1 = bf16_hi(xp[d]);
-      const float s = fp8_scale(wave_max(fmaxf(fabsf(x0), fabsf(x1))));
+      const float s =
+          fp8_scale(lanes_max<1, 32>(absmax_bits(absmax_pair(u16x2_t{0, 0}, xp[d]))));
       const float inv = __fdiv_rn(1.0f, s);
       if constexpr (kU == kOwnU) s_x[wave][d][lane] = xp[d];
       s_q[wave][d][lane] = static_cast<uint16_t>(__builtin_amdgcn_cvt_pk_fp8_f32(

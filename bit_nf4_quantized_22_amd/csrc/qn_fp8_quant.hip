@@ -3,8 +3,9 @@
 // values back.
 //
 // Per block: s = max(fl32(max |x| / 448), 2^-100), code = the E4M3 number
-// nearest to fl32(x / s), ties to even.  All three are one pass over the
-// data: a block's values stay in registers between its maximum and its codes.
+// nearest to fl32(x / s), ties to even; s = NaN for a block that is not all
+// finite.  All three are one pass over the data: a block's values stay in
+// registers between its maximum and its codes.
 
 #include "qn_fp8.h"
 #include "qn_launch.h"
@@ -15,14 +16,45 @@ namespace {
 
 constexpr int kT = 256;
 
-__device__ __forceinline__ void load8(const uint16_t* p, float (&v)[8]) {
-  bf16x8_to_f32(*reinterpret_cast<const uint4*>(p), v);
+// 8 values as they lie in memory; the bits of their largest magnitude; the
+// values as fp32.
+template <typename T>
+struct Raw8 {
+  uint4 w[sizeof(T) / 2] = {};
+};
+
+template <typename T>
+__device__ __forceinline__ void load8(const T* p, Raw8<T>& x) {
+#pragma unroll
+  for (int h = 0; h < static_cast<int>(sizeof(T) / 2); ++h)
+    x.w[h] = reinterpret_cast<const uint4*>(p)[h];
 }
 
-__device__ __forceinline__ void load8(const float* p, float (&v)[8]) {
-  const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
-  v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
-  v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+__device__ __forceinline__ uint32_t absmax8(const Raw8<uint16_t>& x) {
+  return absmax_bits(absmax_pair(u16x2_t{0, 0}, x.w[0]));
+}
+
+__device__ __forceinline__ uint32_t absmax8(const Raw8<float>& x) {
+  uint32_t m = 0;
+#pragma unroll
+  for (int h = 0; h < 2; ++h)
+    for (const uint32_t w : {x.w[h].x, x.w[h].y, x.w[h].z, x.w[h].w}) {
+      const uint32_t u = w & 0x7FFFFFFFu;
+      m = m > u ? m : u;
+    }
+  return m;
+}
+
+__device__ __forceinline__ void values8(const Raw8<uint16_t>& x, float (&v)[8]) {
+  bf16x8_to_f32(x.w[0], v);
+}
+
+__device__ __forceinline__ void values8(const Raw8<float>& x, float (&v)[8]) {
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    v[4 * h] = __uint_as_float(x.w[h].x), v[4 * h + 1] = __uint_as_float(x.w[h].y);
+    v[4 * h + 2] = __uint_as_float(x.w[h].z), v[4 * h + 3] = __uint_as_float(x.w[h].w);
+  }
 }
 
 // One workgroup per 128 x 128 block: 16 lanes span a row's 128 columns, the
@@ -31,38 +63,37 @@ template <typename T>
 __global__ __launch_bounds__(kT) void quantize_blocks_kernel(const T* __restrict__ w, int64_t N,
                                                              int64_t K, uint8_t* __restrict__ codes,
                                                              float* __restrict__ scale) {
-  __shared__ float s_max[kT / 64];
+  __shared__ uint32_t s_max[kT / 64];
   const int64_t kb = (K + 127) / 128;
   const int64_t bn = blockIdx.x / kb, bk = blockIdx.x % kb;
   const int t = threadIdx.x;
   const int64_t k = bk * 128 + (t & 15) * 8;
   const int64_t n0 = bn * 128 + (t >> 4);
   const bool kin = k < K;  // K is a multiple of 16: a run of 8 is in or out
-  float v[8][8];
-  float m = 0.0f;
+  Raw8<T> x[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    if (kin && n0 + 16 * i < N) load8(w + (n0 + 16 * i) * K + k, x[i]);
+  uint32_t m = 0;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    const int64_t n = n0 + 16 * i;
-    if (kin && n < N) {
-      load8(w + n * K + k, v[i]);
-    } else {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) v[i][j] = 0.0f;
-    }
+    const uint32_t mi = absmax8(x[i]);
+    m = m > mi ? m : mi;
   }
-#pragma unroll
-  for (int i = 0; i < 8; ++i) m = fmaxf(m, absmax8(v[i]));
-  m = wave_max(m);
+  m = lanes_max<1, 32>(m);
   if ((t & 63) == 0) s_max[t >> 6] = m;
   __syncthreads();
-  m = fmaxf(fmaxf(s_max[0], s_max[1]), fmaxf(s_max[2], s_max[3]));
+#pragma unroll
+  for (int i = 0; i < kT / 64; ++i) m = m > s_max[i] ? m : s_max[i];
   const float s = fp8_scale(m), inv = __fdiv_rn(1.0f, s);
   if (t == 0) scale[blockIdx.x] = s;
   if (!kin) return;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const int64_t n = n0 + 16 * i;
-    if (n < N) *reinterpret_cast<uint2*>(codes + n * K + k) = fp8_codes8(v[i], s, inv);
+    float v[8];
+    values8(x[i], v);
+    if (n < N) *reinterpret_cast<uint2*>(codes + n * K + k) = fp8_codes8(v, s, inv);
   }
 }
 
@@ -77,14 +108,11 @@ __global__ __launch_bounds__(kT) void quantize_rows_kernel(const uint16_t* __res
   const int64_t m = q / kb, b = q % kb;
   const int64_t k = b * 128 + (threadIdx.x & 15) * 8;
   const bool in = m < M && k < K;
+  Raw8<uint16_t> raw;
   float v[8];
-  if (in) {
-    load8(x + m * K + k, v);
-  } else {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = 0.0f;
-  }
-  const float s = fp8_scale(max16(absmax8(v))), inv = __fdiv_rn(1.0f, s);
+  if (in) load8(x + m * K + k, raw);
+  values8(raw, v);
+  const float s = fp8_scale(lanes_max<1, 8>(absmax8(raw))), inv = __fdiv_rn(1.0f, s);
   if (m < M && (threadIdx.x & 15) == 0) scale[b * M + m] = s;
   if (in) *reinterpret_cast<uint2*>(codes + m * K + k) = fp8_codes8(v, s, inv);
 }
@@ -177,23 +205,24 @@ __global__ __launch_bounds__(64 * kWaves) void quantize_project_kernel(
       load_x(b + 1);
       load_p(b + 1);
     }
-    float v[4][8], am = 0.0f;
+    float v[4][8];
+    u16x2_t am{0, 0};
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
       bf16x8_to_f32(cur[c], v[c]);
-      am = fmaxf(am, absmax8(v[c]));
+      am = absmax_pair(am, cur[c]);
     }
-    am = fmaxf(am, __shfl_xor(am, 16, 64));
-    am = fmaxf(am, __shfl_xor(am, 32, 64));
-    const float s = fp8_scale(am), inv = __fdiv_rn(1.0f, s);
+    const float s = fp8_scale(lanes_max<16, 32>(absmax_bits(am))), inv = __fdiv_rn(1.0f, s);
     if (row < M && lg == 0) scale[b * M + row] = s;
     // the codes leave as whole 128-byte rows, 8 of them per store (8 bytes of
-    // 16 rows per store took 40% longer for the whole kernel); the wave's own
-    // LDS order keeps the turns of sQ apart
+    // 16 rows per store took 40% longer for the whole kernel); sQ is the
+    // wave's own, so the order of its LDS accesses keeps the turns apart
     uint8_t* sq = sQ[t >> 6];
+    __builtin_amdgcn_wave_barrier();
 #pragma unroll
     for (int c = 0; c < 4; ++c)
       *reinterpret_cast<uint2*>(sq + li * kQPitch + 32 * c + 8 * lg) = fp8_codes8(v[c], s, inv);
+    __builtin_amdgcn_wave_barrier();
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       const int rr = 8 * h + (lane >> 3);
@@ -263,15 +292,14 @@ __global__ __launch_bounds__(kT) void decode_project_kernel(
       a[i][c] = load_bf16x8(A + j * L + k, j < r && k < L ? 8 : 0, vec_a);
     }
   }
-  float v[4][8], am = 0.0f;
+  float v[4][8];
+  u16x2_t am{0, 0};
 #pragma unroll
   for (int c = 0; c < 4; ++c) {
     bf16x8_to_f32(w[c], v[c]);
-    am = fmaxf(am, absmax8(v[c]));
+    am = absmax_pair(am, w[c]);
   }
-  am = fmaxf(am, __shfl_xor(am, 16, 64));
-  am = fmaxf(am, __shfl_xor(am, 32, 64));
-  const float s = fp8_scale(am), inv = __fdiv_rn(1.0f, s);
+  const float s = fp8_scale(lanes_max<16, 32>(absmax_bits(am))), inv = __fdiv_rn(1.0f, s);
   if (codes && li < M && b * 128 < L) {
     if (lg == 0) scale[b * M + li] = s;
 #pragma unroll

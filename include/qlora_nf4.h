@@ -476,8 +476,10 @@ typedef struct qn_fp8_weight {
  *   w      device, [N, K] of type dtype (QN_F32 or QN_BF16).
  *   codes  device uint8[N, K] out;  scale fp32[ceil(N/128), ceil(K/128)] out.
  * Per block: scale = max(fl32(max|w| / 448), 2^-100); code = the E4M3
- * number nearest to fl32(w / scale), ties to the even code.  N and K are
- * non-negative multiples of 16.  Results are bit-reproducible.
+ * number nearest to fl32(w / scale), ties to the even code.  A block with an
+ * infinity or NaN gets the scale NaN (its codes mean nothing), so that every
+ * product with it is NaN.  N and K are non-negative multiples of 16.  Results
+ * are bit-reproducible.  At most 2^24 - 1 blocks.
  */
 QN_API int fp8_quantize_blocks(const void* w, int32_t dtype, int64_t N, int64_t K, uint8_t* codes,
                                float* scale, void* stream);
@@ -485,7 +487,9 @@ QN_API int fp8_quantize_blocks(const void* w, int32_t dtype, int64_t N, int64_t 
 /*
  * fp8_quantize_rows -- the same of activations or gradients, one scale per
  * 128 columns of a row.
- *   x      device bf16[M, K], K a multiple of 16.
+ *   x      device bf16[M, K], K a multiple of 16; M <= 2^26 rows of M
+ *          ceil(K/128) <= 2^27 scales in all (QN_ERR_SHAPE; the same holds
+ *          for both sides of the products below).
  *   codes  device uint8[M, K] out.
  *   scale  device fp32[ceil(K/128), M] out: scale[b M + m] is that of row m,
  *          columns 128 b .. 128 b + 127 (the order the product reads).
@@ -495,7 +499,7 @@ QN_API int fp8_quantize_rows(const qn_bf16* x, int64_t M, int64_t K, uint8_t* co
 
 /*
  * fp8_dequant -- out[N, K] = the weight's values: fl32(code value * scale),
- * as QN_F32 or rounded (nearest even) to QN_BF16.
+ * as QN_F32 or rounded (nearest even) to QN_BF16.  N K <= 2^35.
  */
 QN_API int fp8_dequant(const qn_fp8_weight* w, int32_t out_dtype, void* out, void* stream);
 
@@ -526,8 +530,10 @@ QN_API int fp8_matmul(const qn_fp8_weight* w, const uint8_t* x, const float* xsc
  * overlapping any operand (dx likewise below).
  *   ws  device workspace of ws_bytes >= qn_workspace_bytes(QN_OP_FP8_FWD,..)
  *       (needed for r == 0 too: x's codes lie there).
- * A row of y is bit-reproducible for a given batch; batches of up to 16, up
- * to 64 and more tokens add the blocks up in orders of their own.
+ * A row of y is bit-reproducible for a given batch; one token, batches of up
+ * to 16, up to 64 and more tokens add the blocks up in orders of their own.
+ * A row of x with an infinity or NaN gives a row of NaN and touches no other
+ * (padding rows may hold anything).
  */
 QN_API int fp8_linear_fwd(const qn_fp8_weight* w, const qn_bf16* x, int64_t M, const qn_bf16* A,
                           const qn_bf16* B, int32_t r, float alpha, qn_bf16* y, qn_bf16* u_out,
@@ -561,6 +567,8 @@ QN_API int fp8_linear_bwd_dx(const qn_fp8_weight* w, const qn_bf16* dy, int64_t 
  *            Ignored (may be NULL) for QN_STATE_F32.
  *   p_bf16   bf16[n] out (the new p rounded to bf16), or NULL.
  *   n        >= 0; a matrix of 0 elements is skipped, its pointers not read.
+ *            The matrices of a table have less than 2^24 chunks of 2048
+ *            elements in all (QN_ERR_SHAPE).
  */
 typedef struct qn_adamw_tensor {
   float* p;
@@ -641,6 +649,8 @@ QN_API int lora_grad_norm(const qn_adamw_plan* plan, const void* table, float ma
  * the sum is cut.  Over the steps the codes' mean follows x, where
  * rounding to nearest would lose every change smaller than half a code.
  * The code of a v > 0 is at least 1.  Results are bit-reproducible.
+ * Without grad_scale, a NaN or infinite gradient makes p of its element NaN;
+ * with 8-bit states later steps may do so for its whole block.
  * `step` and the hyperparameters are host values: a captured graph repeats
  * the step that it was captured with.
  */

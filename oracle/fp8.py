@@ -39,7 +39,9 @@ def e4m3_codes(v):
 
 
 def group_scale(amax):
-    return np.maximum((amax.astype(np.float32) / np.float32(448)).astype(np.float32), FLOOR)
+    """NaN where a group has an infinity or NaN: its codes mean nothing."""
+    s = np.maximum((amax.astype(np.float32) / np.float32(448)).astype(np.float32), FLOOR)
+    return np.where(np.isfinite(amax), s, np.float32(np.nan)).astype(np.float32)
 
 
 def _codes(x, s):

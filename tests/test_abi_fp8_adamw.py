@@ -230,3 +230,24 @@ def test_binding_refuses_host_and_mistyped_tensors():
         qn.lora_adamw_table([w], [w], [w], [w])
     with pytest.raises(ValueError):
         qn.lora_adamw_table([w], [w.half()], [w], [w])
+
+
+def test_sizes_beyond_a_launch_are_refused(lib):  # noqa: F811
+    """A launch has less than 2^32 threads."""
+    row = lib.fp8_quantize_rows
+    assert row(FAKE, (1 << 26) + 1, 16, FAKE, FAKE, None) == qn.QN_ERR_SHAPE
+    assert row(FAKE, (1 << 24) + 1, 1024, FAKE, FAKE, None) == qn.QN_ERR_SHAPE
+    assert lib.fp8_quantize_blocks(FAKE, qn.QN_BF16, 1 << 19, 1 << 19, FAKE, FAKE,
+                                   None) == qn.QN_ERR_SHAPE
+    assert lib.fp8_dequant(fp8_w(N=1 << 18, K=(1 << 17) + 16), qn.QN_BF16, FAKE,
+                           None) == qn.QN_ERR_SHAPE
+    for f in (lib.fp8_linear_fwd, lib.fp8_linear_bwd_dx):
+        for N, K in ((1 << 16, 16), (16, 1 << 16)):
+            assert f(fp8_w(N=N, K=K), FAKE, (1 << 18) + 1, None, None, 0, 1.0, FAKE, None, FAKE,
+                     BIG, None) == qn.QN_ERR_SHAPE
+    n = 2048 * ((1 << 24) - 1)
+    big = (qn.qn_adamw_tensor * 1)(qn.qn_adamw_tensor(*one(n=n)))
+    assert lib.lora_adamw_table_bytes(big, 1) == 64 * ((1 << 24) - 1)
+    big[0].n = n + 1
+    assert lib.lora_adamw_table_bytes(big, 1) == 0
+    assert table([one(n=n + 1)])[0] == qn.QN_ERR_SHAPE

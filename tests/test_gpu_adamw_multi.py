@@ -354,3 +354,50 @@ def test_steps_on_another_stream():
     qn.lora_adamw_multi_step(tab, 3, grad_scale=norm[1:], stream=side, **HYPER)
     torch.cuda.synchronize()
     check(state, t, 8, 3)
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+@pytest.mark.parametrize("bits", [32, 8])
+def test_a_gradient_that_is_not_finite_without_clipping(bits, bad):
+    """p of its element is NaN, and nothing outside its block of 256 differs."""
+    state = make([3000], bits, 4, False, seed=6)
+    clean, t = upload(state, bits, False), upload(state, bits, False)
+    t[0]["g"][700] = bad
+    for e in (clean, t):
+        tab = table_of(e, bits)
+        qn.lora_adamw_multi_step(tab, 4, **HYPER)
+        qn.lora_adamw_multi_step(tab, 5, **HYPER)
+    torch.cuda.synchronize()
+    assert torch.isnan(t[0]["p"][700])
+    for k in ("p", "b", "m", "v"):
+        same = t[0][k].view(torch.uint8).view(3000, -1) == clean[0][k].view(torch.uint8).view(3000, -1)
+        same[512:768] = True
+        assert same.all(), k
+
+
+def test_offsets_past_32_bits():
+    """A matrix whose fp32 values take more than 2^32 bytes: its end steps as
+    a small matrix of the same values does."""
+    n, n0 = 2 ** 30 + 2125, 2 ** 30 - 2048
+    g = torch.Generator(device=DEV).manual_seed(1)
+    p = torch.randn(n, generator=g, device=DEV)
+    grad = torch.randn(n, generator=g, device=DEV).bfloat16()
+    blocks = -(-n // 256)
+    ms = torch.rand(blocks, generator=g, device=DEV) * 1e-4
+    vs = torch.rand(blocks, generator=g, device=DEV) * 1e-4
+    m = torch.randint(0, 0x7F, (n,), generator=g, device=DEV, dtype=torch.uint8)
+    v = torch.randint(0, 0x7C, (n,), generator=g, device=DEV, dtype=torch.uint8)
+    b = torch.empty(n, dtype=torch.bfloat16, device=DEV)
+    whole = [p, grad, m.view(torch.float8_e4m3fn), v.view(torch.float8_e5m2), ms, vs, b]
+    first = [n0 // 256 if i in (4, 5) else n0 for i in range(7)]
+    end = [t[a:].clone() for a, t in zip(first, whole)]
+    norms = []
+    for cols in (whole, end):
+        tab = qn.lora_adamw_table(*[[t] for t in cols])
+        norms.append(qn.lora_grad_norm(tab, 1e9))
+        qn.lora_adamw_multi_step(tab, 100, **HYPER)
+    torch.cuda.synchronize()
+    want = sum(float(grad[i:i + 2 ** 27].double().square().sum()) for i in range(0, n, 2 ** 27))
+    assert abs(norms[0][0].item() - want ** 0.5) <= 2.0 ** -23 * want ** 0.5
+    for a, t, e in zip(first, whole, end):
+        assert torch.equal(t[a:].view(torch.uint8), e.view(torch.uint8))

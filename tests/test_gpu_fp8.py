@@ -407,3 +407,155 @@ def test_tile_grids_on_some_rows(M, N):
     v, Af, Bf = f64(xb[rows]), f64(A), f64(B)
     qv = fp8.row_values(*fp8.quantize_rows(v.astype(np.float32)))
     check(f"fp8 y {M}x{N}x{K}", to_np(y)[rows], qv @ wv.T + 2.0 * (v @ Af.T) @ Bf.T)
+
+
+# every path: one token, few, some, small tiles (split and not), large tiles
+@pytest.mark.parametrize("M,N,K", [(1, 144, 272), (5, 144, 272), (40, 144, 1040), (100, 144, 272),
+                                   (80, 1040, 2064), (1100, 4096, 400)])
+@pytest.mark.parametrize("r", [0, 16])
+def test_a_row_that_is_not_finite_spoils_itself_alone(M, N, K, r):
+    rng = np.random.default_rng(M)
+    fw = qn.fp8_quantize_weight(torch.from_numpy(weights(N, K, 1)).to(DEV))
+    A, B = ((bf16_dev(bf16_of(rng.standard_normal(s) * 0.02)) for s in ((r, K), (N, r)))
+            if r else (None, None))
+    for f, L in ((qn.fp8_linear_fwd, K), (qn.fp8_linear_bwd_dx, N)):
+        x = bf16_dev(acts(M, L, 8))
+        good = f(fw, x, A, B, r, 16.0)
+        for row, col, v in ((0, 3, np.nan), (M // 2, L - 1, np.inf), (M - 1, 130, -np.inf)):
+            y = x.clone()
+            y[row, col] = v
+            got = f(fw, y, A, B, r, 16.0)
+            assert torch.isnan(got[row]).all()
+            got[row] = good[row]
+            assert torch.equal(got.view(torch.int16), good.view(torch.int16))
+
+
+def test_scales_of_groups_that_are_not_finite():
+    x = acts(6, 400, 3)
+    f = synth.bf16_to_f32(x)
+    f[1, 200], f[4, 399] = np.nan, np.inf
+    t = torch.from_numpy(f).to(DEV)
+    codes, scale = qn.fp8_quantize_rows(t.bfloat16())
+    rc, rs = fp8.quantize_rows(f)
+    assert np.isnan(rs).sum() == 2
+    assert np.array_equal(np.isnan(scale.cpu().numpy()), np.isnan(rs))
+    ok = ~np.isnan(rs)
+    assert np.array_equal(bits32(scale.cpu().numpy()[ok]), bits32(rs[ok]))
+    ok = np.repeat(ok.T, 128, axis=1)[:, :400]
+    assert np.array_equal(codes_np(codes)[ok], rc[ok])
+    w = np.zeros((16, 400), np.float32)
+    w[:6] = f
+    for m in (torch.from_numpy(w).to(DEV), torch.from_numpy(w).to(DEV).bfloat16()):
+        fw = qn.fp8_quantize_weight(m)
+        assert np.isnan(fw.scale.cpu().numpy()).tolist() == [[False, True, False, True]]
+        val = qn.fp8_dequant(fw, torch.float32)
+        assert torch.isnan(val[:, 128:256]).all() and torch.isnan(val[:, 384:]).all()
+        assert torch.isfinite(val[:, :128]).all() and torch.isfinite(val[:, 256:384]).all()
+
+
+@pytest.mark.parametrize("M", [1, 5, 40, 100])
+@pytest.mark.parametrize("r", [8, 16, 40])
+def test_adapters_at_any_element(M, r):
+    """A and B need no alignment beyond their elements'."""
+    N, K = 272, 528
+    rng = np.random.default_rng(r)
+    fw = qn.fp8_quantize_weight(torch.from_numpy(weights(N, K, 1)).to(DEV))
+    A, B = (bf16_dev(bf16_of(rng.standard_normal(s) * 0.02)) for s in ((r, K), (N, r)))
+
+    def moved(t):
+        out = torch.empty(t.numel() + 3, dtype=t.dtype, device=DEV)[3:].view(t.shape)
+        out.copy_(t)
+        assert out.data_ptr() % 4 == 2
+        return out
+
+    for f, L in ((qn.fp8_linear_fwd, K), (qn.fp8_linear_bwd_dx, N)):
+        x = bf16_dev(acts(M, L, 8))
+        low, low2 = (torch.empty(M * r + 1, dtype=torch.bfloat16, device=DEV)[1:].view(M, r)
+                     for _ in range(2))
+        a = f(fw, x, A, B, r, 16.0, None, low)
+        b = f(fw, x, moved(A), moved(B), r, 16.0, None, low2)
+        assert torch.equal(a.view(torch.int16), b.view(torch.int16))
+        assert torch.equal(low.view(torch.int16), low2.view(torch.int16))
+
+
+def random_weight(N, K, seed):
+    """Finite random codes and scales, made on the device."""
+    g = torch.Generator(device=DEV).manual_seed(seed)
+    c = torch.randint(0, 0x7F, (N, K), generator=g, device=DEV, dtype=torch.uint8)
+    c[:, ::2] |= 0x80
+    s = torch.rand((-(-N // 128), -(-K // 128)), generator=g, device=DEV) + 0.5
+    return qn.Fp8Weight(c.view(torch.float8_e4m3fn), s)
+
+
+def near(got, want):
+    """Equal block products, summed in fp32 in other orders and rounded to
+    bf16: 2^-8 of the value each, 2^-7 of the largest, and L / 128 steps of
+    2^-23 of the terms' magnitude, which is below 100 times the largest sum
+    here: less than 2^-9.  2^-6 holds both; a wrong address is off by the size
+    of the values."""
+    assert torch.isfinite(got.float()).all()
+    d = (got.float() - want.float()).abs().max()
+    assert d <= 2.0 ** -6 * want.float().abs().max()
+
+
+def test_offsets_past_32_bits_in_the_weight():
+    """A weight of more than 2^32 codes: its last columns (rows for the
+    backward) are those of a small weight of the same codes."""
+    N, K, n0 = 262160, 16400, 262016
+    fw = random_weight(N, K, 1)
+    assert fw.codes.numel() > 2 ** 32
+    end = qn.Fp8Weight(fw.codes[n0:], fw.scale[n0 // 128:])
+    for M in (1, 3, 40, 100):
+        x = bf16_dev(acts(M, K, M))
+        near(qn.fp8_linear_fwd(fw, x, None, None, 0, 1.0)[:, n0:],
+             qn.fp8_linear_fwd(end, x, None, None, 0, 1.0))
+    for M in (3, 300):
+        dy = torch.zeros((M, N), dtype=torch.bfloat16, device=DEV)
+        dy[:, n0:] = bf16_dev(acts(M, N - n0, M))
+        near(qn.fp8_linear_bwd_dx(fw, dy, None, None, 0, 1.0),
+             qn.fp8_linear_bwd_dx(end, dy[:, n0:].contiguous(), None, None, 0, 1.0))
+    val = qn.fp8_dequant(fw)
+    assert torch.equal(val[n0:].view(torch.int16), qn.fp8_dequant(end).view(torch.int16))
+    c, s = qn.fp8_quantize_blocks(val)
+    c1, s1 = qn.fp8_quantize_blocks(val[n0:].contiguous())
+    assert torch.equal(s[n0 // 128:], s1)
+    assert torch.equal(c[n0:].view(torch.uint8), c1.view(torch.uint8))
+
+
+def test_offsets_past_32_bits_in_the_batch():
+    """More than 2^32 values of x, and of y."""
+    M, L, m0 = 262160, 16400, 262100
+    g = torch.Generator(device=DEV).manual_seed(2)
+    x = torch.randint(-200, 200, (M, L), generator=g, device=DEV, dtype=torch.int16).bfloat16()
+    assert x.numel() > 2 ** 32
+    last = x[m0:].contiguous()
+    fw = random_weight(144, L, 3)
+    A = bf16_dev(bf16_of(np.random.default_rng(1).standard_normal((16, L)) * 0.02))
+    B = bf16_dev(bf16_of(np.random.default_rng(2).standard_normal((144, 16))))
+    near(qn.fp8_linear_fwd(fw, x, A, B, 16, 16.0)[m0:],
+         qn.fp8_linear_fwd(fw, last, A, B, 16, 16.0))
+    wide = random_weight(L, 144, 4)
+    dy = x[:, :144].contiguous()
+    near(qn.fp8_linear_fwd(wide, dy, None, None, 0, 1.0)[m0:],
+         qn.fp8_linear_fwd(wide, dy[m0:].contiguous(), None, None, 0, 1.0))
+
+
+def test_tensors_made_by_a_call_belong_to_its_stream():
+    """A call on another stream than the current one, with nothing passed in:
+    its workspace and output must not be memory that the current stream's
+    work still uses or gets next."""
+    M, N, K, r = 200, 1040, 2064, 24
+    rng = np.random.default_rng(11)
+    fw = qn.fp8_quantize_weight(torch.from_numpy(weights(N, K, 2)).to(DEV))
+    A, B = (bf16_dev(bf16_of(rng.standard_normal(s) * 0.02)) for s in ((r, K), (N, r)))
+    x = bf16_dev(acts(M, K, 9))
+    want = qn.fp8_linear_fwd(fw, x, A, B, r, 16.0)
+    need = qn.qn_workspace_bytes(qn.QN_OP_FP8_FWD, M, N, K, r)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(20):
+        got = qn.fp8_linear_fwd(fw, x, A, B, r, 16.0, stream=side)
+        torch.full((need,), 255, dtype=torch.uint8, device=DEV)
+        torch.full((M, N), 3.0, dtype=torch.bfloat16, device=DEV)
+        torch.cuda.synchronize()
+        assert torch.equal(got.view(torch.int16), want.view(torch.int16))

@@ -69,3 +69,13 @@ def test_smallest_positive_v_keeps_code_one():
     v[0], v[1] = 1.0, 1e-30
     c, _ = optim8.encode_v(v, 5)
     assert c[1] == 1 and c[2] == 0
+
+
+def test_a_group_that_is_not_finite_has_no_scale():
+    x = np.ones((3, 300), np.float32)
+    x[0, 130], x[1, 0], x[2, 299] = np.nan, -np.inf, np.inf
+    _, s = fp8.quantize_rows(x)
+    bad = np.zeros((3, 3), bool)
+    bad[1, 0] = bad[0, 1] = bad[2, 2] = True
+    assert np.array_equal(np.isnan(s), bad)
+    assert np.isnan(fp8.quantize_blocks(x)[1]).all()
