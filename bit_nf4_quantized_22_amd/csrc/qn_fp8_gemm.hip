@@ -8,9 +8,8 @@
 // 16x16x128 FP8 MFMA per 16 x 16 outputs; its fp32 result is multiplied by
 // the block's two scales and added to the fp32 accumulator with one fused
 // multiply-add per output, so no scale is ever rounded to fewer bits.  The
-// LoRA term follows on the same accumulators: 64 ranks of bf16 are a block of
-// 128 bytes too, brought in by the same DMAs under the last block's MFMAs and
-// multiplied by bf16 MFMAs.
+// LoRA term comes first on the same accumulators: 64 ranks of bf16 are a block
+// of 128 bytes too, laid out like one and multiplied by bf16 MFMAs.
 //
 // Tiles.  A wave holds kWTM x 64 outputs, which lie in one 128-block of the
 // weight, so the weight's scale is wave-uniform; the MFMAs take the weight as
@@ -208,6 +207,201 @@ __device__ __forceinline__ void add_pending(const Pending<T>& p, int j, f32x4_t&
   for (int e = 0; e < 4; ++e) acc[e] = fmaf(p.c[j][e], p.f, acc[e]);
 }
 
+// LoRA term, 64 ranks at a time: the tokens' side (padded rows of 128 bytes)
+// by DMA, the adapter's from where it lies, through registers: rows of B as
+// the codes' rows, or A's 64 rows of kBN columns, which the transposing LDS
+// loads read.
+template <typename T>
+struct LoraRows {
+  uint4 v[T::kBN * 8 / T::kThreads];
+};
+
+template <typename T, bool kBwd>
+__device__ __forceinline__ void lora_load(const Fp8Args& g, int lb, int64_t m0, int64_t c0,
+                                          uint8_t* st, LoraRows<T>& w) {
+  const int t = threadIdx.x, lane = t & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
+  const uint16_t* pa = g.act + m0 * g.pitch + lb * 64;
+#pragma unroll
+  for (int d = 0; d < T::kDmaA; ++d) {
+    const int row = 8 * (wave * T::kDmaA + d) + (lane >> 3);
+    const int64_t at = m0 + row < g.M ? row : g.M - 1 - m0;
+    dma16(static_cast<uint32_t>(at * g.pitch * 2 + ((lane & 7) ^ row_swz(row)) * 16), pa,
+          lds_addr(st) + (wave * T::kDmaA + d) * 1024);
+  }
+#pragma unroll
+  for (int q = 0; q < static_cast<int>(sizeof(w.v) / 16); ++q) {
+    const int e = q * T::kThreads + t;
+    const uint16_t* src;
+    bool in;
+    int left;
+    if constexpr (kBwd) {
+      const int64_t c = c0 + e % (T::kBN / 8) * 8;
+      const int j = lb * 64 + e / (T::kBN / 8);
+      in = j < g.r;
+      left = 8;
+      src = g.lw + (in ? j : 0) * g.K + (c < g.K ? c : g.K - 8);
+    } else {
+      const int64_t n = c0 + (e >> 3);
+      const int j = lb * 64 + (e & 7) * 8;
+      in = j < g.r;
+      left = in ? g.r - j : 8;
+      src = g.lw + (n < g.N ? n : g.N - 1) * g.r + (in ? j : 0);
+    }
+    if (g.vec_w) {
+      w.v[q] = *reinterpret_cast<const uint4*>(src);
+      if (!in) w.v[q] = make_uint4(0, 0, 0, 0);
+    } else {
+      w.v[q] = load_bf16x8(src, in ? left : 0, false);
+    }
+  }
+}
+
+template <typename T, bool kBwd>
+__device__ __forceinline__ void lora_store(uint8_t* st, const LoraRows<T>& w) {
+#pragma unroll
+  for (int q = 0; q < static_cast<int>(sizeof(w.v) / 16); ++q) {
+    const int e = q * T::kThreads + static_cast<int>(threadIdx.x);
+    uint8_t* dst = st + T::kA;
+    if constexpr (kBwd) {
+      const int j = e / (T::kBN / 8), c = e % (T::kBN / 8);
+      dst += j * (T::kBN * 2) + (((c >> 1) ^ lora_swz(j)) << 5) + (c & 1) * 16;
+    } else {
+      dst += (e >> 3) * 128 + ((e & 7) ^ row_swz(e >> 3)) * 16;
+    }
+    *reinterpret_cast<uint4*>(dst) = w.v[q];
+  }
+}
+
+template <typename T, bool kBwd>
+__device__ __forceinline__ void lora_add(const Fp8Args& g, int lb, const uint8_t* st,
+                                         f32x4_t (&acc)[T::kTI][T::kTJ]) {
+  const int lane = threadIdx.x & 63, li = lane & 15, lg = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wm = wave / T::kGN, wn = wave % T::kGN;
+#pragma unroll 1
+  for (int kk = 0; kk < 2 && lb * 64 + kk * 32 < g.r; ++kk) {
+    const int at = ((4 * kk + lg) ^ row_swz(li)) * 16;
+    uint4 b[T::kTJ];
+#pragma unroll
+    for (int j = 0; j < T::kTJ; ++j) {
+      if constexpr (kBwd) {
+        // lane 4 a + e of a group points at rank row a, columns 4 e .. + 3
+        uint2 h[2];
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          const int row = 32 * kk + 8 * lg + 4 * q + (li >> 2);
+          const i16x4_t d = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+              (lds_i16x4_t*)(lds_u8_t*)(st + T::kA + row * (T::kBN * 2) +
+                                        (((wn * 4 + j) ^ lora_swz(row)) << 5) + (li & 3) * 8));
+          h[q] = __builtin_bit_cast(uint2, d);
+        }
+        b[j] = make_uint4(h[0].x, h[0].y, h[1].x, h[1].y);
+      } else {
+        b[j] = *reinterpret_cast<const uint4*>(st + T::kA + (wn * 64 + j * 16 + li) * 128 + at);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < T::kTI; ++i) {
+      const uint4 a = *reinterpret_cast<const uint4*>(st + (wm * T::kWTM + i * 16 + li) * 128 + at);
+#pragma unroll
+      for (int j = 0; j < T::kTJ; ++j) acc[i][j] = mfma_bf16_32(b[j], a, acc[i][j]);
+    }
+  }
+}
+
+// The contraction's last, partial block: through registers, zeros behind its
+// end.
+template <typename T>
+struct TailRows {
+  uint4 a[T::kBM * 8 / T::kThreads], b[T::kBN * 8 / T::kThreads];
+  float s, ws;
+};
+
+template <typename T, bool kBwd>
+__device__ __forceinline__ void tail_load(const Fp8Args& g, int tail, int64_t m0, int64_t c0,
+                                          int64_t bt, TailRows<T>& w) {
+  const int t = threadIdx.x;
+  const int64_t ncols = kBwd ? g.K : g.N, L = kBwd ? g.N : g.K;
+  const int64_t kb = (g.K + 127) / 128, cmax = (ncols - 1) / 128, l0 = bt * 128;
+  auto row_chunk = [&](const uint8_t* src, int64_t row0, int64_t rows, int q) {
+    const int c = q & 7;
+    const int64_t row = row0 + (q >> 3);
+    uint4 v = make_uint4(0, 0, 0, 0);
+    if (c * 16 < tail)
+      v = *reinterpret_cast<const uint4*>(src + (row < rows ? row : rows - 1) * L + l0 + c * 16);
+    return v;
+  };
+#pragma unroll
+  for (int q = 0; q < static_cast<int>(sizeof(w.a) / 16); ++q)
+    w.a[q] = row_chunk(g.x, m0, g.M, q * T::kThreads + t);
+#pragma unroll
+  for (int q = 0; q < static_cast<int>(sizeof(w.b) / 16); ++q) {
+    const int e = q * T::kThreads + t;
+    if constexpr (kBwd) {
+      constexpr int kSlots = T::kBN / 16;
+      const int row = e / kSlots;
+      const int64_t col = c0 + e % kSlots * 16;
+      w.b[q] = make_uint4(0, 0, 0, 0);
+      if (row < tail)
+        w.b[q] = *reinterpret_cast<const uint4*>(g.w + (l0 + row) * g.K +
+                                                 (col < g.K ? col : g.K - 16));
+    } else {
+      w.b[q] = row_chunk(g.w, c0, g.N, e);
+    }
+  }
+  static_assert(T::kThreads >= T::kBM, "a thread per token's scale");
+  const int64_t m = m0 + t < g.M ? m0 + t : g.M - 1;
+  const int64_t cb = c0 / 128 + (t & 3), c = cb < cmax ? cb : cmax;
+  w.s = g.xs[bt * g.M + m];
+  w.ws = g.ws[kBwd ? bt * kb + c : c * kb + bt];
+}
+
+template <typename T, bool kBwd>
+__device__ __forceinline__ void tail_store(uint8_t* st, const TailRows<T>& w) {
+  const int t = threadIdx.x;
+#pragma unroll
+  for (int q = 0; q < static_cast<int>(sizeof(w.a) / 16); ++q) {
+    const int e = q * T::kThreads + t, row = e >> 3;
+    *reinterpret_cast<uint4*>(st + row * 128 + ((e & 7) ^ row_swz(row)) * 16) = w.a[q];
+  }
+#pragma unroll
+  for (int q = 0; q < static_cast<int>(sizeof(w.b) / 16); ++q) {
+    const int e = q * T::kThreads + t;
+    if constexpr (kBwd) {
+      constexpr int kSlots = T::kBN / 16;
+      const int row = e / kSlots, c = e % kSlots;
+      *reinterpret_cast<uint4*>(st + T::kA + row * T::kBN + (c ^ col_swz<T::kBN>(row)) * 16) =
+          w.b[q];
+    } else {
+      const int row = e >> 3;
+      *reinterpret_cast<uint4*>(st + T::kA + row * 128 + ((e & 7) ^ row_swz(row)) * 16) = w.b[q];
+    }
+  }
+  if (t < T::kBM) reinterpret_cast<float*>(st + T::kScales)[t] = w.s;
+  if (t < 4) reinterpret_cast<float*>(st + T::kWScales)[t] = w.ws;
+}
+
+template <typename T, bool kBwd>
+__device__ __forceinline__ void tail_add(const uint8_t* st, f32x4_t (&acc)[T::kTI][T::kTJ]) {
+  const int lane = threadIdx.x & 63, li = lane & 15, lg = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wm = wave / T::kGN, wn = wave % T::kGN;
+  Ahead<T> f;
+  read_ahead<T, kBwd>(st, wm, wn, li, lg, f);
+#pragma unroll
+  for (int i = 0; i < T::kTI; ++i) {
+    if (i > 0) f.a[0] = token_frag<T>(st, wm, i, li, lg);
+#pragma unroll
+    for (int j = 0; j < T::kTJ; ++j) {
+      const f32x4_t c = mfma_fp8(f.b[j], f.a[0], f32x4_t{0.f, 0.f, 0.f, 0.f});
+#pragma unroll
+      for (int e = 0; e < 4; ++e) acc[i][j][e] = fmaf(c[e], f.s[i] * f.sw, acc[i][j][e]);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+  }
+}
+
 // One output tile: rows from m0, columns from c0, the contraction's blocks
 // from b0, nfull whole ones and a tail of `tail` values behind them; the LoRA
 // term is added where first is set.
@@ -282,6 +476,44 @@ __device__ __forceinline__ void fp8_tile(const Fp8Args& g, uint8_t* smem, int64_
 #pragma unroll
     for (int j = 0; j < T::kTJ; ++j) acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
 
+  // Before the blocks, with the first block's DMAs in flight: the LoRA term
+  // and the tail, whose own memory latency passes meanwhile (behind the last
+  // block it was exposed: PREFIG).
+  constexpr int kShares = (kDma + T::kShare - 1) / T::kShare;
+  const int last = nfull - 1;
+  auto upto = [&](int b) { return b < last ? b : last; };
+  auto issue_all = [&](int b) {
+#pragma unroll
+    for (int q = 0; q < kShares; ++q) issue(upto(b), b, q);
+  };
+  if (nfull > 0) issue_all(0);
+  const int rank = first ? g.r : 0;
+  if (rank > 0 || tail) {
+    uint8_t* stL = smem + (T::kBuf - 1) * T::kStage;
+    uint8_t* stT = smem + (T::kBuf > 2 ? T::kBuf - 2 : 1) * T::kStage;
+    LoraRows<T> lw;
+    TailRows<T> tr;
+    if (rank > 0) lora_load<T, kBwd>(g, 0, m0, c0, stL, lw);
+    if (tail) tail_load<T, kBwd>(g, tail, m0, c0, b0 + nfull, tr);
+    for (int lb = 0; lb * 64 < rank; ++lb) {
+      if (lb > 0) {
+        __syncthreads();
+        lora_load<T, kBwd>(g, lb, m0, c0, stL, lw);
+      }
+      lora_store<T, kBwd>(stL, lw);
+      asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+      __syncthreads();
+      lora_add<T, kBwd>(g, lb, stL, acc);
+    }
+    if (tail) {
+      if (T::kBuf == 2) __syncthreads();
+      tail_store<T, kBwd>(stT, tr);
+      __syncthreads();
+      tail_add<T, kBwd>(stT, acc);
+    }
+    __syncthreads();
+  }
+
   // Step b multiplies block b (buffer b % kBuf).  Its MFMAs of tokens 16 i run
   // while the fragment of tokens 16 (i + 1) is read and the results of tokens
   // 16 (i - 1) are scaled and added.  Before the last i comes the turn: this
@@ -294,15 +526,10 @@ __device__ __forceinline__ void fp8_tile(const Fp8Args& g, uint8_t* smem, int64_
   // step into pieces, and the last steps compiled apart without those DMAs
   // spilled registers (656 -> 745 us at 4096 x 22016 x 8192).
   if (nfull > 0) {
-    constexpr int kShares = (kDma + T::kShare - 1) / T::kShare;
     constexpr int kEnd = T::kTI - 1;
     static_assert(kShares < T::kTI, "the DMAs of a block go out before the next turn");
-    const int last = nfull - 1;
-    auto upto = [&](int b) { return b < last ? b : last; };
 #pragma unroll
-    for (int b = 0; b < T::kBuf - 1; ++b)
-#pragma unroll
-      for (int q = 0; q < kShares; ++q) issue(upto(b), b, q);
+    for (int b = 1; b < T::kBuf - 1; ++b) issue_all(b);
     // all DMAs but those of the kBuf - 2 youngest blocks have landed
     asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"((T::kBuf - 2) * (kDma + 1)) : "memory");
     issue(upto(T::kBuf - 1), T::kBuf - 1, 0);
@@ -351,145 +578,6 @@ __device__ __forceinline__ void fp8_tile(const Fp8Args& g, uint8_t* smem, int64_
 #pragma unroll
     for (int j = 0; j < T::kTJ; ++j) add_pending<T>(p, j, acc[kEnd][j]);
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-    __syncthreads();
-  }
-
-  // LoRA term, 64 ranks at a time in the two buffers in turn: the tokens' side
-  // (padded rows of 128 bytes) by DMA, the adapter's from where it lies,
-  // through registers: rows of B as the codes' rows, or A's 64 rows of kBN
-  // columns, which the transposing LDS loads read.
-  for (int lb = 0; first && lb * 64 < g.r; ++lb) {
-    uint8_t* st = smem + (lb & 1) * T::kStage;
-    const uint16_t* pa = g.act + m0 * g.pitch + lb * 64;
-#pragma unroll
-    for (int d = 0; d < T::kDmaA; ++d) {
-      const int row = 8 * (wave * T::kDmaA + d) + (lane >> 3);
-      const int64_t at = m0 + row < g.M ? row : g.M - 1 - m0;
-      dma16(static_cast<uint32_t>(at * g.pitch * 2 + ((lane & 7) ^ row_swz(row)) * 16), pa,
-            lds_addr(st) + (wave * T::kDmaA + d) * 1024);
-    }
-    constexpr int kPer = T::kBN * 8 / T::kThreads;  // 16-byte chunks per thread
-    uint4 v[kPer];
-#pragma unroll
-    for (int q = 0; q < kPer; ++q) {
-      const int e = q * T::kThreads + t;
-      const uint16_t* src;
-      bool in;
-      int left;
-      if constexpr (kBwd) {
-        const int64_t c = c0 + e % (T::kBN / 8) * 8;
-        const int j = lb * 64 + e / (T::kBN / 8);
-        in = j < g.r;
-        left = 8;
-        src = g.lw + (in ? j : 0) * g.K + (c < g.K ? c : g.K - 8);
-      } else {
-        const int64_t n = c0 + (e >> 3);
-        const int j = lb * 64 + (e & 7) * 8;
-        in = j < g.r;
-        left = in ? g.r - j : 8;
-        src = g.lw + (n < g.N ? n : g.N - 1) * g.r + (in ? j : 0);
-      }
-      if (g.vec_w) {
-        v[q] = *reinterpret_cast<const uint4*>(src);
-        if (!in) v[q] = make_uint4(0, 0, 0, 0);
-      } else {
-        v[q] = load_bf16x8(src, in ? left : 0, false);
-      }
-    }
-#pragma unroll
-    for (int q = 0; q < kPer; ++q) {
-      const int e = q * T::kThreads + t;
-      uint8_t* dst = st + T::kA;
-      if constexpr (kBwd) {
-        const int j = e / (T::kBN / 8), c = e % (T::kBN / 8);
-        dst += j * (T::kBN * 2) + (((c >> 1) ^ lora_swz(j)) << 5) + (c & 1) * 16;
-      } else {
-        dst += (e >> 3) * 128 + ((e & 7) ^ row_swz(e >> 3)) * 16;
-      }
-      *reinterpret_cast<uint4*>(dst) = v[q];
-    }
-    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-    __syncthreads();
-#pragma unroll 1
-    for (int kk = 0; kk < 2 && lb * 64 + kk * 32 < g.r; ++kk) {
-      const int at = ((4 * kk + lg) ^ row_swz(li)) * 16;
-      uint4 b[T::kTJ];
-#pragma unroll
-      for (int j = 0; j < T::kTJ; ++j) {
-        if constexpr (kBwd) {
-          // lane 4 a + e of a group points at rank row a, columns 4 e .. + 3
-          uint2 h[2];
-#pragma unroll
-          for (int q = 0; q < 2; ++q) {
-            const int row = 32 * kk + 8 * lg + 4 * q + (li >> 2);
-            const i16x4_t d = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                (lds_i16x4_t*)(lds_u8_t*)(st + T::kA + row * (T::kBN * 2) +
-                                          (((wn * 4 + j) ^ lora_swz(row)) << 5) + (li & 3) * 8));
-            h[q] = __builtin_bit_cast(uint2, d);
-          }
-          b[j] = make_uint4(h[0].x, h[0].y, h[1].x, h[1].y);
-        } else {
-          b[j] = *reinterpret_cast<const uint4*>(st + T::kA + (wn * 64 + j * 16 + li) * 128 + at);
-        }
-      }
-#pragma unroll
-      for (int i = 0; i < T::kTI; ++i) {
-        const uint4 a =
-            *reinterpret_cast<const uint4*>(st + (wm * T::kWTM + i * 16 + li) * 128 + at);
-#pragma unroll
-        for (int j = 0; j < T::kTJ; ++j) acc[i][j] = mfma_bf16_32(b[j], a, acc[i][j]);
-      }
-    }
-  }
-  __syncthreads();
-  if (tail) {
-    // the last, partial block: through registers, zeros behind its end
-    uint8_t* st = smem + (nfull & 1) * T::kStage;
-    const int64_t bt = b0 + nfull, l0 = bt * 128;
-    auto row_tile = [&](uint8_t* dst, const uint8_t* src, int64_t row0, int64_t rows, int count) {
-      for (int q = t; q < count * 8; q += T::kThreads) {
-        const int row = q >> 3, c = q & 7;
-        const int64_t at = row0 + row < rows ? row0 + row : rows - 1;
-        uint4 v = make_uint4(0, 0, 0, 0);
-        if (c * 16 < tail) v = *reinterpret_cast<const uint4*>(src + at * L + l0 + c * 16);
-        *reinterpret_cast<uint4*>(dst + row * 128 + (c ^ row_swz(row)) * 16) = v;
-      }
-    };
-    row_tile(st, g.x, m0, g.M, T::kBM);
-    if constexpr (kBwd) {
-      constexpr int kSlots = T::kBN / 16;
-      for (int q = t; q < 128 * kSlots; q += T::kThreads) {
-        const int row = q / kSlots, c = q % kSlots;
-        const int64_t col = c0 + c * 16 < g.K ? c0 + c * 16 : g.K - 16;
-        uint4 v = make_uint4(0, 0, 0, 0);
-        if (row < tail) v = *reinterpret_cast<const uint4*>(g.w + (l0 + row) * g.K + col);
-        *reinterpret_cast<uint4*>(st + T::kA + row * T::kBN +
-                                  (c ^ col_swz<T::kBN>(row)) * 16) = v;
-      }
-    } else {
-      row_tile(st + T::kA, g.w, c0, g.N, T::kBN);
-    }
-    float* sS = reinterpret_cast<float*>(st + T::kScales);
-    for (int q = t; q < T::kBM; q += T::kThreads)
-      sS[q] = g.xs[bt * g.M + (m0 + q < g.M ? m0 + q : g.M - 1)];
-    if (t < 4) {
-      const int64_t c = c0 / 128 + t < cmax ? c0 / 128 + t : cmax;
-      reinterpret_cast<float*>(st + T::kWScales)[t] = g.ws[kBwd ? bt * kb + c : c * kb + bt];
-    }
-    __syncthreads();
-    Ahead<T> f;
-    read_ahead<T, kBwd>(st, wm, wn, li, lg, f);
-#pragma unroll
-    for (int i = 0; i < T::kTI; ++i) {
-      if (i > 0) f.a[0] = token_frag<T>(st, wm, i, li, lg);
-#pragma unroll
-      for (int j = 0; j < T::kTJ; ++j) {
-        const f32x4_t c = mfma_fp8(f.b[j], f.a[0], f32x4_t{0.f, 0.f, 0.f, 0.f});
-#pragma unroll
-        for (int e = 0; e < 4; ++e) acc[i][j][e] = fmaf(c[e], f.s[i] * f.sw, acc[i][j][e]);
-      }
-      __builtin_amdgcn_sched_barrier(0);
-    }
   }
 
   if (g.part) {
@@ -508,24 +596,25 @@ __device__ __forceinline__ void fp8_tile(const Fp8Args& g, uint8_t* smem, int64_
   // and stores whole 128-byte row segments.
   __syncthreads();
   constexpr int kPitch = 64 + 8;
-  uint16_t* stg = reinterpret_cast<uint16_t*>(smem) + wave * 64 * kPitch;
-  static_assert(T::kWaves * 64 * kPitch * 2 <= 2 * T::kStage, "staging fits");
+  constexpr int kTurn = T::kWTM < 64 ? T::kWTM : 64;  // tokens of a turn
+  uint16_t* stg = reinterpret_cast<uint16_t*>(smem) + wave * kTurn * kPitch;
+  static_assert(T::kWaves * kTurn * kPitch * 2 <= 2 * T::kStage, "staging fits");
 #pragma unroll
-  for (int h = 0; h < T::kWTM / 64; ++h) {
+  for (int h = 0; h < T::kWTM / kTurn; ++h) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < kTurn / 16; ++i)
 #pragma unroll
       for (int j = 0; j < T::kTJ; ++j) {
-        const f32x4_t& c = acc[4 * h + i][j];
+        const f32x4_t& c = acc[kTurn / 16 * h + i][j];
         *reinterpret_cast<uint2*>(stg + (i * 16 + li) * kPitch + j * 16 + 4 * lg) =
             make_uint2(pack_bf16x2(c[0], c[1]), pack_bf16x2(c[2], c[3]));
       }
     __syncthreads();
 #pragma unroll
-    for (int s = 0; s < 8; ++s) {
+    for (int s = 0; s < kTurn / 8; ++s) {
       const int row = s * 8 + (lane >> 3), ch = lane & 7;
       const uint4 v = *reinterpret_cast<const uint4*>(stg + row * kPitch + ch * 8);
-      const int64_t m = m0 + wm * T::kWTM + h * 64 + row;
+      const int64_t m = m0 + wm * T::kWTM + h * kTurn + row;
       const int64_t n = c0 + wn * 64 + ch * 8;
       if (m < g.M && n < ncols) *reinterpret_cast<uint4*>(g.out + m * ncols + n) = v;
     }
@@ -535,7 +624,7 @@ __device__ __forceinline__ void fp8_tile(const Fp8Args& g, uint8_t* smem, int64_
 
 using Big = Tile<128, 2, 4, 2>;    // 256 x 256, 8 waves
 using Half = Tile<64, 2, 4, 3>;    // 128 x 256, 8 waves
-using Small = Tile<64, 2, 2, 2>;   // 128 x 128, 4 waves, two workgroups per CU
+using Small = Tile<32, 4, 2, 3>;   // 128 x 128, 8 waves
 constexpr int kMixedLds = Big::kBuf * Big::kStage > Half::kBuf * Half::kStage
                               ? Big::kBuf * Big::kStage
                               : Half::kBuf * Half::kStage;
@@ -573,7 +662,7 @@ __global__ __launch_bounds__(Big::kThreads, 2) void fp8_gemm_kernel(Fp8Args g, i
 // Workgroup row z takes the blocks z per .. of the contraction; the last one
 // has the tail too.
 template <bool kBwd>
-__global__ __launch_bounds__(Small::kThreads, 2) void fp8_gemm_small_kernel(Fp8Args g, int per) {
+__global__ __launch_bounds__(Small::kThreads) void fp8_gemm_small_kernel(Fp8Args g, int per) {
   __shared__ __attribute__((aligned(1024))) uint8_t smem[Small::kBuf * Small::kStage];
   const int nc = static_cast<int>(((kBwd ? g.K : g.N) + Small::kBN - 1) / Small::kBN);
   const int nr = static_cast<int>((g.M + Small::kBM - 1) / Small::kBM);
@@ -588,21 +677,21 @@ __global__ __launch_bounds__(Small::kThreads, 2) void fp8_gemm_small_kernel(Fp8A
                         static_cast<int>(blockIdx.y));
 }
 
-// Large tiles for this many outputs?
-bool large(int64_t M, int64_t ncols) {
-  return ((ncols + Big::kBN - 1) / Big::kBN) * ((M + Big::kBM - 1) / Big::kBM) >= 64;
+int64_t small_tiles(int64_t M, int64_t ncols) {
+  return ((ncols + Small::kBN - 1) / Small::kBN) * ((M + Small::kBM - 1) / Small::kBM);
 }
+
+// Large tiles where the small ones would take more than one round of the CUs.
+bool large(int64_t M, int64_t ncols) { return small_tiles(M, ncols) > 256; }
 
 }  // namespace
 
 int fp8_gemm_splits(int64_t M, int64_t ncols, int64_t L) {
   if (M <= 0 || large(M, ncols)) return 1;
-  const int64_t tiles = ((ncols + Small::kBN - 1) / Small::kBN) *
-                        ((M + Small::kBM - 1) / Small::kBM);
   // one workgroup per CU, at least 8 blocks each: adding the parts up costs a
   // launch (333 x 1088 x 2112 backward, 8 blocks: whole 10.8 us, in two 14.8;
   // 128 x 11008 x 4096, 86 blocks: whole 68 us, in eight 21)
-  int64_t s = 256 / tiles;
+  int64_t s = 256 / small_tiles(M, ncols);
   const int64_t most = L / 128 / 8;
   s = s < most ? s : most;
   if (s < 2) return 1;
@@ -637,9 +726,7 @@ hipError_t launch_fp8_gemm(const Fp8View& w, const uint8_t* x, const float* xs, 
   const int splits = part ? fp8_gemm_splits(M, ncols, L) : 1;
   const int per = static_cast<int>((L / 128 + splits - 1) / splits);
   if (splits > 1) g.part = part;
-  const dim3 grid(static_cast<uint32_t>(((ncols + Small::kBN - 1) / Small::kBN) *
-                                        ((M + Small::kBM - 1) / Small::kBM)),
-                  static_cast<uint32_t>(splits));
+  const dim3 grid(static_cast<uint32_t>(small_tiles(M, ncols)), static_cast<uint32_t>(splits));
   if (bwd)
     hipLaunchKernelGGL(fp8_gemm_small_kernel<true>, grid, dim3(Small::kThreads), 0, st, g, per);
   else
