@@ -478,7 +478,7 @@ __device__ __forceinline__ void fp8_tile(const Fp8Args& g, uint8_t* smem, int64_
 
   // Before the blocks, with the first block's DMAs in flight: the LoRA term
   // and the tail, whose own memory latency passes meanwhile (behind the last
-  // block it was exposed: PREFIG).
+  // block it was exposed: 3000 x 5008 x 2000 with r = 16 53 -> 51 us).
   constexpr int kShares = (kDma + T::kShare - 1) / T::kShare;
   const int last = nfull - 1;
   auto upto = [&](int b) { return b < last ? b : last; };
@@ -624,7 +624,11 @@ __device__ __forceinline__ void fp8_tile(const Fp8Args& g, uint8_t* smem, int64_
 
 using Big = Tile<128, 2, 4, 2>;    // 256 x 256, 8 waves
 using Half = Tile<64, 2, 4, 3>;    // 128 x 256, 8 waves
-using Small = Tile<32, 4, 2, 3>;   // 128 x 128, 8 waves
+// 128 x 128, 8 waves: grids of at most one workgroup per CU are bound by the
+// latency of a step, which a second wave per SIMD and a third buffer hide
+// (333 x 1088 x 2112: 13.7 us; with 4 waves 16.8, with two buffers 15.4, with
+// four 14.2; a 32 x 64 wave tile reads LDS 1.5 times as often as 64 x 64).
+using Small = Tile<32, 4, 2, 3>;
 constexpr int kMixedLds = Big::kBuf * Big::kStage > Half::kBuf * Half::kStage
                               ? Big::kBuf * Big::kStage
                               : Half::kBuf * Half::kStage;
@@ -681,7 +685,8 @@ int64_t small_tiles(int64_t M, int64_t ncols) {
   return ((ncols + Small::kBN - 1) / Small::kBN) * ((M + Small::kBM - 1) / Small::kBM);
 }
 
-// Large tiles where the small ones would take more than one round of the CUs.
+// Large tiles where the small ones would take more than one round of the CUs
+// (256 small tiles, 1000 x 4096 x 4096 with r = 16: small 33 us, large 40).
 bool large(int64_t M, int64_t ncols) { return small_tiles(M, ncols) > 256; }
 
 }  // namespace
@@ -689,8 +694,8 @@ bool large(int64_t M, int64_t ncols) { return small_tiles(M, ncols) > 256; }
 int fp8_gemm_splits(int64_t M, int64_t ncols, int64_t L) {
   if (M <= 0 || large(M, ncols)) return 1;
   // one workgroup per CU, at least 8 blocks each: adding the parts up costs a
-  // launch (333 x 1088 x 2112 backward, 8 blocks: whole 10.8 us, in two 14.8;
-  // 128 x 11008 x 4096, 86 blocks: whole 68 us, in eight 21)
+  // launch (backward of 333 x 1088 x 2112, 8 blocks: whole 9.9 us, in two
+  // 12.9; of 128 x 11008 x 4096, 86 blocks: whole 48 us, in eight 21)
   int64_t s = 256 / small_tiles(M, ncols);
   const int64_t most = L / 128 / 8;
   s = s < most ? s : most;
