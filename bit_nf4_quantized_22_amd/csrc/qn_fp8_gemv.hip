@@ -60,13 +60,13 @@ __device__ __forceinline__ void store_columns(uint16_t* y, f32x4_t acc) {
 // or `slices` partial sums of it.
 enum TokenU { kNoAdapter, kOwnU, kGivenU };
 
-template <int kU>
-__global__ __launch_bounds__(1024) void fp8_token_kernel(
+template <int kU, int kWaves>
+__global__ __launch_bounds__(64 * kWaves) void fp8_token_kernel(
     const uint8_t* __restrict__ w, const float* __restrict__ ws, int64_t N, int64_t K,
     const uint16_t* __restrict__ x, const uint16_t* __restrict__ A, bool vec_a,
     const float* __restrict__ part, int slices, const uint16_t* __restrict__ B, int r, bool vec_b,
     float lora_scale, uint16_t* __restrict__ y, uint16_t* __restrict__ u_out) {
-  constexpr int kWaves = 16, kThreads = 64 * kWaves, kAhead = 2;
+  constexpr int kThreads = 64 * kWaves, kAhead = 2;
   constexpr int kFrags = kU == kGivenU ? kMaxRank / 32 : 1;
   __shared__ f32x4_t s_acc[kWaves][4];
   __shared__ float s_u[kU == kNoAdapter ? 1 : kThreads];  // kOwnU: [wave][16 ranks]
@@ -325,7 +325,7 @@ __global__ __launch_bounds__(64 * kWaves) void fp8_decode_kernel(
 bool fp8_token_self_u(const Fp8View& w, int r) {
   // A is read by every workgroup, from the caches: past about 40 MB in all a
   // projection launch of its own costs less (one token, r = 16: 4096 x 4096,
-  // 34 MB, 9.1 us against 10.9; 11008 x 4096, 90 MB, 23.6 against 18.3)
+  // 34 MB, 9.2 us against 10.9; 6000 x 4096, 49 MB, 14.8 against 11.7)
   return r <= 16 && w.N / 16 * r * w.K * 2 <= (int64_t{40} << 20);
 }
 
@@ -335,14 +335,20 @@ hipError_t launch_fp8_token(const Fp8View& w, const uint16_t* x, const uint16_t*
   const dim3 grid(static_cast<uint32_t>(w.N / 16));
   const bool vec_a = (reinterpret_cast<uintptr_t>(A) & 15) == 0;
   const bool vec_b = (r & 7) == 0 && (reinterpret_cast<uintptr_t>(B) & 15) == 0;
-  auto go = [&](auto k) {
-    hipLaunchKernelGGL(k, grid, dim3(1024), 0, st, w.codes, w.scale, w.N, w.K, x, A, vec_a, part,
+  auto go = [&](auto k, int waves) {
+    hipLaunchKernelGGL(k, grid, dim3(64 * waves), 0, st, w.codes, w.scale, w.N, w.K, x, A, vec_a, part,
                        slices, B, r, vec_b, lora_scale, y, u_out);
     return hipGetLastError();
   };
-  return r == 0   ? go(fp8_token_kernel<kNoAdapter>)
-         : part   ? go(fp8_token_kernel<kGivenU>)
-                  : go(fp8_token_kernel<kOwnU>);
+  // 16 waves where one workgroup per CU has the whole weight and for the form
+  // with the fewest registers, else 8, of which more fit on a CU at once
+  // (one token, 8 and 16 waves: r = 0 4096 x 4096 6.6 and 5.8 us; r = 16
+  // 5008 x 2000 7.3 and 9.4, 11008 x 4096 15.6 and 17.0; r = 64 4096 x 4096
+  // 11.0 and 10.4)
+  return r == 0 ? go(fp8_token_kernel<kNoAdapter, 16>, 16)
+         : !part        ? go(fp8_token_kernel<kOwnU, 8>, 8)
+         : grid.x > 256 ? go(fp8_token_kernel<kGivenU, 8>, 8)
+                        : go(fp8_token_kernel<kGivenU, 16>, 16);
 }
 
 hipError_t launch_fp8_decode(const Fp8View& w, const uint8_t* x, const float* xs, int M,
@@ -358,13 +364,9 @@ hipError_t launch_fp8_decode(const Fp8View& w, const uint8_t* x, const float* xs
                        slices, act, fp8_lora_pitch(r), B, r, vec_b, lora_scale, y, u_out);
     return hipGetLastError();
   };
-  // few columns: all 16 waves on one workgroup per CU; many: smaller
-  // workgroups, so that all of them run at once
-  if (M <= 16)
-    return kb <= 8        ? go(fp8_decode_kernel<4, 1>, 4)
-           : grid.x > 512 ? go(fp8_decode_kernel<8, 1>, 8)
-                          : go(fp8_decode_kernel<16, 1>, 16);
-  // more tokens need the registers of 8 waves
+  // 8 waves: 16 leave room for one workgroup per CU only (5 tokens, 5008 x
+  // 2000: 9.9 us against 13.8; 16 tokens, 4096 x 11008: the same)
+  if (M <= 16) return kb <= 8 ? go(fp8_decode_kernel<4, 1>, 4) : go(fp8_decode_kernel<8, 1>, 8);
   if (M <= 32) return kb <= 8 ? go(fp8_decode_kernel<4, 2>, 4) : go(fp8_decode_kernel<8, 2>, 8);
   return kb <= 8 ? go(fp8_decode_kernel<4, 4>, 4) : go(fp8_decode_kernel<8, 4>, 8);
 }
