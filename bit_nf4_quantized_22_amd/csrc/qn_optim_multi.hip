@@ -88,6 +88,10 @@ __device__ __forceinline__ float state_scale(float most, float top) {
   return fmaxf(__fdiv_rn(most, top), 0x1p-100f);
 }
 
+// Bound by HBM: 160 M elements, 32-bit states, 30 bytes each, in 892 us (5.4
+// TB/s); 40 M, 8-bit states, 18 bytes each, in 113-139 us (5.2-6.4 TB/s, part
+// of it from the cache); one 7B layer's 1.25 M with 32-bit states in 9.0 us.
+// Chunks of 1024 or 4096 elements and nontemporal accesses were slower.
 template <bool kState8, bool kBf16Grad>
 __global__ __launch_bounds__(kThreads) void adamw_multi_kernel(
     const AdamChunk* __restrict__ tab, const float* __restrict__ grad_scale, MultiArgs a) {
@@ -261,7 +265,8 @@ __device__ __forceinline__ double block_sum64(double x) {
 
 // Squares summed in fp64 (the vector unit's fp64 rate is far above what the
 // reads of g need, and no gradient's square overflows): workgroup b takes
-// chunks b, b + gridDim.x, ..., a fixed order.
+// chunks b, b + gridDim.x, ..., a fixed order.  1024 workgroups, four chunks in
+// flight each: 160 M gradients in 115 us (5.6 TB/s), 40 M in 31.
 template <bool kBf16Grad>
 __global__ __launch_bounds__(kThreads) void grad_sq_kernel(const AdamChunk* __restrict__ tab,
                                                            int64_t chunks,
