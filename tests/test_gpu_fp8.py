@@ -559,3 +559,32 @@ def test_tensors_made_by_a_call_belong_to_its_stream():
         torch.full((M, N), 3.0, dtype=torch.bfloat16, device=DEV)
         torch.cuda.synchronize()
         assert torch.equal(got.view(torch.int16), want.view(torch.int16))
+
+
+# large tiles: two blocks of ranks, with and without a partial last block, and
+# contractions of nothing but a partial block; r = 0 beside them
+@pytest.mark.parametrize("M,N,K,r", [(1100, 4096, 400, 128), (1100, 4096, 512, 72),
+                                     (2100, 8000, 48, 100), (2100, 48, 8000, 66),
+                                     (2100, 8000, 96, 0), (4200, 256, 4096, 128)])
+def test_large_tiles_with_many_ranks_and_short_contractions(M, N, K, r):
+    w = weights(N, K, M)
+    rng = np.random.default_rng(N + r)
+    xb, dyb = acts(M, K, 3), acts(M, N, 4, 1e-3)
+    A, B = (bf16_of(rng.standard_normal(sh) * 0.02) for sh in ((r, K), (N, r)))
+    a, b = (bf16_dev(A), bf16_dev(B)) if r else (None, None)
+    fw = qn.fp8_quantize_weight(torch.from_numpy(w).to(DEV))
+    wv = fp8.weight_values(*fp8.quantize_blocks(w))
+    s = 16.0 / r if r else 0.0
+    Af, Bf = f64(A), f64(B)
+    rows = np.unique(np.concatenate([np.arange(0, M, 211), [127, 128, 255, 256, M - 1]]))
+    for f, bits, ww, P, Q, L in ((qn.fp8_linear_fwd, xb, wv.T, Af, Bf, K),
+                                 (qn.fp8_linear_bwd_dx, dyb, wv, Bf.T, Af.T, N)):
+        out = torch.full((M + 1, ww.shape[1]), 7.0, dtype=torch.bfloat16, device=DEV)
+        f(fw, bf16_dev(bits), a, b, r, 16.0, out[:M])
+        torch.cuda.synchronize()
+        assert torch.all(out[M] == 7.0)
+        v = f64(bits[rows])
+        qv = fp8.row_values(*fp8.quantize_rows(v.astype(np.float32)))
+        ref = qv @ ww + (s * (v @ P.T) @ Q.T if r else 0.0)
+        bound = layer_bound(ref, qv, ww, v, P if r else None, Q, s, L)
+        assert rel_to_bound(to_np(out)[rows], ref, bound) <= 1
