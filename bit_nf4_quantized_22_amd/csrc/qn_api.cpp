@@ -293,7 +293,7 @@ Fp8Ws fp8_ws(bool bwd, int64_t M, int64_t N, int64_t K, int32_t r) {
   if (r > 0 && (bwd || M > qn::kFp8DecodeM))
     f.split += round_up(m * static_cast<size_t>(qn::fp8_lora_pitch(r)) * 2, 256);
   f.total = f.split;
-  const int splits = bwd || M > qn::kFp8FewM ? qn::fp8_gemm_splits(M, cols, L) : 1;
+  const int splits = bwd || !qn::fp8_few(M, N, K) ? qn::fp8_gemm_splits(M, cols, L) : 1;
   if (splits > 1)
     f.total += m * static_cast<size_t>(cols) * 4 * static_cast<size_t>(splits);
   return f;
@@ -336,7 +336,7 @@ int fp8_linear(bool bwd, const qn_fp8_weight* w, const qn_bf16* in, int64_t M, c
     return hip_status(qn::launch_fp8_token(v, in, A, own_u ? nullptr : part,
                                            qn::fp8_decode_slices(L), B, r, ls, out, low, s));
   }
-  const bool decode = !bwd && M <= qn::kFp8DecodeM, few = !bwd && M <= qn::kFp8FewM;
+  const bool decode = !bwd && M <= qn::kFp8DecodeM, few = !bwd && qn::fp8_few(M, v.N, v.K);
   const int m32 = static_cast<int>(few ? M : 0);
   hipError_t e = r == 0   ? qn::launch_fp8_quantize_rows(in, M, L, codes, scale, s)
                  : decode ? qn::launch_fp8_decode_project(in, m32, L, A, r, codes, scale, part, s)
@@ -708,7 +708,7 @@ int fp8_matmul(const qn_fp8_weight* w, const uint8_t* x, const float* xscale, in
       f.total > f.split ? reinterpret_cast<float*>(static_cast<char*>(ws) + f.split) : nullptr;
   (void)hipGetLastError();
   hipStream_t s = as_stream(stream);
-  if (!transposed && M <= qn::kFp8FewM)
+  if (!transposed && qn::fp8_few(M, v.N, v.K))
     return hip_status(qn::launch_fp8_decode(v, x, xscale, static_cast<int>(M), nullptr, 0, nullptr,
                                             nullptr, 0, 0.0f, out, nullptr, s));
   return hip_status(

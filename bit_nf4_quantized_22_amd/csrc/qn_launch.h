@@ -146,10 +146,11 @@ int fp8_project_slices(int64_t M, int64_t L);
 hipError_t launch_fp8_quantize_project(const uint16_t* x, int64_t M, int64_t L, const uint16_t* P,
                                        int r, bool rows_l, uint8_t* codes, float* scale,
                                        float* part, hipStream_t st);
-// y [M, N] = x W^T + (lora_scale u) B^T for M <= kFp8FewM tokens, u given as
+// y [M, N] = x W^T + (lora_scale u) B^T for fp8_few(..) tokens, u given as
 // slices partial sums [slices][M][r] (M <= kFp8DecodeM; bf16(u) to u_out if
 // not null) or as act (see launch_fp8_project_sum).
 constexpr int kFp8DecodeM = 16, kFp8FewM = 64;
+bool fp8_few(int64_t M, int64_t N, int64_t K);
 hipError_t launch_fp8_decode(const Fp8View& w, const uint8_t* x, const float* xs, int M,
                              const float* part, int slices, const uint16_t* act,
                              const uint16_t* B, int r, float lora_scale, uint16_t* y,

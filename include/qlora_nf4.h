@@ -530,8 +530,8 @@ QN_API int fp8_matmul(const qn_fp8_weight* w, const uint8_t* x, const float* xsc
  * overlapping any operand (dx likewise below).
  *   ws  device workspace of ws_bytes >= qn_workspace_bytes(QN_OP_FP8_FWD,..)
  *       (needed for r == 0 too: x's codes lie there).
- * A row of y is bit-reproducible for a given batch; one token, batches of up
- * to 16, up to 64 and more tokens add the blocks up in orders of their own.
+ * A row of y is bit-reproducible for a given batch; batches of other sizes may
+ * add the blocks up in another order.
  * A row of x with an infinity or NaN gives a row of NaN and touches no other
  * (padding rows may hold anything).
  */

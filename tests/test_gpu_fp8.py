@@ -588,3 +588,29 @@ def test_large_tiles_with_many_ranks_and_short_contractions(M, N, K, r):
         ref = qv @ ww + (s * (v @ P.T) @ Q.T if r else 0.0)
         bound = layer_bound(ref, qv, ww, v, P if r else None, Q, s, L)
         assert rel_to_bound(to_np(out)[rows], ref, bound) <= 1
+
+
+@pytest.mark.parametrize("M,N,K", [(64, 4096, 4096), (64, 4112, 4096), (33, 5600, 4000),
+                                   (17, 8192, 4112), (17, 8192, 4096)])
+def test_batches_at_the_border_between_few_and_tiles(M, N, K):
+    """Sizes on both sides of the rule that picks the kernel of 17 to 64
+    tokens, with a workspace of the asked size and a guard behind it."""
+    r = 16
+    w = weights(N, K, M)
+    rng = np.random.default_rng(N)
+    xb = acts(M, K, 3)
+    A, B = (bf16_of(rng.standard_normal(sh) * 0.02) for sh in ((r, K), (N, r)))
+    fw = qn.fp8_quantize_weight(torch.from_numpy(w).to(DEV))
+    wv = fp8.weight_values(*fp8.quantize_blocks(w))
+    xf, Af, Bf = f64(xb), f64(A), f64(B)
+    need = qn.qn_workspace_bytes(qn.QN_OP_FP8_FWD, M, N, K, r)
+    buf = torch.full((need + 4096,), 85, dtype=torch.uint8, device=DEV)
+    y = qn.fp8_linear_fwd(fw, bf16_dev(xb), bf16_dev(A), bf16_dev(B), r, 16.0, ws=buf[:need])
+    torch.cuda.synchronize()
+    assert (buf[need:] == 85).all()
+    xv = fp8.row_values(*fp8.quantize_rows(xf.astype(np.float32)))
+    check(f"fp8 y {M}x{N}x{K} r={r}", to_np(y), xv @ wv.T + (xf @ Af.T) @ Bf.T)
+    c = np.unique(np.concatenate([np.arange(0, N, 61), np.arange(N - 16, N)]))
+    ref = xv @ wv[c].T + (xf @ Af.T) @ Bf[c].T
+    bound = layer_bound(ref, xv, wv[c].T, xf, Af, Bf[c], 1.0, K)
+    assert rel_to_bound(to_np(y)[:, c], ref, bound) <= 1
