@@ -2,8 +2,10 @@
 //
 //   y[m, n] = sum_b xs[b, m] ws[n / 128, b] (xq_b[m] . wq_b[n]) + (s u) B^T
 //
-// Bound by reading the weight once (N K bytes).  A workgroup owns 16 output
-// columns and the whole contraction: its waves take the blocks of 128 in
+// Bound by reading the weight once (N K bytes), and past one token by x's
+// codes, which every workgroup reads from the L2s (16 tokens' are as many bytes
+// as the workgroup's weight).  A workgroup owns 16 output columns (or 32, see
+// the launch) and the whole contraction: its waves take the blocks of 128 in
 // turn, each block one 16x16x128 FP8 MFMA with the weight's rows as the first
 // operand and 16 tokens (the last one again past the end) as the second.
 // Every lane loads 32 consecutive bytes of its row straight into its
@@ -187,7 +189,7 @@ __global__ __launch_bounds__(64 * kWaves) void fp8_token_kernel(
 
 // Up to 16 kMT tokens, codes and scales of x given; u as `slices` partial
 // sums (kMT == 1), or act = bf16(s u) in rows of `pitch` values.
-template <int kWaves, int kMT>
+template <int kWaves, int kMT, int kRows>
 __global__ __launch_bounds__(64 * kWaves) void fp8_decode_kernel(
     const uint8_t* __restrict__ w, const float* __restrict__ ws, int64_t N, int64_t K,
     const uint8_t* __restrict__ x, const float* __restrict__ xs, int M,
@@ -196,28 +198,35 @@ __global__ __launch_bounds__(64 * kWaves) void fp8_decode_kernel(
     uint16_t* __restrict__ u_out) {
   constexpr int kThreads = 64 * kWaves;
   constexpr int kAhead = kMT <= 2 ? 2 : 1;  // blocks in flight besides the one multiplied
-  static_assert(kMT <= kWaves, "a wave finishes 16 tokens");
-  __shared__ f32x4_t s_acc[kWaves][kMT][64];
+  constexpr int kTiles = kMT * kRows;
+  static_assert(kTiles <= kWaves, "a wave finishes 16 columns of 16 tokens");
+  __shared__ f32x4_t s_acc[kWaves][kTiles][64];
   __shared__ float s_u[kMT == 1 ? kFp8DecodeM * kMaxRank : 1];
   __shared__ __attribute__((aligned(16))) uint16_t s_us[kMT == 1 ? 16 * kMaxRank : 8];
   const int t = threadIdx.x, lane = t & 63;
   const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
   const int li = lane & 15, lg = lane >> 4;
-  const int64_t n0 = static_cast<int64_t>(blockIdx.x) * 16;  // N is a multiple of 16
+  const int64_t n0 = static_cast<int64_t>(blockIdx.x) * (16 * kRows);
   const int64_t kb = (K + 127) / 128;
-  const uint8_t* wr = w + (n0 + li) * K;
+  // N is a multiple of 16: the last workgroup may have fewer rows of 16, and
+  // reads its last ones again
+  const uint8_t* wr[kRows];
+#pragma unroll
+  for (int q = 0; q < kRows; ++q)
+    wr[q] = w + ((n0 + 16 * q < N ? n0 + 16 * q : N - 16) + li) * K;
   const float* wsr = ws + (n0 / 128) * kb;
   int m[kMT];
 #pragma unroll
   for (int i = 0; i < kMT; ++i) m[i] = 16 * i + li < M ? 16 * i + li : M - 1;
 
   struct Block {
-    Bytes32 w, x[kMT];
+    Bytes32 w[kRows], x[kMT];
     float sw, sx[kMT];
   };
   auto load = [&](int64_t b, Block& d) {
     const bool in = b < kb;
-    d.w = row_bytes(wr, in ? b : kb, K, lg);
+#pragma unroll
+    for (int q = 0; q < kRows; ++q) d.w[q] = row_bytes(wr[q], in ? b : kb, K, lg);
     d.sw = in ? wsr[b] : 0.0f;
 #pragma unroll
     for (int i = 0; i < kMT; ++i) {
@@ -243,13 +252,16 @@ __global__ __launch_bounds__(64 * kWaves) void fp8_decode_kernel(
   Block blk[kAhead + 1];
 #pragma unroll
   for (int d = 0; d <= kAhead; ++d) load(wave + d * kWaves, blk[d]);
+  // wave 0 .. kTiles - 1 finishes token tile wave % kMT, row tile wave / kMT
+  const int64_t nw = n0 + 16 * (wave / kMT);
+  const bool finish = wave < kTiles && nw < N;
   uint4 bf[kMaxRank / 32];
-  if (wave < kMT) {
+  if (finish) {
 #pragma unroll
     for (int q = 0; q < kMaxRank / 32; ++q) {
       bf[q] = make_uint4(0, 0, 0, 0);
       if (32 * q < r)
-        bf[q] = load_bf16x8(B + (n0 + li) * r + 32 * q + 8 * lg, r - 32 * q - 8 * lg, vec_b);
+        bf[q] = load_bf16x8(B + (nw + li) * r + 32 * q + 8 * lg, r - 32 * q - 8 * lg, vec_b);
     }
   }
   if (kMT == 1 && r > 0) {
@@ -261,18 +273,18 @@ __global__ __launch_bounds__(64 * kWaves) void fp8_decode_kernel(
     if (t < par * mr) s_u[t] = s;
   }
 
-  f32x4_t acc[kMT];
+  f32x4_t acc[kTiles];
 #pragma unroll
-  for (int i = 0; i < kMT; ++i) acc[i] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+  for (int i = 0; i < kTiles; ++i) acc[i] = f32x4_t{0.f, 0.f, 0.f, 0.f};
   for (int64_t b = wave; b < kb; b += (kAhead + 1) * kWaves) {
 #pragma unroll
     for (int d = 0; d <= kAhead; ++d) {
-      const i32x8_t wf = frag8(blk[d].w.lo, blk[d].w.hi);
 #pragma unroll
-      for (int i = 0; i < kMT; ++i) {
-        const f32x4_t c = mfma_fp8(wf, frag8(blk[d].x[i].lo, blk[d].x[i].hi),
-                                   f32x4_t{0.f, 0.f, 0.f, 0.f});
-        const float s = blk[d].sx[i] * blk[d].sw;
+      for (int i = 0; i < kTiles; ++i) {
+        const Bytes32 &wv = blk[d].w[i / kMT], &xv = blk[d].x[i % kMT];
+        const f32x4_t c =
+            mfma_fp8(frag8(wv.lo, wv.hi), frag8(xv.lo, xv.hi), f32x4_t{0.f, 0.f, 0.f, 0.f});
+        const float s = blk[d].sx[i % kMT] * blk[d].sw;
 #pragma unroll
         for (int e = 0; e < 4; ++e) acc[i][e] = fmaf(c[e], s, acc[i][e]);
       }
@@ -280,7 +292,7 @@ __global__ __launch_bounds__(64 * kWaves) void fp8_decode_kernel(
     }
   }
 #pragma unroll
-  for (int i = 0; i < kMT; ++i) s_acc[wave][i][lane] = acc[i];
+  for (int i = 0; i < kTiles; ++i) s_acc[wave][i][lane] = acc[i];
   if constexpr (kMT == 1) {
     if (r > 0) {
       // the slices past the early ones, and the values past the first kThreads
@@ -307,11 +319,11 @@ __global__ __launch_bounds__(64 * kWaves) void fp8_decode_kernel(
     }
   }
   __syncthreads();
-  if (wave >= kMT) return;
+  if (!finish) return;
   f32x4_t sum = s_acc[0][wave][lane];
 #pragma unroll
   for (int q = 1; q < kWaves; ++q) sum += s_acc[q][wave][lane];
-  const int row = 16 * wave + li;
+  const int row = 16 * (wave % kMT) + li;
   if (r > 0) {
     if constexpr (kMT == 1)
       sum = lora_up(sum, bf, s_us, (r + 31) & ~31, r, li, lg);
@@ -319,8 +331,8 @@ __global__ __launch_bounds__(64 * kWaves) void fp8_decode_kernel(
       sum = lora_up(sum, bf, act + static_cast<int64_t>(row < M ? row - li : M - 1 - li) * pitch,
                     pitch, r, li, lg);
   }
-  // lane (li, lg): columns n0 + 4 lg .. + 3 of token 16 wave + li
-  if (row < M) store_columns(y + row * N + n0 + 4 * lg, sum);
+  // lane (li, lg): columns nw + 4 lg .. + 3 of its token
+  if (row < M) store_columns(y + row * N + nw + 4 * lg, sum);
 }
 
 }  // namespace
@@ -370,19 +382,31 @@ hipError_t launch_fp8_decode(const Fp8View& w, const uint8_t* x, const float* xs
                              const uint16_t* B, int r, float lora_scale, uint16_t* y,
                              uint16_t* u_out, hipStream_t st) {
   if (M == 0) return hipSuccess;
-  const dim3 grid(static_cast<uint32_t>(w.N / 16));
   const bool vec_b = (r & 7) == 0 && (reinterpret_cast<uintptr_t>(B) & 15) == 0;
   const int64_t kb = (w.K + 127) / 128;
-  auto go = [&](auto k, int waves) {
+  auto go = [&](auto k, int waves, int rows) {
+    const dim3 grid(static_cast<uint32_t>((w.N + 16 * rows - 1) / (16 * rows)));
     hipLaunchKernelGGL(k, grid, dim3(64 * waves), 0, st, w.codes, w.scale, w.N, w.K, x, xs, M, part,
                        slices, act, fp8_lora_pitch(r), B, r, vec_b, lora_scale, y, u_out);
     return hipGetLastError();
   };
   // 8 waves: 16 leave room for one workgroup per CU only (5 tokens, 5008 x
   // 2000: 9.9 us against 13.8; 16 tokens, 4096 x 11008: the same)
-  if (M <= 16) return kb <= 8 ? go(fp8_decode_kernel<4, 1>, 4) : go(fp8_decode_kernel<8, 1>, 8);
-  if (M <= 32) return kb <= 8 ? go(fp8_decode_kernel<4, 2>, 4) : go(fp8_decode_kernel<8, 2>, 8);
-  return kb <= 8 ? go(fp8_decode_kernel<4, 4>, 4) : go(fp8_decode_kernel<8, 4>, 8);
+  // Two row tiles share x's codes, but only one such workgroup fits on a CU:
+  // where they are one round of the CUs and more than half of one (r = 16:
+  // 16 x 8192 x 8192 27.1 -> 23.9 us, 20 x 5008 x 2000 14.5 -> 12.0; outside,
+  // 16 x 4096 x 11008 19.7 -> 24.4, 16 x 11008 x 4096 21.3 -> 22.7).
+  const int64_t pairs = (w.N + 31) / 32;
+  const bool two = pairs > 128 && pairs <= 256 && kb > 8;
+  if (M <= 16)
+    return two       ? go(fp8_decode_kernel<8, 1, 2>, 8, 2)
+           : kb <= 8 ? go(fp8_decode_kernel<4, 1, 1>, 4, 1)
+                     : go(fp8_decode_kernel<8, 1, 1>, 8, 1);
+  if (M <= 32)
+    return two       ? go(fp8_decode_kernel<8, 2, 2>, 8, 2)
+           : kb <= 8 ? go(fp8_decode_kernel<4, 2, 1>, 4, 1)
+                     : go(fp8_decode_kernel<8, 2, 1>, 8, 1);
+  return kb <= 8 ? go(fp8_decode_kernel<4, 4, 1>, 4, 1) : go(fp8_decode_kernel<8, 4, 1>, 8, 1);
 }
 
 }  // namespace qn

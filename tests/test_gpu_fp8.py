@@ -614,3 +614,34 @@ def test_batches_at_the_border_between_few_and_tiles(M, N, K):
     ref = xv @ wv[c].T + (xf @ Af.T) @ Bf[c].T
     bound = layer_bound(ref, xv, wv[c].T, xf, Af, Bf[c], 1.0, K)
     assert rel_to_bound(to_np(y)[:, c], ref, bound) <= 1
+
+
+# few tokens, two tiles of 16 rows a workgroup: the last one half empty or not
+@pytest.mark.parametrize("M,N,K,r", [(5, 4112, 1168, 16), (16, 4128, 1296, 64), (2, 8192, 1040, 0),
+                                     (16, 8176, 1168, 24), (31, 4112, 1296, 16),
+                                     (32, 5008, 1168, 128), (17, 8192, 1040, 0)])
+def test_few_tokens_with_two_row_tiles(M, N, K, r):
+    w = weights(N, K, M)
+    rng = np.random.default_rng(N)
+    xb = acts(M, K, 3)
+    A, B = (bf16_of(rng.standard_normal(sh) * 0.02) for sh in ((r, K), (N, r)))
+    fw = qn.fp8_quantize_weight(torch.from_numpy(w).to(DEV))
+    wv = fp8.weight_values(*fp8.quantize_blocks(w))
+    xf, Af, Bf = f64(xb), f64(A), f64(B)
+    y = torch.full((M * N + 64,), 7.0, dtype=torch.bfloat16, device=DEV)
+    u = torch.empty((M, r), dtype=torch.bfloat16, device=DEV) if r else None
+    s = 16.0 / r if r else 0.0
+    qn.fp8_linear_fwd(fw, bf16_dev(xb), bf16_dev(A) if r else None, bf16_dev(B) if r else None, r,
+                      16.0, y=y[:M * N].view(M, N), u_out=u)
+    torch.cuda.synchronize()
+    assert torch.all(y[M * N:] == 7.0)
+    got = to_np(y[:M * N].view(M, N))
+    xv = fp8.row_values(*fp8.quantize_rows(xf.astype(np.float32)))
+    check(f"fp8 y {M}x{N}x{K} r={r}", got, xv @ wv.T + s * (xf @ Af.T) @ Bf.T)
+    c = np.unique(np.concatenate([np.arange(0, N, 37), np.arange(N - 48, N)]))
+    ref = xv @ wv[c].T + s * (xf @ Af.T) @ Bf[c].T
+    bound = layer_bound(ref, xv, wv[c].T, xf, Af if r else None, Bf[c], s, K)
+    assert rel_to_bound(got[:, c], ref, bound) <= 1
+    if r:
+        bu = 2.0 ** -8 * 1.01 * np.abs(xf @ Af.T) + (K + 4) * 2.0 ** -23 * (np.abs(xf) @ np.abs(Af.T))
+        assert rel_to_bound(to_np(u), xf @ Af.T, bu + 1e-30) <= 1
