@@ -349,10 +349,13 @@ bool fp8_few(int64_t M, int64_t N, int64_t K) {
 }
 
 bool fp8_token_self_u(const Fp8View& w, int r) {
-  // A is read by every workgroup, from the caches: past about 40 MB in all a
-  // projection launch of its own costs less (one token, r = 16: 4096 x 4096,
-  // 34 MB, 9.2 us against 10.9; 6000 x 4096, 49 MB, 14.8 against 11.7)
-  return r <= 16 && w.N / 16 * r * w.K * 2 <= (int64_t{40} << 20);
+  // A is read by every workgroup, from the caches: past about 40 MB in all, or
+  // 128 KB each, a projection launch of its own costs less (one token, r = 16:
+  // 4096 x 4096, 34 MB and 128 KB, 9.2 us against 8.8 and a launch more for
+  // the host; 6000 x 4096, 49 MB, 14.8 against 11.7; 1008 x 8192, 256 KB, 13.8
+  // against 9.7)
+  const int64_t a = int64_t{2} * r * w.K;
+  return r <= 16 && a <= (int64_t{128} << 10) && w.N / 16 * a <= (int64_t{40} << 20);
 }
 
 hipError_t launch_fp8_token(const Fp8View& w, const uint16_t* x, const uint16_t* A,

@@ -624,7 +624,7 @@ QN_API int lora_adamw_table(const qn_adamw_tensor* t, int32_t count, int32_t gra
  *   ws   device workspace, 8-byte aligned, of at least
  *        lora_grad_norm_workspace_bytes(plan); not shared by calls that may
  *        run at the same time.
- * A table without elements gives norm 0 and coefficient 1.
+ * A table without elements gives norm 0.
  */
 QN_API size_t lora_grad_norm_workspace_bytes(const qn_adamw_plan* plan);
 QN_API int lora_grad_norm(const qn_adamw_plan* plan, const void* table, float max_norm, float* out,
