@@ -645,3 +645,12 @@ def test_few_tokens_with_two_row_tiles(M, N, K, r):
     if r:
         bu = 2.0 ** -8 * 1.01 * np.abs(xf @ Af.T) + (K + 4) * 2.0 ** -23 * (np.abs(xf) @ np.abs(Af.T))
         assert rel_to_bound(to_np(u), xf @ Af.T, bu + 1e-30) <= 1
+
+
+# one token, u from a launch before, in the forms of 8 and of 16 waves, and of
+# its own at the border of the rule on A's size
+@pytest.mark.parametrize("N,K,r", [(4112, 4112, 16), (8192, 1040, 128), (4112, 528, 17),
+                                   (4096, 1040, 33), (144, 4096, 16), (144, 4112, 16),
+                                   (144, 8192, 8), (144, 8208, 8), (5008, 400, 0)])
+def test_one_token_with_many_columns(N, K, r):
+    test_few_tokens_with_two_row_tiles(1, N, K, r)
