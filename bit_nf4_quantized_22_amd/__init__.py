@@ -657,14 +657,14 @@ def _call(fn, dev, stream, *args):
         _check(fn, status)
 
 
-def _new(shape, dtype, dev, stream):
+def _new(stream, dtype, dev, *shape):
     """A tensor for a call on the given stream: in that stream's memory, so
     that neither earlier nor later work of the current stream shares it."""
     torch = _torch()
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=dev)
+        return torch.empty(*shape, dtype=dtype, device=dev)
     with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=dev)
+        return torch.empty(*shape, dtype=dtype, device=dev)
 
 
 def _addr(t):
@@ -699,11 +699,11 @@ def fp8_quantize_blocks(w, codes=None, scale=None, stream=None):
     N, K = w.shape
     nb, kb = -(-N // FP8_BLOCK), -(-K // FP8_BLOCK)
     if codes is None:
-        codes = _new((N, K), torch.float8_e4m3fn, w.device, stream)
+        codes = _new(stream, torch.float8_e4m3fn, w.device, N, K)
     else:
         _fit(codes, torch.float8_e4m3fn, N * K, w.device, "codes")
     if scale is None:
-        scale = _new((nb, kb), torch.float32, w.device, stream)
+        scale = _new(stream, torch.float32, w.device, nb, kb)
     else:
         _fit(scale, torch.float32, nb * kb, w.device, "scale")
     _call("fp8_quantize_blocks", w.device, stream, w.data_ptr(),
@@ -727,11 +727,11 @@ def fp8_quantize_rows(x, codes=None, scale=None, stream=None):
     kb = -(-K // FP8_BLOCK)
     _dev(x, torch.bfloat16, name="x")
     if codes is None:
-        codes = _new((M, K), torch.float8_e4m3fn, x.device, stream)
+        codes = _new(stream, torch.float8_e4m3fn, x.device, M, K)
     else:
         _fit(codes, torch.float8_e4m3fn, M * K, x.device, "codes")
     if scale is None:
-        scale = _new((kb, M), torch.float32, x.device, stream)
+        scale = _new(stream, torch.float32, x.device, kb, M)
     else:
         _fit(scale, torch.float32, kb * M, x.device, "scale")
     _call("fp8_quantize_rows", x.device, stream, x.data_ptr(), M, K, codes.data_ptr(),
@@ -747,7 +747,7 @@ def fp8_dequant(fw, out_dtype=None, out=None, stream=None):
         raise ValueError("fp8_dequant: out_dtype must be float32 or bfloat16")
     dev = fw.device
     if out is None:
-        out = _new((fw.N, fw.K), out_dtype, dev, stream)
+        out = _new(stream, out_dtype, dev, fw.N, fw.K)
     else:
         _fit(out, out_dtype, fw.N * fw.K, dev, "out")
     _call("fp8_dequant", dev, stream, fw.c_struct(),
@@ -767,12 +767,12 @@ def fp8_matmul(fw, codes, scale, transposed=False, out=None, ws=None, stream=Non
     _fit(codes, torch.float8_e4m3fn, M * L, dev, "codes")
     _fit(scale, torch.float32, -(-L // FP8_BLOCK) * M, dev, "scale")
     if out is None:
-        out = _new((M, n), torch.bfloat16, dev, stream)
+        out = _new(stream, torch.bfloat16, dev, M, n)
     else:
         _fit(out, torch.bfloat16, M * n, dev, "out")
     if ws is None:
         op = QN_OP_FP8_BWD_DX if transposed else QN_OP_FP8_FWD
-        ws = _new(qn_workspace_bytes(op, M, fw.N, fw.K, 0), torch.uint8, dev, stream)
+        ws = _new(stream, torch.uint8, dev, qn_workspace_bytes(op, M, fw.N, fw.K, 0))
     else:
         _fit(ws, torch.uint8, ws.numel(), dev, "ws")
     _call("fp8_matmul", dev, stream, fw.c_struct(), codes.data_ptr(), scale.data_ptr(), M,
@@ -806,13 +806,13 @@ def _fp8_linear(fn, op, fw, x, L, n, A, B, r, alpha, out, low, ws, stream):
         _fit(B, bf16, fw.N * r, dev, "B")
         b = B.data_ptr()
     if out is None:
-        out = _new((M, n), bf16, dev, stream)
+        out = _new(stream, bf16, dev, M, n)
     else:
         _fit(out, bf16, M * n, dev, "y" if fwd else "dx")
     if low is not None:
         _fit(low, bf16, M * r, dev, "u_out" if fwd else "t_out")
     if ws is None:
-        ws = _new(qn_workspace_bytes(op, M, fw.N, fw.K, r), torch.uint8, dev, stream)
+        ws = _new(stream, torch.uint8, dev, qn_workspace_bytes(op, M, fw.N, fw.K, r))
     else:
         _fit(ws, torch.uint8, ws.numel(), dev, "ws")
     _call(fn, dev, stream, fw.c_struct(), x.data_ptr(), M, a, b, r, alpha, out.data_ptr(),
@@ -893,11 +893,11 @@ def lora_grad_norm(table, max_norm, out=None, ws=None, stream=None):
     torch = _torch()
     dev = table.device
     if out is None:
-        out = _new(2, torch.float32, dev, stream)
+        out = _new(stream, torch.float32, dev, 2)
     else:
         _fit(out, torch.float32, 2, dev, "out")
     if ws is None:
-        ws = _new(lora_grad_norm_workspace_bytes(table), torch.uint8, dev, stream)
+        ws = _new(stream, torch.uint8, dev, lora_grad_norm_workspace_bytes(table))
     else:
         _fit(ws, torch.uint8, ws.numel(), dev, "ws")
     _call("lora_grad_norm", dev, stream, table.plan, table.table.data_ptr(),
