@@ -339,13 +339,15 @@ __global__ __launch_bounds__(64 * kWaves) void fp8_decode_kernel(
 
 bool fp8_few(int64_t M, int64_t N, int64_t K) {
   // x's codes go to every workgroup: 16 tokens' as many bytes from the L2s as
-  // the weight has.  Past 64 MiB of them the tiles, which share x among 128
-  // columns, cost less (r = 16: 32 x 4096 x 4096, 32 MiB, 16.2 us against 18.3;
-  // 64 x 4096 x 4096, 64 MiB, 20.1 and 20.2; 64 x 4096 x 11008, 42 against 31;
-  // 64 x 22016 x 8192, 127 against 53).  Up to 16 tokens the two differ by 5%
-  // at most there.
+  // the weight has.  From 64 MiB of them over a full round of CUs (4096
+  // columns) on, the tiles, which share x among 128 columns, cost less (r =
+  // 16: 32 x 4096 x 4096, 32 MiB, 16.2 us against 18.3; 64 x 4096 x 4096, 64
+  // MiB, 20.1 and 20.2; 64 x 1008 x 8192, 31 against 21; 64 x 4096 x 11008, 42
+  // against 31; 64 x 22016 x 8192, 127 against 53).  Up to 16 tokens the two
+  // differ by 5% at most there.
+  const int64_t cols = N > 4096 ? N : 4096;
   return M <= kFp8DecodeM ||
-         (M <= kFp8FewM && (M + 15) / 16 * N * K <= (int64_t{64} << 20));
+         (M <= kFp8FewM && (M + 15) / 16 * cols * K < (int64_t{64} << 20));
 }
 
 bool fp8_token_self_u(const Fp8View& w, int r) {

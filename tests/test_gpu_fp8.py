@@ -591,7 +591,9 @@ def test_large_tiles_with_many_ranks_and_short_contractions(M, N, K, r):
 
 
 @pytest.mark.parametrize("M,N,K", [(64, 4096, 4096), (64, 4112, 4096), (33, 5600, 4000),
-                                   (17, 8192, 4112), (17, 8192, 4096)])
+                                   (17, 8192, 4112), (17, 8192, 4096), (64, 4096, 4080),
+                                   (64, 256, 4096), (64, 256, 4080), (17, 144, 8192),
+                                   (32, 272, 8176)])
 def test_batches_at_the_border_between_few_and_tiles(M, N, K):
     """Sizes on both sides of the rule that picks the kernel of 17 to 64
     tokens, with a workspace of the asked size and a guard behind it."""
