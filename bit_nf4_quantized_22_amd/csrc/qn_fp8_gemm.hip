@@ -699,15 +699,23 @@ bool large(int64_t M, int64_t ncols) { return small_tiles(M, ncols) > 256; }
 
 int fp8_gemm_splits(int64_t M, int64_t ncols, int64_t L) {
   if (M <= 0 || large(M, ncols)) return 1;
-  // one workgroup per CU, at least 8 blocks each: adding the parts up costs a
-  // launch (backward of 333 x 1088 x 2112, 8 blocks: whole 9.9 us, in two
-  // 12.9; of 128 x 11008 x 4096, 86 blocks: whole 48 us, in eight 21)
-  int64_t s = 256 / small_tiles(M, ncols);
-  const int64_t most = L / 128 / 8;
-  s = s < most ? s : most;
-  if (s < 2) return 1;
-  const int64_t per = (L / 128 + s - 1) / s;
-  return static_cast<int>((L / 128 + per - 1) / per);
+  // Up to one workgroup per CU.  A block takes 0.42 us of a workgroup; the
+  // parts cost a launch, 1.5 us, and their way out and back, 8 bytes an output
+  // at 4.5 TB/s: as many as make the sum least (whole and in parts: 128 x 4096 x 11008, 32 tiles, 41 us, in eight 20.6;
+  // 1000 x 1024 x 8192, 64 tiles, 32 us, in four 19.9; 1000 x 1024 x 2048 11.6
+  // us, in two 15.4; 333 x 2112 x 1088 8.9 us, in two 13.5).  More parts than
+  // CUs gain nothing (412 x 4416 x 8672, 140 tiles, 45.9 us, in three
+  // 44.9).
+  const int64_t blocks = L / 128, most = 256 / small_tiles(M, ncols);
+  const double out = static_cast<double>(M) * static_cast<double>(ncols) * 8 / 4.5e6;
+  double best = 0.42 * static_cast<double>(blocks);
+  int splits = 1;
+  for (int64_t s = 2; s <= most && s <= blocks; ++s) {
+    const int64_t per = (blocks + s - 1) / s, n = (blocks + per - 1) / per;
+    const double t = 0.42 * static_cast<double>(per) + 1.5 + out * static_cast<double>(n);
+    if (t < best) best = t, splits = static_cast<int>(n);
+  }
+  return splits;
 }
 
 hipError_t launch_fp8_gemm(const Fp8View& w, const uint8_t* x, const float* xs, int64_t M,
