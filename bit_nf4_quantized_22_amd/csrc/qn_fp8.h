@@ -104,6 +104,19 @@ __device__ __forceinline__ uint4 load_bf16x8(const uint16_t* p, int left, bool v
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
+// Two values as sums hi + lo of bf16 numbers (pairs of each): 16 significant
+// bits.  What bf16 holds as an infinity or NaN has lo = 0.
+struct Bf16Split {
+  uint32_t hi, lo;
+};
+
+__device__ __forceinline__ Bf16Split split_bf16x2(float a, float b) {
+  const uint32_t hi = pack_bf16x2(a, b);
+  const float ha = bf16_lo(hi), hb = bf16_hi(hi);
+  return {hi, pack_bf16x2(fabsf(ha) < __builtin_inff() ? a - ha : 0.0f,
+                          fabsf(hb) < __builtin_inff() ? b - hb : 0.0f)};
+}
+
 __device__ __forceinline__ f32x4_t mfma_bf16_32(const uint4& a, const uint4& b, f32x4_t c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, a),
                                                   __builtin_bit_cast(bf16x8_t, b), c, 0, 0, 0);

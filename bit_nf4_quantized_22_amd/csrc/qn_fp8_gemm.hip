@@ -8,8 +8,9 @@
 // 16x16x128 FP8 MFMA per 16 x 16 outputs; its fp32 result is multiplied by
 // the block's two scales and added to the fp32 accumulator with one fused
 // multiply-add per output, so no scale is ever rounded to fewer bits.  The
-// LoRA term comes first on the same accumulators: 64 ranks of bf16 are a block
-// of 128 bytes too, laid out like one and multiplied by bf16 MFMAs.
+// LoRA term comes first on the same accumulators, multiplied by bf16 MFMAs: s u
+// (s t) is there as two bf16 parts, whose 32 ranks are a block of 128 bytes
+// too, and 64 ranks of the adapter are another, both laid out like codes.
 //
 // Tiles.  A wave holds kWTM x 64 outputs, which lie in one 128-block of the
 // weight, so the weight's scale is wave-uniform; the MFMAs take the weight as
@@ -44,7 +45,7 @@ struct Fp8Args {
   const uint8_t* x;    // codes [M, L], L the contraction length
   const float* xs;     // scales [ceil(L / 128), M]
   int64_t M, N, K;
-  const uint16_t* act;  // bf16(s u) or bf16(s t), [M] rows of `pitch` values
+  const uint16_t* act;  // s u or s t in two parts, [M] rows of `pitch` values
   const uint16_t* lw;   // B [N, r] or A [r, K]
   int r, pitch;
   bool vec_w;           // lw can be read 16 bytes at a time
@@ -207,20 +208,19 @@ __device__ __forceinline__ void add_pending(const Pending<T>& p, int j, f32x4_t&
   for (int e = 0; e < 4; ++e) acc[e] = fmaf(p.c[j][e], p.f, acc[e]);
 }
 
-// LoRA term, 64 ranks at a time: the tokens' side (padded rows of 128 bytes)
-// by DMA, the adapter's from where it lies, through registers: rows of B as
-// the codes' rows, or A's 64 rows of kBN columns, which the transposing LDS
-// loads read.
+// LoRA term: the tokens' side 32 ranks at a time (128 bytes a row, both parts)
+// by DMA, the adapter's 64 at a time from where it lies, through registers:
+// rows of B as the codes' rows, or A's 64 rows of kBN columns, which the
+// transposing LDS loads read.
 template <typename T>
 struct LoraRows {
   uint4 v[T::kBN * 8 / T::kThreads];
 };
 
-template <typename T, bool kBwd>
-__device__ __forceinline__ void lora_load(const Fp8Args& g, int lb, int64_t m0, int64_t c0,
-                                          uint8_t* st, LoraRows<T>& w) {
-  const int t = threadIdx.x, lane = t & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
+template <typename T>
+__device__ __forceinline__ void lora_tokens(const Fp8Args& g, int lb, int64_t m0, uint8_t* st) {
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const uint16_t* pa = g.act + m0 * g.pitch + lb * 64;
 #pragma unroll
   for (int d = 0; d < T::kDmaA; ++d) {
@@ -229,6 +229,11 @@ __device__ __forceinline__ void lora_load(const Fp8Args& g, int lb, int64_t m0, 
     dma16(static_cast<uint32_t>(at * g.pitch * 2 + ((lane & 7) ^ row_swz(row)) * 16), pa,
           lds_addr(st) + (wave * T::kDmaA + d) * 1024);
   }
+}
+
+template <typename T, bool kBwd>
+__device__ __forceinline__ void lora_load(const Fp8Args& g, int lb, int64_t c0, LoraRows<T>& w) {
+  const int t = threadIdx.x;
 #pragma unroll
   for (int q = 0; q < static_cast<int>(sizeof(w.v) / 16); ++q) {
     const int e = q * T::kThreads + t;
@@ -273,34 +278,37 @@ __device__ __forceinline__ void lora_store(uint8_t* st, const LoraRows<T>& w) {
   }
 }
 
+// Adds the ranks 32 lb .. + 31, which are the half lb & 1 of the adapter's.
 template <typename T, bool kBwd>
-__device__ __forceinline__ void lora_add(const Fp8Args& g, int lb, const uint8_t* st,
+__device__ __forceinline__ void lora_add(int lb, const uint8_t* st,
                                          f32x4_t (&acc)[T::kTI][T::kTJ]) {
   const int lane = threadIdx.x & 63, li = lane & 15, lg = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wave / T::kGN, wn = wave % T::kGN;
-#pragma unroll 1
-  for (int kk = 0; kk < 2 && lb * 64 + kk * 32 < g.r; ++kk) {
-    const int at = ((4 * kk + lg) ^ row_swz(li)) * 16;
-    uint4 b[T::kTJ];
+  const int half = lb & 1;
+  uint4 b[T::kTJ];
 #pragma unroll
-    for (int j = 0; j < T::kTJ; ++j) {
-      if constexpr (kBwd) {
-        // lane 4 a + e of a group points at rank row a, columns 4 e .. + 3
-        uint2 h[2];
+  for (int j = 0; j < T::kTJ; ++j) {
+    if constexpr (kBwd) {
+      // lane 4 a + e of a group points at rank row a, columns 4 e .. + 3
+      uint2 h[2];
 #pragma unroll
-        for (int q = 0; q < 2; ++q) {
-          const int row = 32 * kk + 8 * lg + 4 * q + (li >> 2);
-          const i16x4_t d = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-              (lds_i16x4_t*)(lds_u8_t*)(st + T::kA + row * (T::kBN * 2) +
-                                        (((wn * 4 + j) ^ lora_swz(row)) << 5) + (li & 3) * 8));
-          h[q] = __builtin_bit_cast(uint2, d);
-        }
-        b[j] = make_uint4(h[0].x, h[0].y, h[1].x, h[1].y);
-      } else {
-        b[j] = *reinterpret_cast<const uint4*>(st + T::kA + (wn * 64 + j * 16 + li) * 128 + at);
+      for (int q = 0; q < 2; ++q) {
+        const int row = 32 * half + 8 * lg + 4 * q + (li >> 2);
+        const i16x4_t d = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+            (lds_i16x4_t*)(lds_u8_t*)(st + T::kA + row * (T::kBN * 2) +
+                                      (((wn * 4 + j) ^ lora_swz(row)) << 5) + (li & 3) * 8));
+        h[q] = __builtin_bit_cast(uint2, d);
       }
+      b[j] = make_uint4(h[0].x, h[0].y, h[1].x, h[1].y);
+    } else {
+      const int at = ((4 * half + lg) ^ row_swz(li)) * 16;
+      b[j] = *reinterpret_cast<const uint4*>(st + T::kA + (wn * 64 + j * 16 + li) * 128 + at);
     }
+  }
+#pragma unroll 1
+  for (int p = 0; p < 2; ++p) {
+    const int at = ((4 * p + lg) ^ row_swz(li)) * 16;
 #pragma unroll
     for (int i = 0; i < T::kTI; ++i) {
       const uint4 a = *reinterpret_cast<const uint4*>(st + (wm * T::kWTM + i * 16 + li) * 128 + at);
@@ -493,17 +501,21 @@ __device__ __forceinline__ void fp8_tile(const Fp8Args& g, uint8_t* smem, int64_
     uint8_t* stT = smem + (T::kBuf > 2 ? T::kBuf - 2 : 1) * T::kStage;
     LoraRows<T> lw;
     TailRows<T> tr;
-    if (rank > 0) lora_load<T, kBwd>(g, 0, m0, c0, stL, lw);
+    if (rank > 0) {
+      lora_tokens<T>(g, 0, m0, stL);
+      lora_load<T, kBwd>(g, 0, c0, lw);
+    }
     if (tail) tail_load<T, kBwd>(g, tail, m0, c0, b0 + nfull, tr);
-    for (int lb = 0; lb * 64 < rank; ++lb) {
+    for (int lb = 0; lb * 32 < rank; ++lb) {
       if (lb > 0) {
         __syncthreads();
-        lora_load<T, kBwd>(g, lb, m0, c0, stL, lw);
+        lora_tokens<T>(g, lb, m0, stL);
+        if ((lb & 1) == 0) lora_load<T, kBwd>(g, lb >> 1, c0, lw);
       }
-      lora_store<T, kBwd>(stL, lw);
+      if ((lb & 1) == 0) lora_store<T, kBwd>(stL, lw);
       asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
       __syncthreads();
-      lora_add<T, kBwd>(g, lb, stL, acc);
+      lora_add<T, kBwd>(lb, stL, acc);
     }
     if (tail) {
       if (T::kBuf == 2) __syncthreads();

@@ -44,16 +44,27 @@ __device__ __forceinline__ Bytes32 row_bytes(const uint8_t* row, int64_t b, int6
 }
 
 // LoRA-up term of 16 tokens: acc += B[n rows] us^T, us rows of `pitch` bf16
-// (zero past r) at sus, B's fragments already in registers.
+// (the two parts of 32 ranks at a time, zero past r) at sus, B's fragments
+// already in registers.
 template <int kFrags>
 __device__ __forceinline__ f32x4_t lora_up(f32x4_t acc, const uint4 (&bf)[kFrags],
                                            const uint16_t* sus, int pitch, int r, int li, int lg) {
 #pragma unroll
   for (int q = 0; q < kFrags; ++q)
-    if (32 * q < r)
-      acc = mfma_bf16_32(bf[q], *reinterpret_cast<const uint4*>(sus + li * pitch + 32 * q + 8 * lg),
-                         acc);
+    if (32 * q < r) {
+      const uint16_t* p = sus + li * pitch + 64 * q + 8 * lg;
+      acc = mfma_bf16_32(bf[q], *reinterpret_cast<const uint4*>(p), acc);
+      acc = mfma_bf16_32(bf[q], *reinterpret_cast<const uint4*>(p + 32), acc);
+    }
   return acc;
+}
+
+// Rank j of a row of us = the two parts of v.
+__device__ __forceinline__ void store_us(uint16_t* row, int j, float v) {
+  const Bf16Split p = split_bf16x2(v, 0.0f);
+  uint16_t* at = row + (j & ~31) * 2 + (j & 31);
+  at[0] = static_cast<uint16_t>(p.hi & 0xFFFF);
+  at[32] = static_cast<uint16_t>(p.lo & 0xFFFF);
 }
 
 __device__ __forceinline__ void store_columns(uint16_t* y, f32x4_t acc) {
@@ -75,7 +86,7 @@ __global__ __launch_bounds__(64 * kWaves) void fp8_token_kernel(
   constexpr int kFrags = kU == kGivenU ? kMaxRank / 32 : 1;
   __shared__ f32x4_t s_acc[kWaves][4];
   __shared__ float s_u[kU == kNoAdapter ? 1 : kThreads];  // kOwnU: [wave][16 ranks]
-  __shared__ __attribute__((aligned(16))) uint16_t s_us[32 * kFrags];
+  __shared__ __attribute__((aligned(16))) uint16_t s_us[64 * kFrags];
   __shared__ __attribute__((aligned(16))) uint32_t s_x[kWaves][kAhead][64];   // bf16 pairs
   __shared__ __attribute__((aligned(16))) uint16_t s_q[kWaves][kAhead][64];   // code pairs
   const int t = threadIdx.x, lane = t & 63;
@@ -179,7 +190,7 @@ __global__ __launch_bounds__(64 * kWaves) void fp8_token_kernel(
       }
       if (u_out && blockIdx.x == 0 && j < r)
         u_out[j] = static_cast<uint16_t>(pack_bf16x2(s, 0.f) & 0xFFFF);
-      s_us[j] = static_cast<uint16_t>(pack_bf16x2(s * lora_scale, 0.f) & 0xFFFF);
+      store_us(s_us, j, s * lora_scale);
     }
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
     acc = lora_up(acc, bf, s_us, 0, r, li, lg);
@@ -188,7 +199,7 @@ __global__ __launch_bounds__(64 * kWaves) void fp8_token_kernel(
 }
 
 // Up to 16 kMT tokens, codes and scales of x given; u as `slices` partial
-// sums (kMT == 1), or act = bf16(s u) in rows of `pitch` values.
+// sums (kMT == 1), or act = s u in two parts in rows of `pitch` values.
 template <int kWaves, int kMT, int kRows>
 __global__ __launch_bounds__(64 * kWaves) void fp8_decode_kernel(
     const uint8_t* __restrict__ w, const float* __restrict__ ws, int64_t N, int64_t K,
@@ -202,7 +213,7 @@ __global__ __launch_bounds__(64 * kWaves) void fp8_decode_kernel(
   static_assert(kTiles <= kWaves, "a wave finishes 16 columns of 16 tokens");
   __shared__ f32x4_t s_acc[kWaves][kTiles][64];
   __shared__ float s_u[kMT == 1 ? kFp8DecodeM * kMaxRank : 1];
-  __shared__ __attribute__((aligned(16))) uint16_t s_us[kMT == 1 ? 16 * kMaxRank : 8];
+  __shared__ __attribute__((aligned(16))) uint16_t s_us[kMT == 1 ? 32 * kMaxRank : 8];
   const int t = threadIdx.x, lane = t & 63;
   const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
   const int li = lane & 15, lg = lane >> 4;
@@ -314,7 +325,7 @@ __global__ __launch_bounds__(64 * kWaves) void fp8_decode_kernel(
           if (u_out && blockIdx.x == 0)
             u_out[row * r + j] = static_cast<uint16_t>(pack_bf16x2(s, 0.f) & 0xFFFF);
         }
-        s_us[i] = static_cast<uint16_t>(pack_bf16x2(s * lora_scale, 0.f) & 0xFFFF);
+        store_us(s_us + row * 2 * rp, j, s * lora_scale);
       }
     }
   }
@@ -326,7 +337,7 @@ __global__ __launch_bounds__(64 * kWaves) void fp8_decode_kernel(
   const int row = 16 * (wave % kMT) + li;
   if (r > 0) {
     if constexpr (kMT == 1)
-      sum = lora_up(sum, bf, s_us, (r + 31) & ~31, r, li, lg);
+      sum = lora_up(sum, bf, s_us, 2 * ((r + 31) & ~31), r, li, lg);
     else
       sum = lora_up(sum, bf, act + static_cast<int64_t>(row < M ? row - li : M - 1 - li) * pitch,
                     pitch, r, li, lg);

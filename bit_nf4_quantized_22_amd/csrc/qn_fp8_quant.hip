@@ -336,18 +336,18 @@ __global__ __launch_bounds__(kT) void decode_project_kernel(
   }
 }
 
-// The LoRA term's token side for the tile kernel: act[M][ld] = bf16(scale u),
-// u the slices' sum in slice order, rows zero-padded to ld = 64 or 128 values
-// so that a row is one or two 128-byte runs, like the codes of a block; bf16(u)
-// also to `plain` [M, r] for the caller.  Four values per thread; kSlices
-// loads go out before the first is added.
+// The LoRA term's token side for the tile kernel: scale u, u the slices' sum in
+// slice order, as two bf16 parts in rows of act zero-padded to `ranks`, a
+// multiple of 32, so that the parts of 32 ranks are one 128-byte run, like the
+// codes of a block; bf16(u) also to `plain` [M, r] for the caller.  Four values
+// per thread; kSlices loads go out before the first is added.
 __global__ __launch_bounds__(kT) void project_sum_kernel(const float* __restrict__ part, int slices,
-                                                         int64_t M, int r, int ld, float scale,
+                                                         int64_t M, int r, int ranks, float scale,
                                                          uint16_t* __restrict__ act,
                                                          uint16_t* __restrict__ plain) {
   const int64_t i = (static_cast<int64_t>(blockIdx.x) * kT + threadIdx.x) * 4;
-  const int64_t m = i / ld;
-  const int j = static_cast<int>(i % ld);
+  const int64_t m = i / ranks;
+  const int j = static_cast<int>(i % ranks);
   if (m >= M) return;
   f32x4_t s = f32x4_t{0.f, 0.f, 0.f, 0.f};
   const int64_t step = M * r;
@@ -369,8 +369,11 @@ __global__ __launch_bounds__(kT) void project_sum_kernel(const float* __restrict
       if (j + e < r)
         for (int k = 0; k < slices; ++k) s[e] += p[k * step + e];
   }
-  *reinterpret_cast<uint2*>(act + i) = make_uint2(pack_bf16x2(s[0] * scale, s[1] * scale),
-                                                  pack_bf16x2(s[2] * scale, s[3] * scale));
+  const Bf16Split a = split_bf16x2(s[0] * scale, s[1] * scale);
+  const Bf16Split b = split_bf16x2(s[2] * scale, s[3] * scale);
+  uint16_t* at = act + 2 * (i - (j & 31)) + (j & 31);
+  *reinterpret_cast<uint2*>(at) = make_uint2(a.hi, b.hi);
+  *reinterpret_cast<uint2*>(at + 32) = make_uint2(a.lo, b.lo);
   if (plain) {
     const uint32_t u[2] = {pack_bf16x2(s[0], s[1]), pack_bf16x2(s[2], s[3])};
 #pragma unroll
@@ -520,10 +523,10 @@ hipError_t launch_fp8_decode_project(const uint16_t* x, int M, int64_t L, const 
 hipError_t launch_fp8_project_sum(const float* part, int slices, int64_t M, int r, float scale,
                                   uint16_t* act, uint16_t* plain, hipStream_t st) {
   if (M == 0 || r == 0) return hipSuccess;
-  const int ld = fp8_lora_pitch(r);
-  const int64_t threads = M * ld / 4;
+  const int ranks = fp8_lora_ranks(r);
+  const int64_t threads = M * ranks / 4;
   hipLaunchKernelGGL(project_sum_kernel, dim3(static_cast<uint32_t>((threads + kT - 1) / kT)),
-                     dim3(kT), 0, st, part, slices, M, r, ld, scale, act, plain);
+                     dim3(kT), 0, st, part, slices, M, r, ranks, scale, act, plain);
   return hipGetLastError();
 }
 

@@ -171,11 +171,14 @@ hipError_t launch_fp8_token(const Fp8View& w, const uint16_t* x, const uint16_t*
 hipError_t launch_fp8_split_sum(const float* part, int splits, int64_t n, uint16_t* out,
                                 hipStream_t st);
 hipError_t launch_fp8_dequant(const Fp8View& w, bool out_bf16, void* out, hipStream_t st);
-// The LoRA term's token side for launch_fp8_gemm: act[M], rows of
-// fp8_lora_pitch(r) = 64 or 128 bf16 values padded with zeros, = scale * the
-// sum of the slices of part; its bf16 without the scale to plain [M, r] if
+// The LoRA term's token side for launch_fp8_gemm: act[M], scale * the sum of
+// the slices of part, each value as a sum hi + lo of two bf16 numbers: one
+// bf16 alone would cost 2^-8 of the term before the result is rounded.  Rows of
+// fp8_lora_pitch(r) values: for each 32 ranks their 32 hi, then their 32 lo,
+// zeros behind r.  The sum's bf16 without the scale goes to plain [M, r] if
 // not null.
-inline int fp8_lora_pitch(int r) { return r <= 64 ? 64 : 128; }
+inline int fp8_lora_ranks(int r) { return (r + 31) / 32 * 32; }
+inline int fp8_lora_pitch(int r) { return 2 * fp8_lora_ranks(r); }
 hipError_t launch_fp8_project_sum(const float* part, int slices, int64_t M, int r, float scale,
                                   uint16_t* act, uint16_t* plain, hipStream_t st);
 // out = x W^T + act lw^T (x [M, K], lw = B [N, r]), or with bwd
