@@ -532,8 +532,9 @@ QN_API int fp8_matmul(const qn_fp8_weight* w, const uint8_t* x, const float* xsc
  *       (needed for r == 0 too: x's codes lie there).
  * u = x A^T is summed in fp32, and (alpha/r) u enters its product as the sum
  * of two bf16 numbers (16 significant bits); y is rounded to bf16 once.
- * A row of y is bit-reproducible for a given batch; batches of other sizes may
- * add the blocks up in another order.
+ * A row of y (and of u) is bit-reproducible for a given batch, and the same in
+ * all batches of 2 to 16 tokens; other batches may add the blocks up in another
+ * order.
  * A row of x with an infinity or NaN gives a row of NaN and touches no other
  * (padding rows may hold anything).
  */

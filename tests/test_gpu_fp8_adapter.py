@@ -81,3 +81,30 @@ def test_a_lora_operand_past_bf16s_range_is_an_infinity(M):
     y = to_np(y)
     assert np.all(y[0] == np.inf)
     assert np.all(np.isfinite(y[1:])) and np.all(y[1:] > 5)
+
+
+# one, two and more groups of slices of u; one and several threads per value of
+# u; the forms of 4 waves, of 8, and of two row tiles; contractions of other
+# lengths than whole slices
+@pytest.mark.parametrize("N,K,r", [(144, 272, 16), (272, 1040, 5), (144, 4096, 16),
+                                   (272, 11008, 16), (144, 11008, 128), (4112, 4112, 24),
+                                   (16, 2 ** 16 + 528, 8)])
+@pytest.mark.parametrize("seed", [1, 2])
+def test_up_to_16_tokens_the_batch_does_not_change_a_row(N, K, r, seed):
+    """The bits of y and of u: the slices of u are added in an order that
+    depends on K alone."""
+    rng = np.random.default_rng(seed)
+    bits = lambda *shape: bf16_dev(synth.bf16_bits(rng.standard_normal(shape).astype(np.float32)))
+    fw = qn.fp8_quantize_weight(bits(N, K))
+    A, B, x = bits(r, K), bits(N, r), bits(16, K)
+
+    def both(M):
+        u = torch.empty((M, r), dtype=torch.bfloat16, device=DEV)
+        y = qn.fp8_linear_fwd(fw, x[:M], A, B, r, 16.0, u_out=u)
+        torch.cuda.synchronize()
+        return y.view(torch.int16), u.view(torch.int16)
+
+    all_y, all_u = both(16)
+    for M in (2, 3, 4, 7, 8, 15):
+        y, u = both(M)
+        assert torch.equal(u, all_u[:M]) and torch.equal(y, all_y[:M]), M
