@@ -652,8 +652,10 @@ QN_API int lora_grad_norm(const qn_adamw_plan* plan, const void* table, float ma
  * the sum is cut.  Over the steps the codes' mean follows x, where
  * rounding to nearest would lose every change smaller than half a code.
  * The code of a v > 0 is at least 1.  Results are bit-reproducible.
- * Without grad_scale, a NaN or infinite gradient makes p of its element NaN;
- * with 8-bit states later steps may do so for its whole block.
+ * Without grad_scale, a NaN or infinite gradient makes p of its element NaN,
+ * and its states are not finite from then on; no other element is touched.
+ * 8-bit states keep an m that is not finite as E4M3's NaN and a v as E5M2's
+ * infinity or NaN; a block's scales are those of its finite elements.
  * `step` and the hyperparameters are host values: a captured graph repeats
  * the step that it was captured with.
  */

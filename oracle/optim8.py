@@ -8,7 +8,9 @@ scale: m as E4M3 codes (top 448), v as E5M2 codes (top 57344).  The rounding
 to codes is decided by integers, so it is restated here by arithmetic on the
 values of the codes, one element at a time in the exact rationals that fp64
 holds: q = n / step with step the spacing of the codes at n, code value
-floor(q + f) step, f the dither's fraction.
+floor(q + f) step, f the dither's fraction.  A value that is not finite takes
+no part in its block's scale: an m is the NaN code, a v the code of infinity or
+NaN.
 """
 
 import numpy as np
@@ -51,7 +53,8 @@ def _per_block(x, fn):
 
 
 def _scales(x, top):
-    s = _per_block(np.abs(x), np.max) / np.float32(top)
+    a = np.where(np.isfinite(x), np.abs(x), np.float32(0))
+    s = _per_block(a, np.max) / np.float32(top)
     return np.maximum(s.astype(np.float32), FLOOR)
 
 
@@ -62,23 +65,29 @@ def _spread(s, n):
 def encode_m(m, step):
     """(codes uint8, scales) of fp32 m."""
     s = _scales(m, 448)
+    lost, m = ~np.isfinite(m), np.where(np.isnan(m), np.float32(0), m)
+    sign = np.where(m < 0, 0x80, 0)
+    m = np.where(lost, np.float32(0), m)
     inv = _spread((np.float32(1) / s).astype(np.float32), m.size)
     n = np.minimum((np.abs(m) * inv).astype(np.float32), np.float32(448))
     frac = (_dither(m.size, step) >> np.uint64(12)).astype(np.float64) / 2.0 ** 20
     # the fraction is added below the last mantissa bit of a 24-bit number, so
     # a subnormal's bits below 2^-20 of its step are cut before the addition
     c = _codes(_cut(n, 3, -6, 20), frac, 3, -6, 7, 448.0)
-    return (c | np.where(m < 0, 0x80, 0)).astype(np.uint8), s
+    return (np.where(lost, 0x7F, c) | sign).astype(np.uint8), s
 
 
 def encode_v(v, step):
     """(codes uint8, scales) of fp32 v >= 0; a positive v is at least code 1."""
     s = _scales(v, 57344)
+    inf, nan = np.isinf(v), np.isnan(v)
+    v = np.where(inf | nan, np.float32(0), v)
     inv = _spread((np.float32(1) / s).astype(np.float32), v.size)
     n = np.minimum((v * inv).astype(np.float32), np.float32(57344))
     frac = ((np.uint64(0xFFFFFFFF) - _dither(v.size, step)) >> np.uint64(11)).astype(np.float64)
     c = _codes(_cut(n, 2, -14, 21), frac / 2.0 ** 21, 2, -14, 15, 57344.0)
-    return np.where(v > 0, np.maximum(c, 1), 0).astype(np.uint8), s
+    c = np.where(v > 0, np.maximum(c, 1), 0)
+    return np.where(inf, 0x7C, np.where(nan, 0x7F, c)).astype(np.uint8), s
 
 
 def _cut(n, mant, min_exp, bits):
