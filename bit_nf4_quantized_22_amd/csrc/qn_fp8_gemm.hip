@@ -711,20 +711,24 @@ bool large(int64_t M, int64_t ncols) { return small_tiles(M, ncols) > 256; }
 
 int fp8_gemm_splits(int64_t M, int64_t ncols, int64_t L) {
   if (M <= 0 || large(M, ncols)) return 1;
-  // Up to one workgroup per CU.  A block takes 0.42 us of a workgroup; the
-  // parts cost a launch, 1.5 us, and their way out and back, 8 bytes an output
-  // at 4.5 TB/s: as many as make the sum least (whole and in parts: 128 x 4096 x 11008, 32 tiles, 41 us, in eight 20.6;
-  // 1000 x 1024 x 8192, 64 tiles, 32 us, in four 19.9; 1000 x 1024 x 2048 11.6
-  // us, in two 15.4; 333 x 2112 x 1088 8.9 us, in two 13.5).  More parts than
-  // CUs gain nothing (412 x 4416 x 8672, 140 tiles, 45.9 us, in three
-  // 44.9).
+  // Up to one workgroup per CU.  A block takes 0.42 us of a workgroup.  The
+  // parts cost a launch, the turn to another workgroup and its latency, 2.4 us
+  // in all, 0.1 us each in the sum, and their way out and back, 8 bytes an
+  // output at 5.5 TB/s (mostly in the caches): as many as make the total least.
+  // Whole and as chosen here, products of given rows, in us: 128 x 4096 x 11008
+  // 41.0, in 6 20.1; 1000 x 1024 x 8192 32.2, in 4 20.4; 65 x 4096 x 4096 18.2,
+  // in 4 12.6; 512 x 2048 x 4096 18.5, in 3 17.5; 128 x 11008 x 4096 19.8, in 2
+  // 19.1; 100 x 1088 x 2112 11.8, in 4 10.2; 333 x 1088 x 2112 13.6, in 4 13.6.
+  // Kept whole: 200 x 1040 x 1552 10.3, in 2 to 4 11.3 to 10.6; 333 x 2112 x
+  // 1088 8.9, in 2 13.5; 1000 x 1024 x 2048 11.9, in 2 15.3.  More parts than
+  // CUs gain nothing (412 x 4416 x 8672, 140 tiles, 45.9 us, in three 44.9).
   const int64_t blocks = L / 128, most = 256 / small_tiles(M, ncols);
-  const double out = static_cast<double>(M) * static_cast<double>(ncols) * 8 / 4.5e6;
+  const double out = static_cast<double>(M) * static_cast<double>(ncols) * 8 / 5.5e6;
   double best = 0.42 * static_cast<double>(blocks);
   int splits = 1;
   for (int64_t s = 2; s <= most && s <= blocks; ++s) {
     const int64_t per = (blocks + s - 1) / s, n = (blocks + per - 1) / per;
-    const double t = 0.42 * static_cast<double>(per) + 1.5 + out * static_cast<double>(n);
+    const double t = 0.42 * static_cast<double>(per) + 2.4 + (out + 0.1) * static_cast<double>(n);
     if (t < best) best = t, splits = static_cast<int>(n);
   }
   return splits;
