@@ -654,7 +654,9 @@ constexpr int kMixedLds = Big::kBuf * Big::kStage > Half::kBuf * Half::kStage
 // Workgroups below nbig take one 256 x 256 tile each, the others half of one
 // of the remaining tiles: 256-row tiles halve the LDS reads per product, but
 // a last round that fills less than half of the 256 CUs with them costs as
-// much as a full one, and as halves it takes about 0.6 of that.
+// much as a full one, and as halves it takes about 0.6 of that.  A batch of up
+// to 128 tokens is one row of upper halves (32 x 65536 x 4096 71 us, in whole
+// tiles 82; 100 x 33024 x 4096 37 and 53; 128 x 128256 x 4096 140 and 154).
 template <bool kBwd>
 __global__ __launch_bounds__(Big::kThreads, 2) void fp8_gemm_kernel(Fp8Args g, int nbig) {
   static_assert(Big::kThreads == Half::kThreads && Big::kBN == Half::kBN &&
@@ -672,9 +674,10 @@ __global__ __launch_bounds__(Big::kThreads, 2) void fp8_gemm_kernel(Fp8Args g, i
     fp8_tile<Big, kBwd>(g, smem, static_cast<int64_t>(row) * Big::kBM,
                         static_cast<int64_t>(col) * Big::kBN, 0, nfull, tail, true, 0);
   } else {
-    const int q = xcd_run(bid - nbig, 2 * (nc * nr - nbig));
-    fp8_tile_of(nbig + (q >> 1), nc, nr, row, col);
-    const int64_t m0 = static_cast<int64_t>(row) * Big::kBM + (q & 1) * Half::kBM;
+    const int two = g.M > Half::kBM ? 1 : 0;  // log2 of the halves of a tile
+    const int q = xcd_run(bid - nbig, (nc * nr - nbig) << two);
+    fp8_tile_of(nbig + (q >> two), nc, nr, row, col);
+    const int64_t m0 = static_cast<int64_t>(row) * Big::kBM + (q & two) * Half::kBM;
     if (m0 < g.M)
       fp8_tile<Half, kBwd>(g, smem, m0, static_cast<int64_t>(col) * Half::kBN, 0, nfull, tail,
                            true, 0);
@@ -747,9 +750,9 @@ hipError_t launch_fp8_gemm(const Fp8View& w, const uint8_t* x, const float* xs, 
     // whole rounds of the 256 CUs in large tiles, a remainder of up to half
     // a round in halves
     const int64_t tiles = ((ncols + Big::kBN - 1) / Big::kBN) * ((M + Big::kBM - 1) / Big::kBM);
-    const int64_t rest = tiles % 256;
-    const int64_t nbig = rest <= 128 ? tiles - rest : tiles;
-    const dim3 grid(static_cast<uint32_t>(nbig + 2 * (tiles - nbig)));
+    const int64_t rest = tiles % 256, halves = M > Half::kBM ? 2 : 1;
+    const int64_t nbig = halves == 1 ? 0 : rest <= 128 ? tiles - rest : tiles;
+    const dim3 grid(static_cast<uint32_t>(nbig + halves * (tiles - nbig)));
     if (bwd)
       hipLaunchKernelGGL(fp8_gemm_kernel<true>, grid, dim3(Big::kThreads), 0, st, g,
                          static_cast<int>(nbig));
