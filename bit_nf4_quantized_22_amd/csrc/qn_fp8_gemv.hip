@@ -366,13 +366,15 @@ bool fp8_few(int64_t M, int64_t N, int64_t K) {
 }
 
 bool fp8_token_self_u(const Fp8View& w, int r) {
-  // A is read by every workgroup, from the caches: past about 40 MB in all, or
-  // 128 KB each, a projection launch of its own costs less (one token, r = 16:
-  // 4096 x 4096, 34 MB and 128 KB, 9.2 us against 8.8 and a launch more for
-  // the host; 6000 x 4096, 49 MB, 14.8 against 11.7; 1008 x 8192, 256 KB, 13.8
-  // against 9.7)
+  // A is read by every workgroup, from the caches: past 32 MiB in all, or 128
+  // KB each, a projection launch of its own costs less (one token on the
+  // device, own and given u: 4096 x 4096, r = 16, 32 MiB, 9.4 us against 9.0 and
+  // a launch more for the host; 8192 x 1024, r = 16, 6.4 and 7.7; 8192 x 2048,
+  // r = 16, 32 MiB, 9.0 and 8.7; past it 4112 x 4096, which is a second round
+  // of the CUs too, 13.9 and 10.2; 11008 x 2048, r = 8, 10.6 and 9.6; 1008 x
+  // 8192, r = 16, 256 KB each, 13.8 and 9.7)
   const int64_t a = int64_t{2} * r * w.K;
-  return r <= 16 && a <= (int64_t{128} << 10) && w.N / 16 * a <= (int64_t{40} << 20);
+  return r <= 16 && a <= (int64_t{128} << 10) && w.N / 16 * a <= (int64_t{32} << 20);
 }
 
 hipError_t launch_fp8_token(const Fp8View& w, const uint16_t* x, const uint16_t* A,
@@ -386,11 +388,12 @@ hipError_t launch_fp8_token(const Fp8View& w, const uint16_t* x, const uint16_t*
                        slices, B, r, vec_b, lora_scale, y, u_out);
     return hipGetLastError();
   };
-  // 16 waves where one workgroup per CU has the whole weight and for the form
-  // with the fewest registers, else 8, of which more fit on a CU at once
-  // (one token, 8 and 16 waves: r = 0 4096 x 4096 6.6 and 5.8 us; r = 16
-  // 5008 x 2000 7.3 and 9.4, 11008 x 4096 15.6 and 17.0; r = 64 4096 x 4096
-  // 11.0 and 10.4)
+  // Without an adapter, which takes the fewest registers, 16 waves; u given: 16
+  // where one workgroup per CU has the whole weight, else 8, of which more fit on
+  // a CU at once; u of its own: 8, up to one workgroup per CU as fast as 16 and
+  // beyond faster (one token, 8 and 16 waves: r = 0 4096 x 4096 6.6 and 5.8 us;
+  // given, r = 64, 4096 x 4096 11.0 and 10.4; own, r = 16, 4096 x 4096 9.4 and
+  // 9.4, 2048 x 2048 5.5 and 5.8, 5008 x 2000 7.4 and 9.5)
   return r == 0 ? go(fp8_token_kernel<kNoAdapter, 16>, 16)
          : !part        ? go(fp8_token_kernel<kOwnU, 8>, 8)
          : grid.x > 256 ? go(fp8_token_kernel<kGivenU, 8>, 8)

@@ -16,6 +16,7 @@ import torch
 
 import bit_nf4_quantized_22_amd as qn
 from tests.gpu_helpers import bf16_dev, f64, synth, to_np
+from tests.test_gpu_fp8 import test_few_tokens_with_two_row_tiles as layer_against_the_oracle
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda:0"
@@ -108,3 +109,10 @@ def test_up_to_16_tokens_the_batch_does_not_change_a_row(N, K, r, seed):
     for M in (2, 3, 4, 7, 8, 15):
         y, u = both(M)
         assert torch.equal(u, all_u[:M]) and torch.equal(y, all_y[:M]), M
+
+
+@pytest.mark.parametrize("N,K,r", [(4096, 4096, 16), (4112, 4096, 16), (8208, 2048, 16),
+                                   (8192, 2048, 16)])
+def test_one_token_at_the_border_of_an_own_u(N, K, r):
+    """A read by all workgroups together: 32 MiB, and just past it."""
+    layer_against_the_oracle(1, N, K, r)
