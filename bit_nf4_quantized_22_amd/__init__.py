@@ -843,6 +843,9 @@ def lora_adamw_table(ps, gs, ms, vs, m_scales=None, v_scales=None, p_bf16s=None)
     n = len(ps)
     if not n:
         raise ValueError("lora_adamw_table: no matrices")
+    for col, name in zip((ps, gs, ms, vs), ("p", "g", "m", "v")):
+        if any(t is None for t in col):
+            raise ValueError(f"{name}: missing")
     eight = ms[0].dtype != torch.float32
     none = [None] * n
     if eight and (m_scales is None or v_scales is None):
@@ -858,6 +861,7 @@ def lora_adamw_table(ps, gs, ms, vs, m_scales=None, v_scales=None, p_bf16s=None)
         raise ValueError("lora_adamw_table: gradients must be float32 or bfloat16")
     mt, vt = (torch.float8_e4m3fn, torch.float8_e5m2) if eight else (torch.float32,) * 2
     dev = ps[0].device
+    _dev(ps[0], torch.float32, name="p")
     arr = (qn_adamw_tensor * n)()
     for i, row in enumerate(zip(*cols)):
         k = row[0].numel()
@@ -866,12 +870,9 @@ def lora_adamw_table(ps, gs, ms, vs, m_scales=None, v_scales=None, p_bf16s=None)
                                            torch.float32, torch.bfloat16),
                                      (k, k, k, k, blocks, blocks, k),
                                      ("p", "g", "m", "v", "m_scale", "v_scale", "p_bf16")):
-            if t is None and name in ("p", "g", "m", "v"):
-                raise ValueError(f"{name}: missing")
             if t is None and eight and name in ("m_scale", "v_scale"):
                 raise ValueError(f"{name}: missing")
             if t is not None:
-                _dev(t, dt, size, name)
                 _fit(t, dt, size, dev, name)
         arr[i] = qn_adamw_tensor(*[_addr(t) for t in row], k)
     size = lib.lora_adamw_table_bytes(arr, n)

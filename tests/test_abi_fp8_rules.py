@@ -34,3 +34,16 @@ def test_short_products_are_not_split_beyond_their_gain():
     """Measured least times: 4 to 6 parts and 6 to 8."""
     assert 4 <= parts(100, 1088, 2112) <= 6
     assert 6 <= parts(66, 400, 2064) <= 8
+
+
+def test_a_table_with_a_missing_matrix_is_refused():
+    import torch
+
+    t = torch.zeros(4)
+    for k, name in enumerate("pgmv"):
+        cols = [[t, t] for _ in range(4)]
+        cols[k] = [None, t] if k % 2 else [t, None]
+        with pytest.raises(ValueError, match=f"^{name}: missing"):
+            qn.lora_adamw_table(*cols)
+    with pytest.raises(ValueError, match="device tensor"):   # host memory
+        qn.lora_adamw_table([t], [t], [t], [t])
