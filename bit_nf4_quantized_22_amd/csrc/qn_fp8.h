@@ -8,18 +8,19 @@
 namespace qn {
 
 // Scale of a group whose largest magnitude has the fp32 bits amax: fl32(amax /
-// 448), at least 2^-100, so that no group divides by zero and the residuals of
-// fp8_ratio stay normal numbers; NaN for a group with an infinity or NaN, so
-// that every product with the group is NaN.
+// 448), at least 2^-100, so that no group divides by zero and 1 / s is a normal
+// number; NaN for a group with an infinity or NaN, so that every product with
+// the group is NaN.
 __device__ __forceinline__ float fp8_scale(uint32_t amax) {
   const float s = fmaxf(__fdiv_rn(__uint_as_float(amax), 448.0f), 0x1p-100f);
   return amax < 0x7F800000u ? s : __builtin_nanf("");
 }
 
 // fl32(x / s) in the codes' range, inv = fl32(1 / s): one Newton step on
-// x inv (x - q s is exact in the fused multiply-add).  bf16 values often lie
-// on the border between two codes, where the product x inv alone is an ulp
-// to one side.
+// x inv (x - q s is exact in the fused multiply-add; at the lowest borders of
+// a group with the least scale it is a subnormal number, which is kept).  bf16
+// values often lie on the border between two codes, where the product x inv
+// alone is an ulp to one side.
 __device__ __forceinline__ float fp8_ratio(float x, float s, float inv) {
   const float q = x * inv;
   return __builtin_amdgcn_fmed3f(fmaf(fmaf(-q, s, x), inv, q), -448.0f, 448.0f);

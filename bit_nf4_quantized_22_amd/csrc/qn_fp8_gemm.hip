@@ -645,11 +645,11 @@ constexpr int kMixedLds = Big::kBuf * Big::kStage > Half::kBuf * Half::kStage
                               ? Big::kBuf * Big::kStage
                               : Half::kBuf * Half::kStage;
 
-// Measured alone: 4096 x 22016 x 8192 forward 612 us (2413 TF), backward 589
-// (2509 TF); 2048 x 11008 x 4096 93 and 89.  The vendor's FP8 product with one
-// scale per tensor: 622 and, forward, 91.  Without the DMAs the first takes
-// about 80% of its time, without the LDS reads 85%, without the MFMAs 85%:
-// none of them alone bounds it.
+// Measured, median launches of several runs: 4096 x 22016 x 8192 forward 638-645
+// us (2.3 PF; least 614), 2048 x 11008 x 4096 forward 94-105, backward 90-105.
+// The vendor's FP8 product with one scale per tensor: 616-622 and, forward, 91.
+// Without the DMAs the first takes about 80% of its time, without the LDS reads
+// 85%, without the MFMAs 85%: none of them alone bounds it.
 //
 // Workgroups below nbig take one 256 x 256 tile each, the others half of one
 // of the remaining tiles: 256-row tiles halve the LDS reads per product, but

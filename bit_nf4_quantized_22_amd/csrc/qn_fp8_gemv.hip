@@ -12,9 +12,9 @@
 // fragment, some blocks ahead of their products, so the weight needs neither
 // LDS nor a second pass.  The waves' fp32 sums meet in LDS and are added in
 // wave order, so results are bit-reproducible.  One token: 4096 x 4096 in 5.8
-// us (r = 16: 9.2), 8192 x 8192 in 14.5 (4.6 TB/s), 22016 x 8192 with r = 16,
-// two launches, in 38 (4.7 TB/s, a large copy's rate); 16 tokens of 4096 x
-// 11008: 15 us.
+// us (r = 16: 9.4 back to back in a graph, 9.8-10.3 traced alone), 8192 x 8192
+// in 14.5 (4.6 TB/s), 22016 x 8192 with r = 16, two launches, in 38 (4.7 TB/s, a
+// large copy's rate); 16 tokens of 4096 x 11008: 15 us.
 //
 // One token: the same launch quantises x, each wave for its own blocks, and,
 // where the adapter is small, computes u = x A^T: at 4096 x 4096 the whole
@@ -358,8 +358,13 @@ bool fp8_few(int64_t M, int64_t N, int64_t K) {
   // columns) on, the tiles, which share x among 128 columns, cost less (r =
   // 16: 32 x 4096 x 4096, 32 MiB, 16.2 us against 18.3; 64 x 4096 x 4096, 64
   // MiB, 20.1 and 20.2; 64 x 1008 x 8192, 31 against 21; 64 x 4096 x 11008, 42
-  // against 31; 64 x 22016 x 8192, 127 against 53).  Up to 16 tokens the two
-  // differ by 5% at most there.
+  // against 31; 64 x 22016 x 8192, 127 against 53).  Up to 16 tokens this kernel
+  // always, which is the faster one for short contractions and about even for
+  // long ones, but for few columns (products of given rows, here and as tiles,
+  // in us: 16 x 272 x 1040 3.6 and 7.4; 16 x 4096 x 4096 7.5 and 10.0; 16 x 1008
+  // x 8192 10.5 and 10.9; 16 x 4096 x 11008 14.0 and 14.2; 16 x 11008 x 4096 15.8
+  // and 14.5; 16 x 22016 x 8192 52.9 and 50.8; 16 x 144 x 22016, 9 workgroups
+  // here and 2 tiles in parts there, 21.7 and 14.6).
   const int64_t cols = N > 4096 ? N : 4096;
   return M <= kFp8DecodeM ||
          (M <= kFp8FewM && (M + 15) / 16 * cols * K < (int64_t{64} << 20));
