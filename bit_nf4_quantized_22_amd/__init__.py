@@ -23,8 +23,9 @@ QN_ERR_UNSUPPORTED, QN_ERR_WORKSPACE, QN_ERR_HIP = -4, -5, -6
 QN_F32, QN_BF16 = 0, 1
 QN_OP_FWD, QN_OP_BWD_DX, QN_OP_LORA_GRADS, QN_OP_BWD_DX_DROPOUT = 0, 1, 2, 3
 QN_OP_FP8_FWD, QN_OP_FP8_BWD_DX = 4, 5
+QN_OP_MXFP4_FWD, QN_OP_MXFP4_BWD_DX = 6, 7
 QN_STATE_F32, QN_STATE_8BIT = 0, 1
-FP8_BLOCK, STATE_BLOCK = 128, 256
+FP8_BLOCK, STATE_BLOCK, MXFP4_GROUP = 128, 256, 32
 BLOCKSIZE, GROUP = 64, 256
 
 EXPORTS = ("qn_status_string", "nf4_codebook", "nf4_quantize", "dq_quantize_scales",
@@ -36,7 +37,9 @@ EXPORTS = ("qn_status_string", "nf4_codebook", "nf4_quantize", "dq_quantize_scal
            "qn_hbm_read_probe", "fp8_quantize_blocks", "fp8_quantize_rows", "fp8_dequant",
            "fp8_matmul", "fp8_linear_fwd", "fp8_linear_bwd_dx", "lora_adamw_table_bytes",
            "lora_adamw_table", "lora_grad_norm_workspace_bytes", "lora_grad_norm",
-           "lora_adamw_multi_step")
+           "lora_adamw_multi_step", "mxfp4_scale_bytes", "mxfp4_quantize", "mxfp4_dequant",
+           "mxfp4_pack_scales", "mxfp4_unpack_scales", "mxfp4_matmul", "mxfp4_linear_fwd",
+           "mxfp4_linear_bwd_dx")
 
 
 class QnError(RuntimeError):
@@ -55,6 +58,11 @@ class qn_weight(ctypes.Structure):
 
 
 class qn_fp8_weight(ctypes.Structure):
+    _fields_ = [("codes", ctypes.c_void_p), ("scale", ctypes.c_void_p),
+                ("N", ctypes.c_int64), ("K", ctypes.c_int64)]
+
+
+class qn_mxfp4_weight(ctypes.Structure):
     _fields_ = [("codes", ctypes.c_void_p), ("scale", ctypes.c_void_p),
                 ("N", ctypes.c_int64), ("K", ctypes.c_int64)]
 
@@ -129,6 +137,18 @@ def load_library():
         "lora_grad_norm_workspace_bytes": (sz, [pp]),
         "lora_grad_norm": (ctypes.c_int, [pp, vp, f32, vp, vp, sz, vp]),
         "lora_adamw_multi_step": (ctypes.c_int, [pp, vp, vp, f32, f32, f32, f32, f32, i32, vp]),
+    })
+    mp = ctypes.POINTER(qn_mxfp4_weight)
+    lin = [mp, vp, i64, vp, vp, i32, f32, vp, vp, vp, sz, vp]
+    sig.update({
+        "mxfp4_scale_bytes": (sz, [i64, i64]),
+        "mxfp4_quantize": (ctypes.c_int, [vp, i32, i64, i64, vp, vp, vp]),
+        "mxfp4_dequant": (ctypes.c_int, [vp, vp, i64, i64, i32, vp, vp]),
+        "mxfp4_pack_scales": (ctypes.c_int, [vp, i64, i64, vp, vp]),
+        "mxfp4_unpack_scales": (ctypes.c_int, [vp, i64, i64, vp, vp]),
+        "mxfp4_matmul": (ctypes.c_int, [mp, vp, vp, i64, vp, vp, sz, vp]),
+        "mxfp4_linear_fwd": (ctypes.c_int, lin),
+        "mxfp4_linear_bwd_dx": (ctypes.c_int, lin),
     })
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -782,21 +802,22 @@ def fp8_matmul(fw, codes, scale, transposed=False, out=None, ws=None, stream=Non
 
 def fp8_linear_fwd(fw, x, A, B, r, alpha, y=None, u_out=None, ws=None, stream=None):
     """y = Q(x) W^T + (alpha/r) (x A^T) B^T on an Fp8Weight (bf16 in/out)."""
-    return _fp8_linear("fp8_linear_fwd", QN_OP_FP8_FWD, fw, x, fw.K, fw.N, A, B, r, alpha, y,
+    return _scaled_linear("fp8_linear_fwd", QN_OP_FP8_FWD, fw, x, fw.K, fw.N, A, B, r, alpha, y,
                        u_out, ws, stream)
 
 
 def fp8_linear_bwd_dx(fw, dy, A, B, r, alpha, dx=None, t_out=None, ws=None, stream=None):
     """dx = Q(dy) W + (alpha/r) (dy B) A on an Fp8Weight (bf16 in/out)."""
-    return _fp8_linear("fp8_linear_bwd_dx", QN_OP_FP8_BWD_DX, fw, dy, fw.N, fw.K, A, B, r, alpha,
+    return _scaled_linear("fp8_linear_bwd_dx", QN_OP_FP8_BWD_DX, fw, dy, fw.N, fw.K, A, B, r, alpha,
                        dx, t_out, ws, stream)
 
 
-def _fp8_linear(fn, op, fw, x, L, n, A, B, r, alpha, out, low, ws, stream):
+def _scaled_linear(fn, op, fw, x, L, n, A, B, r, alpha, out, low, ws, stream):
+    """A layer on an Fp8Weight or an Mxfp4Weight."""
     torch = _torch()
     bf16, dev = torch.bfloat16, fw.device
     M = x.shape[0]
-    fwd = op == QN_OP_FP8_FWD
+    fwd = op in (QN_OP_FP8_FWD, QN_OP_MXFP4_FWD)
     _fit(x, bf16, M * L, dev, "x" if fwd else "dy")
     a = b = None
     if r and A is not None:
@@ -818,6 +839,139 @@ def _fp8_linear(fn, op, fw, x, L, n, A, B, r, alpha, out, low, ws, stream):
     _call(fn, dev, stream, fw.c_struct(), x.data_ptr(), M, a, b, r, alpha, out.data_ptr(),
           _addr(low), ws.data_ptr(), ws.numel())
     return out
+
+
+# --- microscaled 4-bit ------------------------------------------------------
+
+
+def mxfp4_scale_bytes(R, K):
+    """Bytes of the scales of an MXFP4 matrix [R, K]."""
+    return int(load_library().mxfp4_scale_bytes(R, K))
+
+
+class Mxfp4Weight:
+    """Device tensors of a microscaled 4-bit weight W[N, K]: codes
+    uint8[N, K/2] (E2M1, the even column in the low half of a byte) and scale
+    uint8[mxfp4_scale_bytes(N, K)], in tiles (mxfp4_pack_scales)."""
+
+    def __init__(self, codes, scale):
+        torch = _torch()
+        if codes.dim() != 2:
+            raise ValueError("codes: need a matrix [N, K / 2]")
+        N, K = self.N, self.K = codes.shape[0], 2 * codes.shape[1]
+        dev = self.device = codes.device
+        _dev(codes, torch.uint8, name="codes")
+        _fit(scale, torch.uint8, mxfp4_scale_bytes(N, K), dev, "scale")
+        self.codes, self.scale = codes, scale
+
+    def c_struct(self):
+        return qn_mxfp4_weight(self.codes.data_ptr(), self.scale.data_ptr(), self.N, self.K)
+
+
+def mxfp4_quantize(x, codes=None, scale=None, stream=None):
+    """E2M1 codes uint8[R, K/2] and scales uint8[mxfp4_scale_bytes(R, K)] of a
+    fp32 or bf16 matrix [R, K], one power of two per 32 columns of a row."""
+    torch = _torch()
+    if x.dim() != 2 or x.dtype not in (torch.float32, torch.bfloat16):
+        raise ValueError("mxfp4_quantize: need a float32 or bfloat16 matrix")
+    _dev(x, x.dtype, name="x")
+    R, K = x.shape
+    if codes is None:
+        codes = _new(stream, torch.uint8, x.device, R, K // 2)
+    else:
+        _fit(codes, torch.uint8, R * K // 2, x.device, "codes")
+    size = mxfp4_scale_bytes(R, K)
+    if scale is None:
+        scale = _new(stream, torch.uint8, x.device, size)
+    else:
+        _fit(scale, torch.uint8, size, x.device, "scale")
+    _call("mxfp4_quantize", x.device, stream, x.data_ptr(),
+          QN_F32 if x.dtype == torch.float32 else QN_BF16, R, K, codes.data_ptr(),
+          scale.data_ptr())
+    return codes, scale
+
+
+def mxfp4_quantize_weight(w, stream=None):
+    """The Mxfp4Weight of a fp32 or bf16 matrix [N, K] (mxfp4_quantize)."""
+    return Mxfp4Weight(*mxfp4_quantize(w, stream=stream))
+
+
+def mxfp4_pack_scales(rows, scale=None, stream=None):
+    """Scales uint8[R, K/32], a byte per 32 columns of a row, as tiles."""
+    torch = _torch()
+    if rows.dim() != 2:
+        raise ValueError("rows: need a matrix [R, K / 32]")
+    _dev(rows, torch.uint8, name="rows")
+    R, K = rows.shape[0], rows.shape[1] * MXFP4_GROUP
+    size = mxfp4_scale_bytes(R, K)
+    if scale is None:
+        scale = _new(stream, torch.uint8, rows.device, size)
+    else:
+        _fit(scale, torch.uint8, size, rows.device, "scale")
+    _call("mxfp4_pack_scales", rows.device, stream, rows.data_ptr(), R, K, scale.data_ptr())
+    return scale
+
+
+def mxfp4_unpack_scales(scale, R, K, rows=None, stream=None):
+    """Scales uint8[R, K/32], a byte per 32 columns of a row, of tiles."""
+    torch = _torch()
+    dev = scale.device
+    _dev(scale, torch.uint8, mxfp4_scale_bytes(R, K), "scale")
+    if rows is None:
+        rows = _new(stream, torch.uint8, dev, R, K // MXFP4_GROUP)
+    else:
+        _fit(rows, torch.uint8, R * (K // MXFP4_GROUP), dev, "rows")
+    _call("mxfp4_unpack_scales", dev, stream, scale.data_ptr(), R, K, rows.data_ptr())
+    return rows
+
+
+def mxfp4_dequant(mw, out_dtype=None, out=None, stream=None):
+    """The values of an Mxfp4Weight as bf16 or fp32 [N, K]."""
+    torch = _torch()
+    out_dtype = out_dtype or torch.bfloat16
+    if out_dtype not in (torch.float32, torch.bfloat16):
+        raise ValueError("mxfp4_dequant: out_dtype must be float32 or bfloat16")
+    dev = mw.device
+    if out is None:
+        out = _new(stream, out_dtype, dev, mw.N, mw.K)
+    else:
+        _fit(out, out_dtype, mw.N * mw.K, dev, "out")
+    _call("mxfp4_dequant", dev, stream, mw.codes.data_ptr(), mw.scale.data_ptr(), mw.N, mw.K,
+          QN_BF16 if out_dtype == torch.bfloat16 else QN_F32, out.data_ptr())
+    return out
+
+
+def mxfp4_matmul(mw, codes, scale, out=None, ws=None, stream=None):
+    """x W^T (bf16[M, N]) of x [M, K] from mxfp4_quantize."""
+    torch = _torch()
+    if codes.dim() != 2 or 2 * codes.shape[1] != mw.K:
+        raise ValueError(f"codes: need [M, {mw.K // 2}]")
+    M, dev = codes.shape[0], mw.device
+    _fit(codes, torch.uint8, M * mw.K // 2, dev, "codes")
+    _fit(scale, torch.uint8, mxfp4_scale_bytes(M, mw.K), dev, "scale")
+    if out is None:
+        out = _new(stream, torch.bfloat16, dev, M, mw.N)
+    else:
+        _fit(out, torch.bfloat16, M * mw.N, dev, "out")
+    if ws is None:
+        ws = _new(stream, torch.uint8, dev, qn_workspace_bytes(QN_OP_MXFP4_FWD, M, mw.N, mw.K, 0))
+    else:
+        _fit(ws, torch.uint8, ws.numel(), dev, "ws")
+    _call("mxfp4_matmul", dev, stream, mw.c_struct(), codes.data_ptr(), scale.data_ptr(), M,
+          out.data_ptr(), ws.data_ptr(), ws.numel())
+    return out
+
+
+def mxfp4_linear_fwd(mw, x, A, B, r, alpha, y=None, u_out=None, ws=None, stream=None):
+    """y = Q(x) W^T + (alpha/r) (x A^T) B^T on an Mxfp4Weight (bf16 in/out)."""
+    return _scaled_linear("mxfp4_linear_fwd", QN_OP_MXFP4_FWD, mw, x, mw.K, mw.N, A, B, r, alpha, y,
+                       u_out, ws, stream)
+
+
+def mxfp4_linear_bwd_dx(mw, dy, A, B, r, alpha, dx=None, t_out=None, ws=None, stream=None):
+    """dx = Q8(dy) W + (alpha/r) (dy B) A on an Mxfp4Weight (bf16 in/out)."""
+    return _scaled_linear("mxfp4_linear_bwd_dx", QN_OP_MXFP4_BWD_DX, mw, dy, mw.N, mw.K, A, B, r,
+                       alpha, dx, t_out, ws, stream)
 
 
 # --- AdamW over many matrices ----------------------------------------------

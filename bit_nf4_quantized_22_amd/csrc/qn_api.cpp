@@ -353,6 +353,133 @@ int fp8_linear(bool bwd, const qn_fp8_weight* w, const qn_bf16* in, int64_t M, c
   return hip_status(qn::launch_fp8_gemm(v, codes, scale, M, act, bwd ? A : B, r, bwd, out, split, s));
 }
 
+// --- microscaled 4-bit ---------------------------------------------------
+
+// 32-bit offsets within a tile; tiles of scales and blocks below 2^31.
+constexpr int64_t kMxMaxDim = int64_t{1} << 23;
+
+bool mx_size_ok(int64_t R, int64_t K) {
+  return R >= 0 && K >= 0 && K % 32 == 0 && K <= kMxMaxDim && R <= (int64_t{1} << 26) &&
+         qn::mx_tiles(R, 32) * qn::mx_tiles(K, 256) < (int64_t{1} << 24);
+}
+
+int check_mx_weight(const qn_mxfp4_weight* w, qn::MxView& v) {
+  if (!w || !w->codes || !w->scale) return QN_ERR_NULL;
+  if (w->N <= 0 || w->K <= 0 || w->N % 16 != 0 || w->N > kMxMaxDim || !mx_size_ok(w->N, w->K))
+    return QN_ERR_SHAPE;
+  if (!aligned(w->codes, 16) || !aligned(w->scale, 4)) return QN_ERR_ALIGN;
+  v = qn::MxView{w->codes, w->scale, w->N, w->K};
+  return QN_OK;
+}
+
+// Workspace of a batch [M, L]: codes and their scales, backward the turned
+// weight and its scales, partial sums of the LoRA projection and its scaled
+// sum in padded rows, partial sums of a split contraction.
+struct MxWs {
+  size_t scale, turned, tscale, part, act, split, total;
+  int64_t bytes;  // of a row of codes
+};
+
+MxWs mx_ws(bool bwd, int64_t M, int64_t N, int64_t K, int32_t r) {
+  MxWs f{};
+  if (M <= 0 || N <= 0 || K <= 0) return f;
+  const int64_t L = bwd ? N : K, cols = bwd ? K : N;
+  const size_t m = static_cast<size_t>(M);
+  f.bytes = bwd ? qn::mx_tiles(L, 128) * 128 : L / 2;
+  auto tiles = [&](int64_t rows) {
+    const int64_t n = bwd ? qn::mx_tiles(rows, 64) * qn::mx_tiles(L, 128)
+                          : qn::mx_tiles(rows, 32) * qn::mx_tiles(L, 256);
+    return static_cast<size_t>(n) * 256;
+  };
+  f.scale = round_up(m * static_cast<size_t>(f.bytes), 256);
+  f.turned = f.scale + tiles(M);
+  f.tscale = f.turned + (bwd ? static_cast<size_t>(K * f.bytes) : 0);
+  f.tscale = round_up(f.tscale, 256);
+  f.part = f.tscale + (bwd ? tiles(K) : 0);
+  f.act = f.part;
+  const int slices = !bwd && M <= qn::kFp8DecodeM ? qn::fp8_decode_slices(L)
+                                                  : qn::fp8_project_slices(M, L);
+  if (r > 0)
+    f.act += round_up(m * static_cast<size_t>(r) * 4 * static_cast<size_t>(slices), 256);
+  f.split = f.act;
+  if (r > 0 && (bwd || M > qn::kFp8DecodeM))
+    f.split += round_up(m * static_cast<size_t>(qn::fp8_lora_pitch(r)) * 2, 256);
+  f.total = f.split;
+  const int splits = bwd || !qn::mx_few(M, N, K) ? qn::mx_gemm_splits(M, cols, f.bytes) : 1;
+  if (splits > 1)
+    f.total += m * static_cast<size_t>(cols) * 4 * static_cast<size_t>(splits);
+  return f;
+}
+
+// Batches of the products: the launches over M rows have less than 2^32
+// threads, and the tiles of scales are counted in 32 bits.
+bool mx_rows_ok(int64_t M, int64_t N, int64_t K) {
+  return fp8_rows_ok(M, N) && fp8_rows_ok(M, K);
+}
+
+// Forward (bwd false: in = x [M, K], down = A, up = B) or backward to the
+// input (in = dy [M, N], down = B read in place, up = A).
+int mx_linear(bool bwd, const qn_mxfp4_weight* w, const qn_bf16* in, int64_t M, const qn_bf16* A,
+              const qn_bf16* B, int32_t r, float alpha, qn_bf16* out, qn_bf16* low_out, void* ws,
+              size_t ws_bytes, void* stream) {
+  qn::MxView v;
+  int st = check_mx_weight(w, v);
+  if (st != QN_OK) return st;
+  const int64_t L = bwd ? v.N : v.K;
+  if (r < 0 || !mx_rows_ok(M, v.N, v.K)) return QN_ERR_SHAPE;
+  if (r > kMaxRank) return QN_ERR_UNSUPPORTED;
+  if (M == 0) return QN_OK;
+  if ((st = adapter_rank(r, A, B, r)) != QN_OK) return st;
+  if (!in || !out) return QN_ERR_NULL;
+  if (!aligned(in, 16) || !aligned(out, 16) || (r > 0 && (!aligned(A, 2) || !aligned(B, 2))) ||
+      !aligned(low_out, 2))
+    return QN_ERR_ALIGN;
+  const MxWs f = mx_ws(bwd, M, v.N, v.K, r);
+  if (!ws || ws_bytes < f.total) return QN_ERR_WORKSPACE;
+  if (!aligned(ws, 16)) return QN_ERR_ALIGN;
+  hipStream_t s = as_stream(stream);
+  (void)hipGetLastError();
+  const float ls = r > 0 ? alpha / static_cast<float>(r) : 0.0f;
+  qn_bf16* low = r > 0 ? low_out : nullptr;
+  uint8_t* codes = static_cast<uint8_t*>(ws);
+  uint8_t* scale = codes + f.scale;
+  float* part = reinterpret_cast<float*>(codes + f.part);
+  uint16_t* act = reinterpret_cast<uint16_t*>(codes + f.act);
+  float* split = f.total > f.split ? reinterpret_cast<float*>(codes + f.split) : nullptr;
+  if (!bwd && M == 1) {
+    const bool own_u = qn::mx_token_self_u(v, r);
+    if (!own_u && qn::launch_mx_decode_project(in, 1, L, A, r, nullptr, nullptr, part, s) !=
+                      hipSuccess)
+      return QN_ERR_HIP;
+    return hip_status(qn::launch_mx_token(v, in, A, own_u ? nullptr : part,
+                                          qn::fp8_decode_slices(L), B, r, ls, out, low, s));
+  }
+  const bool decode = !bwd && M <= qn::kFp8DecodeM, few = !bwd && qn::mx_few(M, v.N, v.K);
+  const int m32 = static_cast<int>(few ? M : 0);
+  hipError_t e = r == 0   ? qn::launch_mx_rows(in, M, L, bwd, codes, scale, s)
+                 : decode ? qn::launch_mx_decode_project(in, m32, L, A, r, codes, scale, part, s)
+                          : qn::launch_mx_rows_project(in, M, L, bwd ? B : A, r, bwd, codes, scale,
+                                                       part, s);
+  if (e != hipSuccess) return QN_ERR_HIP;
+  if (r > 0 && !decode &&
+      qn::launch_fp8_project_sum(part, qn::fp8_project_slices(M, L), M, r, ls, act, low, s) !=
+          hipSuccess)
+    return QN_ERR_HIP;
+  if (few)
+    return hip_status(qn::launch_mx_decode(v, codes, scale, m32, part, qn::fp8_decode_slices(L),
+                                           act, B, r, ls, out, low, s));
+  const uint8_t* wc = v.codes;
+  const uint8_t* wsc = v.scale;
+  if (bwd) {
+    if (qn::launch_mx_turn(v, codes + f.turned, codes + f.tscale, s) != hipSuccess)
+      return QN_ERR_HIP;
+    wc = codes + f.turned;
+    wsc = codes + f.tscale;
+  }
+  return hip_status(qn::launch_mx_gemm(wc, wsc, v.N, v.K, f.bytes, codes, scale, M, act,
+                                       bwd ? A : B, r, bwd, out, split, s));
+}
+
 bool adamw_hyper_ok(float lr, float beta1, float beta2, float eps, float weight_decay) {
   return lr >= 0.0f && beta1 >= 0.0f && beta1 < 1.0f && beta2 >= 0.0f && beta2 < 1.0f &&
          eps > 0.0f && weight_decay >= 0.0f;
@@ -570,6 +697,8 @@ size_t qn_workspace_bytes(int32_t op, int64_t M, int64_t N, int64_t K, int32_t r
     case QN_OP_BWD_DX_DROPOUT: return bwd_drop_ws(M, N, K, r);
     case QN_OP_FP8_FWD: return fp8_ws(false, M, N, K, r).total;
     case QN_OP_FP8_BWD_DX: return fp8_ws(true, M, N, K, r).total;
+    case QN_OP_MXFP4_FWD: return mx_ws(false, M, N, K, r).total;
+    case QN_OP_MXFP4_BWD_DX: return mx_ws(true, M, N, K, r).total;
     default: return 0;
   }
 }
@@ -725,6 +854,87 @@ int fp8_linear_bwd_dx(const qn_fp8_weight* w, const qn_bf16* dy, int64_t M, cons
                       const qn_bf16* B, int32_t r, float alpha, qn_bf16* dx, qn_bf16* t_out,
                       void* ws, size_t ws_bytes, void* stream) {
   return fp8_linear(true, w, dy, M, A, B, r, alpha, dx, t_out, ws, ws_bytes, stream);
+}
+
+size_t mxfp4_scale_bytes(int64_t R, int64_t K) {
+  if (!mx_size_ok(R, K)) return 0;
+  return static_cast<size_t>(qn::mx_tiles(R, 32) * qn::mx_tiles(K, 256)) * 256;
+}
+
+int mxfp4_quantize(const void* x, int32_t dtype, int64_t R, int64_t K, uint8_t* codes,
+                   uint8_t* scale, void* stream) {
+  if (dtype != QN_F32 && dtype != QN_BF16) return QN_ERR_UNSUPPORTED;
+  if (!mx_size_ok(R, K)) return QN_ERR_SHAPE;
+  if (R == 0 || K == 0) return QN_OK;
+  if (!x || !codes || !scale) return QN_ERR_NULL;
+  if (!aligned(x, 16) || !aligned(codes, 16) || !aligned(scale, 4)) return QN_ERR_ALIGN;
+  (void)hipGetLastError();
+  return hip_status(
+      qn::launch_mx_quantize(x, dtype == QN_BF16, R, K, codes, scale, as_stream(stream)));
+}
+
+int mxfp4_dequant(const uint8_t* codes, const uint8_t* scale, int64_t R, int64_t K,
+                  int32_t out_dtype, void* out, void* stream) {
+  if (out_dtype != QN_F32 && out_dtype != QN_BF16) return QN_ERR_UNSUPPORTED;
+  if (!mx_size_ok(R, K)) return QN_ERR_SHAPE;
+  if (R == 0 || K == 0) return QN_OK;
+  if (!codes || !scale || !out) return QN_ERR_NULL;
+  if (!aligned(codes, 16) || !aligned(scale, 4) || !aligned(out, 16)) return QN_ERR_ALIGN;
+  (void)hipGetLastError();
+  return hip_status(qn::launch_mx_dequant(qn::MxView{codes, scale, R, K}, out_dtype == QN_BF16, out,
+                                          as_stream(stream)));
+}
+
+static int mx_scales(bool pack, const uint8_t* in, int64_t R, int64_t K, uint8_t* out,
+                     void* stream) {
+  if (!mx_size_ok(R, K)) return QN_ERR_SHAPE;
+  if (R == 0 || K == 0) return QN_OK;
+  if (!in || !out) return QN_ERR_NULL;
+  if (!aligned(pack ? out : in, 4)) return QN_ERR_ALIGN;
+  (void)hipGetLastError();
+  return hip_status(qn::launch_mx_scales(pack, in, R, K, out, as_stream(stream)));
+}
+
+int mxfp4_pack_scales(const uint8_t* rows, int64_t R, int64_t K, uint8_t* scale, void* stream) {
+  return mx_scales(true, rows, R, K, scale, stream);
+}
+
+int mxfp4_unpack_scales(const uint8_t* scale, int64_t R, int64_t K, uint8_t* rows, void* stream) {
+  return mx_scales(false, scale, R, K, rows, stream);
+}
+
+int mxfp4_matmul(const qn_mxfp4_weight* w, const uint8_t* x, const uint8_t* xscale, int64_t M,
+                 qn_bf16* out, void* ws, size_t ws_bytes, void* stream) {
+  qn::MxView v;
+  if (int st = check_mx_weight(w, v); st != QN_OK) return st;
+  if (!mx_rows_ok(M, v.N, v.K)) return QN_ERR_SHAPE;
+  if (M == 0) return QN_OK;
+  if (!x || !xscale || !out) return QN_ERR_NULL;
+  if (!aligned(x, 16) || !aligned(xscale, 4) || !aligned(out, 16)) return QN_ERR_ALIGN;
+  const MxWs f = mx_ws(false, M, v.N, v.K, 0);
+  if (!ws || ws_bytes < f.total) return QN_ERR_WORKSPACE;
+  if (!aligned(ws, 16)) return QN_ERR_ALIGN;
+  float* split =
+      f.total > f.split ? reinterpret_cast<float*>(static_cast<char*>(ws) + f.split) : nullptr;
+  (void)hipGetLastError();
+  hipStream_t s = as_stream(stream);
+  if (qn::mx_few(M, v.N, v.K))
+    return hip_status(qn::launch_mx_decode(v, x, xscale, static_cast<int>(M), nullptr, 0, nullptr,
+                                           nullptr, 0, 0.0f, out, nullptr, s));
+  return hip_status(qn::launch_mx_gemm(v.codes, v.scale, v.N, v.K, f.bytes, x, xscale, M, nullptr,
+                                       nullptr, 0, false, out, split, s));
+}
+
+int mxfp4_linear_fwd(const qn_mxfp4_weight* w, const qn_bf16* x, int64_t M, const qn_bf16* A,
+                     const qn_bf16* B, int32_t r, float alpha, qn_bf16* y, qn_bf16* u_out, void* ws,
+                     size_t ws_bytes, void* stream) {
+  return mx_linear(false, w, x, M, A, B, r, alpha, y, u_out, ws, ws_bytes, stream);
+}
+
+int mxfp4_linear_bwd_dx(const qn_mxfp4_weight* w, const qn_bf16* dy, int64_t M, const qn_bf16* A,
+                        const qn_bf16* B, int32_t r, float alpha, qn_bf16* dx, qn_bf16* t_out,
+                        void* ws, size_t ws_bytes, void* stream) {
+  return mx_linear(true, w, dy, M, A, B, r, alpha, dx, t_out, ws, ws_bytes, stream);
 }
 
 size_t lora_adamw_table_bytes(const qn_adamw_tensor* t, int32_t count) {

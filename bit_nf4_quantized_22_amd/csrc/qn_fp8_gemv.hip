@@ -21,14 +21,13 @@
 // call is one launch.  More tokens: x's codes and u's partial sums come from
 // a launch before.
 
+#include "qn_decode.h"
 #include "qn_fp8.h"
 #include "qn_launch.h"
 
 namespace qn {
 
 namespace {
-
-constexpr int kMaxRank = 128;
 
 // This lane's 32 bytes of block b of a row, zeros behind the row's end.
 struct Bytes32 {
@@ -43,39 +42,6 @@ __device__ __forceinline__ Bytes32 row_bytes(const uint8_t* row, int64_t b, int6
   return v;
 }
 
-// LoRA-up term of 16 tokens: acc += B[n rows] us^T, us rows of `pitch` bf16
-// (the two parts of 32 ranks at a time, zero past r) at sus, B's fragments
-// already in registers.
-template <int kFrags>
-__device__ __forceinline__ f32x4_t lora_up(f32x4_t acc, const uint4 (&bf)[kFrags],
-                                           const uint16_t* sus, int pitch, int r, int li, int lg) {
-#pragma unroll
-  for (int q = 0; q < kFrags; ++q)
-    if (32 * q < r) {
-      const uint16_t* p = sus + li * pitch + 64 * q + 8 * lg;
-      acc = mfma_bf16_32(bf[q], *reinterpret_cast<const uint4*>(p), acc);
-      acc = mfma_bf16_32(bf[q], *reinterpret_cast<const uint4*>(p + 32), acc);
-    }
-  return acc;
-}
-
-// Rank j of a row of us = the two parts of v.
-__device__ __forceinline__ void store_us(uint16_t* row, int j, float v) {
-  const Bf16Split p = split_bf16x2(v, 0.0f);
-  uint16_t* at = row + (j & ~31) * 2 + (j & 31);
-  at[0] = static_cast<uint16_t>(p.hi & 0xFFFF);
-  at[32] = static_cast<uint16_t>(p.lo & 0xFFFF);
-}
-
-__device__ __forceinline__ void store_columns(uint16_t* y, f32x4_t acc) {
-  *reinterpret_cast<uint2*>(y) =
-      make_uint2(pack_bf16x2(acc[0], acc[1]), pack_bf16x2(acc[2], acc[3]));
-}
-
-// Where one token's u comes from: no adapter, x A^T computed here (r <= 16),
-// or `slices` partial sums of it.
-enum TokenU { kNoAdapter, kOwnU, kGivenU };
-
 template <int kU, int kWaves>
 __global__ __launch_bounds__(64 * kWaves) void fp8_token_kernel(
     const uint8_t* __restrict__ w, const float* __restrict__ ws, int64_t N, int64_t K,
@@ -83,7 +49,7 @@ __global__ __launch_bounds__(64 * kWaves) void fp8_token_kernel(
     const float* __restrict__ part, int slices, const uint16_t* __restrict__ B, int r, bool vec_b,
     float lora_scale, uint16_t* __restrict__ y, uint16_t* __restrict__ u_out) {
   constexpr int kThreads = 64 * kWaves, kAhead = 2;
-  constexpr int kFrags = kU == kGivenU ? kMaxRank / 32 : 1;
+  constexpr int kFrags = kU == kGivenU ? kDecodeMaxRank / 32 : 1;
   __shared__ f32x4_t s_acc[kWaves][4];
   __shared__ float s_u[kU == kNoAdapter ? 1 : kThreads];  // kOwnU: [wave][16 ranks]
   __shared__ __attribute__((aligned(16))) uint16_t s_us[64 * kFrags];
@@ -212,8 +178,8 @@ __global__ __launch_bounds__(64 * kWaves) void fp8_decode_kernel(
   constexpr int kTiles = kMT * kRows;
   static_assert(kTiles <= kWaves, "a wave finishes 16 columns of 16 tokens");
   __shared__ f32x4_t s_acc[kWaves][kTiles][64];
-  __shared__ float s_u[kMT == 1 ? kFp8DecodeM * kMaxRank : 1];
-  __shared__ __attribute__((aligned(16))) uint16_t s_us[kMT == 1 ? 32 * kMaxRank : 8];
+  __shared__ float s_u[kMT == 1 ? kFp8DecodeM * kDecodeMaxRank : 1];
+  __shared__ __attribute__((aligned(16))) uint16_t s_us[kMT == 1 ? 32 * kDecodeMaxRank : 8];
   const int t = threadIdx.x, lane = t & 63;
   const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
   const int li = lane & 15, lg = lane >> 4;
@@ -270,10 +236,10 @@ __global__ __launch_bounds__(64 * kWaves) void fp8_decode_kernel(
   // wave 0 .. kTiles - 1 finishes token tile wave % kMT, row tile wave / kMT
   const int64_t nw = n0 + 16 * (wave / kMT);
   const bool finish = wave < kTiles && nw < N;
-  uint4 bf[kMaxRank / 32];
+  uint4 bf[kDecodeMaxRank / 32];
   if (finish) {
 #pragma unroll
-    for (int q = 0; q < kMaxRank / 32; ++q) {
+    for (int q = 0; q < kDecodeMaxRank / 32; ++q) {
       bf[q] = make_uint4(0, 0, 0, 0);
       if (32 * q < r)
         bf[q] = load_bf16x8(B + (nw + li) * r + 32 * q + 8 * lg, r - 32 * q - 8 * lg, vec_b);

@@ -191,6 +191,63 @@ hipError_t launch_fp8_gemm(const Fp8View& w, const uint8_t* x, const float* xs, 
                            const uint16_t* act, const uint16_t* lw, int r, bool bwd, uint16_t* out,
                            float* part, hipStream_t st);
 
+// A weight in microscaled E2M1 codes.
+struct MxView {
+  const uint8_t* codes;  // [N, K / 2]
+  const uint8_t* scale;  // tiles of 32 rows x 256 columns, [ceil(K / 256)][ceil(N / 32)][256]
+  int64_t N, K;          // multiples of 16 and 32
+};
+
+// Tiles of t that cover n.
+constexpr int64_t mx_tiles(int64_t n, int64_t t) { return (n + t - 1) / t; }
+
+// Microscaled 4-bit (see the mxfp4_* entries of the C ABI).  x [R, K].
+hipError_t launch_mx_quantize(const void* x, bool bf16, int64_t R, int64_t K, uint8_t* codes,
+                              uint8_t* scale, hipStream_t st);
+hipError_t launch_mx_dequant(const MxView& w, bool out_bf16, void* out, hipStream_t st);
+// Scales from rows [R, K / 32] to tiles (pack) or back.
+hipError_t launch_mx_scales(bool pack, const uint8_t* in, int64_t R, int64_t K, uint8_t* out,
+                            hipStream_t st);
+// A batch x [M, L] in codes: forward E2M1 [M, L / 2] with tiles as a weight's,
+// backward E4M3 [M, mx_tiles(L, 128) * 128] with tiles of 64 rows x 128 columns.
+// The second form also gives fp8_project_slices(M, L) partial sums
+// part[slices][M][r] of the LoRA projection x P^T (P = A [r, L] forward, B [L, r]
+// backward; r >= 1).
+hipError_t launch_mx_rows(const uint16_t* x, int64_t M, int64_t L, bool bwd, uint8_t* codes,
+                          uint8_t* scale, hipStream_t st);
+hipError_t launch_mx_rows_project(const uint16_t* x, int64_t M, int64_t L, const uint16_t* P, int r,
+                                  bool bwd, uint8_t* codes, uint8_t* scale, float* part,
+                                  hipStream_t st);
+// The same of M <= kFp8DecodeM tokens, forward, in fp8_decode_slices(L) slices.
+hipError_t launch_mx_decode_project(const uint16_t* x, int M, int64_t L, const uint16_t* A, int r,
+                                    uint8_t* codes, uint8_t* scale, float* part, hipStream_t st);
+// W^T in E5M2 codes wt [K, mx_tiles(N, 128) * 128] with tiles ts of 64 rows x
+// 128 columns, for the backward's product.
+hipError_t launch_mx_turn(const MxView& w, uint8_t* wt, uint8_t* ts, hipStream_t st);
+// y [M, N] = x W^T + (lora_scale u) B^T for mx_few(..) tokens in codes, u given as
+// to launch_fp8_decode.
+bool mx_few(int64_t M, int64_t N, int64_t K);
+hipError_t launch_mx_decode(const MxView& w, const uint8_t* x, const uint8_t* xs, int M,
+                            const float* part, int slices, const uint16_t* act, const uint16_t* B,
+                            int r, float lora_scale, uint16_t* y, uint16_t* u_out, hipStream_t st);
+// One token, quantised by the product's workgroups; u = x A^T given as slices
+// partial sums, or (part == nullptr, where mx_token_self_u holds) computed by
+// them too.
+bool mx_token_self_u(const MxView& w, int r);
+hipError_t launch_mx_token(const MxView& w, const uint16_t* x, const uint16_t* A, const float* part,
+                           int slices, const uint16_t* B, int r, float lora_scale, uint16_t* y,
+                           uint16_t* u_out, hipStream_t st);
+// out [M, N] = x w^T + act B^T (w, x E2M1 codes, bytes = K / 2), or with bwd
+// out [M, K] = x w^T + act A (w the turned weight, x E4M3 codes, bytes a multiple
+// of 128); act as launch_fp8_project_sum gives it (r == 0: no LoRA term).  The
+// contraction is split over mx_gemm_splits(M, ncols, bytes) workgroups where the
+// tiles are few and part, fp32 [splits][M][ncols], is given.
+int mx_gemm_splits(int64_t M, int64_t ncols, int64_t bytes);
+hipError_t launch_mx_gemm(const uint8_t* w, const uint8_t* ws, int64_t N, int64_t K, int64_t bytes,
+                          const uint8_t* x, const uint8_t* xs, int64_t M, const uint16_t* act,
+                          const uint16_t* lw, int r, bool bwd, uint16_t* out, float* part,
+                          hipStream_t st);
+
 // LoRA merge: out[N, K] = bf16(dequant(W) + s B A) (A [r, K], B [N, r]).
 hipError_t launch_merge(const WeightView& w, const uint16_t* A, const uint16_t* B, int r, float s,
                         uint16_t* out, hipStream_t st);
