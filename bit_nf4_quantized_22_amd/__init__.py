@@ -25,6 +25,7 @@ QN_OP_FWD, QN_OP_BWD_DX, QN_OP_LORA_GRADS, QN_OP_BWD_DX_DROPOUT = 0, 1, 2, 3
 QN_OP_FP8_FWD, QN_OP_FP8_BWD_DX = 4, 5
 QN_OP_MXFP4_FWD, QN_OP_MXFP4_BWD_DX = 6, 7
 QN_STATE_F32, QN_STATE_8BIT = 0, 1
+QN_MUON_ORIGINAL, QN_MUON_MATCH_RMS = 0, 1
 FP8_BLOCK, STATE_BLOCK, MXFP4_GROUP = 128, 256, 32
 BLOCKSIZE, GROUP = 64, 256
 
@@ -39,7 +40,8 @@ EXPORTS = ("qn_status_string", "nf4_codebook", "nf4_quantize", "dq_quantize_scal
            "lora_adamw_table", "lora_grad_norm_workspace_bytes", "lora_grad_norm",
            "lora_adamw_multi_step", "mxfp4_scale_bytes", "mxfp4_quantize", "mxfp4_dequant",
            "mxfp4_pack_scales", "mxfp4_unpack_scales", "mxfp4_matmul", "mxfp4_linear_fwd",
-           "mxfp4_linear_bwd_dx")
+           "mxfp4_linear_bwd_dx", "lora_muon_table_bytes", "lora_muon_table",
+           "lora_muon_workspace_bytes", "lora_muon_multi_step")
 
 
 class QnError(RuntimeError):
@@ -77,6 +79,24 @@ class qn_adamw_tensor(ctypes.Structure):
 class qn_adamw_plan(ctypes.Structure):
     _fields_ = [("chunks", ctypes.c_int64), ("bytes", ctypes.c_int64),
                 ("grad_dtype", ctypes.c_int32), ("state", ctypes.c_int32)]
+
+
+class qn_muon_tensor(ctypes.Structure):
+    _fields_ = [("p", ctypes.c_void_p), ("g", ctypes.c_void_p), ("m", ctypes.c_void_p),
+                ("p_bf16", ctypes.c_void_p), ("rows", ctypes.c_int64), ("cols", ctypes.c_int64)]
+
+
+class qn_muon_plan(ctypes.Structure):
+    _fields_ = [("matrices", ctypes.c_int64 * 4), ("chunks", ctypes.c_int64 * 4),
+                ("bytes", ctypes.c_int64), ("ws_bytes", ctypes.c_int64),
+                ("grad_dtype", ctypes.c_int32)]
+
+
+class qn_muon_step(ctypes.Structure):
+    _fields_ = [("lr", ctypes.c_float), ("momentum", ctypes.c_float),
+                ("weight_decay", ctypes.c_float), ("eps", ctypes.c_float),
+                ("ns", ctypes.c_double * 3), ("ns_steps", ctypes.c_int32),
+                ("nesterov", ctypes.c_int32), ("adjust", ctypes.c_int32)]
 
 
 _lib = None
@@ -149,6 +169,13 @@ def load_library():
         "mxfp4_matmul": (ctypes.c_int, [mp, vp, vp, i64, vp, vp, sz, vp]),
         "mxfp4_linear_fwd": (ctypes.c_int, lin),
         "mxfp4_linear_bwd_dx": (ctypes.c_int, lin),
+    })
+    tp, pp, sp = (ctypes.POINTER(c) for c in (qn_muon_tensor, qn_muon_plan, qn_muon_step))
+    sig.update({
+        "lora_muon_table_bytes": (sz, [tp, i32]),
+        "lora_muon_table": (ctypes.c_int, [tp, i32, i32, vp, sz, pp]),
+        "lora_muon_workspace_bytes": (sz, [pp]),
+        "lora_muon_multi_step": (ctypes.c_int, [pp, vp, sp, vp, sz, vp]),
     })
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -1071,3 +1098,82 @@ def lora_adamw_multi_step(table, step, lr=2e-4, betas=(0.9, 0.999), eps=1e-8, we
         _fit(grad_scale, torch.float32, 1, dev, "grad_scale")
     _call("lora_adamw_multi_step", dev, stream, table.plan, table.table.data_ptr(),
           _addr(grad_scale), lr, betas[0], betas[1], eps, weight_decay, step)
+
+
+# --- Muon over many matrices -------------------------------------------------
+
+
+class MuonTable:
+    """The device table of lora_muon_multi_step over the given matrices, which it
+    keeps alive (their memory is updated in place)."""
+
+    def __init__(self, plan, table, device, tensors):
+        self.plan, self.table, self.device, self.tensors = plan, table, device, tensors
+
+
+def lora_muon_table(ps, gs, ms, p_bf16s=None):
+    """Table over matrices p (fp32, the smaller side at most 128) with gradients g
+    (all fp32 or all bf16) and momenta m (fp32, zeros at the start).  p_bf16s, if
+    given, holds bf16 matrices (or None) that receive the new p.  Build it once;
+    changed addresses or sizes need a new one."""
+    torch = _torch()
+    lib = load_library()
+    n = len(ps)
+    if not n:
+        raise ValueError("lora_muon_table: no matrices")
+    for col, name in zip((ps, gs, ms), ("p", "g", "m")):
+        if any(t is None for t in col):
+            raise ValueError(f"{name}: missing")
+    cols = [list(c) for c in (ps, gs, ms, [None] * n if p_bf16s is None else p_bf16s)]
+    if any(len(c) != n for c in cols):
+        raise ValueError("lora_muon_table: lists of different lengths")
+    gt = gs[0].dtype
+    if gt not in (torch.float32, torch.bfloat16):
+        raise ValueError("lora_muon_table: gradients must be float32 or bfloat16")
+    dev = ps[0].device
+    _dev(ps[0], torch.float32, name="p")
+    arr = (qn_muon_tensor * n)()
+    for i, row in enumerate(zip(*cols)):
+        if row[0].dim() != 2:
+            raise ValueError("p: need matrices")
+        for t, dt, name in zip(row, (torch.float32, gt, torch.float32, torch.bfloat16),
+                               ("p", "g", "m", "p_bf16")):
+            if t is not None:
+                _fit(t, dt, row[0].numel(), dev, name)
+                if t.shape != row[0].shape:
+                    raise ValueError(f"{name}: shape {tuple(t.shape)}, p has "
+                                     f"{tuple(row[0].shape)}")
+        arr[i] = qn_muon_tensor(*[_addr(t) for t in row], *row[0].shape)
+    size = lib.lora_muon_table_bytes(arr, n)
+    host = torch.empty(max(size, 1), dtype=torch.uint8)
+    plan = qn_muon_plan()
+    _check("lora_muon_table", lib.lora_muon_table(
+        arr, n, QN_F32 if gt == torch.float32 else QN_BF16, host.data_ptr(), size,
+        ctypes.byref(plan)))
+    return MuonTable(plan, host.to(dev), dev, cols)
+
+
+def lora_muon_workspace_bytes(table):
+    return int(load_library().lora_muon_workspace_bytes(table.plan))
+
+
+def lora_muon_multi_step(table, lr=1e-3, momentum=0.95, nesterov=True, weight_decay=0.1, eps=1e-7,
+                         adjust="original", ns_coefficients=(3.4445, -4.775, 2.0315), ns_steps=5,
+                         ws=None, stream=None):
+    """One in-place Muon step on every matrix of a table.  adjust: "original"
+    multiplies the orthogonal update by sqrt(max(1, rows / cols)),
+    "match_rms_adamw" by 0.2 sqrt(max(rows, cols))."""
+    torch = _torch()
+    dev = table.device
+    kinds = {"original": QN_MUON_ORIGINAL, "match_rms_adamw": QN_MUON_MATCH_RMS}
+    if adjust not in kinds:
+        raise ValueError(f"adjust: one of {sorted(kinds)}")
+    step = qn_muon_step(lr, momentum, weight_decay, eps,
+                        (ctypes.c_double * 3)(*ns_coefficients), ns_steps, int(bool(nesterov)),
+                        kinds[adjust])
+    if ws is None:
+        ws = _new(stream, torch.uint8, dev, lora_muon_workspace_bytes(table))
+    else:
+        _fit(ws, torch.uint8, ws.numel(), dev, "ws")
+    _call("lora_muon_multi_step", dev, stream, table.plan, table.table.data_ptr(), step,
+          ws.data_ptr(), ws.numel())

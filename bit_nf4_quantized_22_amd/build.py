@@ -22,7 +22,7 @@ LIB = os.path.join(LIBDIR, "libqlora_nf4.so")
 SOURCES = ["qn_tables.cpp", "qn_api.cpp", "qn_quant.hip", "qn_gemv.hip", "qn_gemm.hip",
            "qn_grads.hip", "qn_merge.hip", "qn_fp8_quant.hip", "qn_fp8_gemm.hip", "qn_fp8_gemv.hip",
            "qn_mx_quant.hip", "qn_mx_gemm.hip", "qn_mx_gemv.hip",
-           "qn_optim.hip", "qn_optim_multi.hip", "qn_dropout.hip",
+           "qn_optim.hip", "qn_optim_multi.hip", "qn_muon.hip", "qn_dropout.hip",
            "qn_scratch.hip", "qn_probe.hip"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")

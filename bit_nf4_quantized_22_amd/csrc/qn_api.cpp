@@ -7,6 +7,7 @@
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
+#include <cmath>
 #include <cstdint>
 #include <cstring>
 #include <vector>
@@ -503,12 +504,26 @@ size_t adamw_table_size(int64_t chunks) {
   return static_cast<size_t>(chunks) * sizeof(qn::AdamChunk);
 }
 
+// Memory that a step reads or writes.
+struct Range {
+  uintptr_t lo, hi;
+  bool written;
+};
+
+// Whether one that is written overlaps any other.
+bool ranges_overlap(std::vector<Range>& all) {
+  std::sort(all.begin(), all.end(), [](const Range& a, const Range& b) { return a.lo < b.lo; });
+  uintptr_t any = 0, written = 0;  // furthest end so far, of all and of the written
+  for (const Range& r : all) {
+    if (r.lo < (r.written ? any : written)) return true;
+    any = std::max(any, r.hi);
+    if (r.written) written = std::max(written, r.hi);
+  }
+  return false;
+}
+
 // Whether memory that a step writes overlaps anything else of the table.
 bool adamw_overlaps(const qn_adamw_tensor* t, int32_t count, size_t grad_size, bool state8) {
-  struct Range {
-    uintptr_t lo, hi;
-    bool written;
-  };
   std::vector<Range> all;
   all.reserve(static_cast<size_t>(count) * 7);
   for (int32_t i = 0; i < count; ++i) {
@@ -530,14 +545,7 @@ bool adamw_overlaps(const qn_adamw_tensor* t, int32_t count, size_t grad_size, b
       add(t[i].v_scale, blocks * 4, true);
     }
   }
-  std::sort(all.begin(), all.end(), [](const Range& a, const Range& b) { return a.lo < b.lo; });
-  uintptr_t any = 0, written = 0;  // furthest end so far, of all and of the written
-  for (const Range& r : all) {
-    if (r.lo < (r.written ? any : written)) return true;
-    any = std::max(any, r.hi);
-    if (r.written) written = std::max(written, r.hi);
-  }
-  return false;
+  return ranges_overlap(all);
 }
 
 int check_adamw_plan(const qn_adamw_plan* plan, const void* table) {
@@ -555,6 +563,91 @@ int check_adamw_plan(const qn_adamw_plan* plan, const void* table) {
 
 const qn::AdamChunk* adamw_table(const void* table) {
   return static_cast<const qn::AdamChunk*>(table);
+}
+
+// --- Muon over many matrices ----------------------------------------------
+
+constexpr int64_t kMuonMaxChunks = int64_t{1} << 23;  // 256 threads each, under 2^31
+constexpr int64_t kMuonMaxLong = (int64_t{1} << 31) - 1;
+
+// How a matrix is split; -1 for one that is not offered.
+struct MuonShape {
+  int64_t r, len;
+  int cls, tiles;     // class, tiles of 16 of the short side
+  int64_t run, runs;  // elements of the long side in a run, runs
+};
+
+int muon_shape(const qn_muon_tensor& t, MuonShape& s) {
+  if (t.rows < 0 || t.cols < 0) return QN_ERR_SHAPE;
+  s.r = std::min(t.rows, t.cols);
+  s.len = std::max(t.rows, t.cols);
+  if (s.r == 0) {
+    s.len = 0;
+    return QN_OK;
+  }
+  if (s.r > kMaxRank) return QN_ERR_UNSUPPORTED;
+  if (s.len > kMuonMaxLong) return QN_ERR_SHAPE;
+  s.cls = 0;
+  while (16 * qn::kMuonTiles[s.cls] < s.r) ++s.cls;
+  s.tiles = qn::kMuonTiles[s.cls];
+  s.run = 256 / s.tiles;
+  s.runs = (s.len + s.run - 1) / s.run;
+  return QN_OK;
+}
+
+// Runs of each chunk: one workgroup's, of about 1536 in all where there are
+// that many runs (six a CU; a chunk's sums are as much as half a run), and at
+// most 256 chunks of a matrix, whose sums one workgroup adds.
+int64_t muon_runs_of_chunk(const MuonShape& s, int64_t total_runs) {
+  return std::max({int64_t{1}, (total_runs + 1535) / 1536, (s.runs + 255) / 256});
+}
+
+int64_t muon_sums(const MuonShape& s) { return s.tiles * (s.tiles + 1) / 2 * 256; }  // doubles
+
+// Matrices and chunks by class, table and workspace of `count` matrices.
+int muon_sizes(const qn_muon_tensor* t, int32_t count, qn_muon_plan& plan, int64_t& total_runs) {
+  plan = qn_muon_plan{};
+  total_runs = 0;
+  MuonShape s;
+  for (int32_t i = 0; i < count; ++i) {
+    if (int st = muon_shape(t[i], s); st != QN_OK) return st;
+    if (s.len > 0) total_runs += s.runs;
+  }
+  int64_t matrices = 0, chunks = 0, doubles = 0;
+  for (int32_t i = 0; i < count; ++i) {
+    muon_shape(t[i], s);
+    if (s.len == 0) continue;
+    const int64_t per = muon_runs_of_chunk(s, total_runs), n = (s.runs + per - 1) / per;
+    ++plan.matrices[s.cls];
+    plan.chunks[s.cls] += n;
+    ++matrices;
+    chunks += n;
+    doubles += n * muon_sums(s) + 256 * s.tiles * s.tiles;
+    if (chunks >= kMuonMaxChunks) return QN_ERR_SHAPE;
+  }
+  plan.bytes = matrices * static_cast<int64_t>(sizeof(qn::MuonMatrix)) +
+               chunks * static_cast<int64_t>(sizeof(qn::MuonChunk));
+  plan.ws_bytes = doubles * 8;
+  return QN_OK;
+}
+
+int check_muon_plan(const qn_muon_plan* plan, const void* table) {
+  if (!plan) return QN_ERR_NULL;
+  if (plan->grad_dtype != QN_F32 && plan->grad_dtype != QN_BF16) return QN_ERR_UNSUPPORTED;
+  int64_t matrices = 0, chunks = 0;
+  for (int k = 0; k < qn::kMuonClasses; ++k) {
+    const int64_t m = plan->matrices[k], c = plan->chunks[k];
+    if (m < 0 || c < m || c >= kMuonMaxChunks || (m == 0 && c > 0)) return QN_ERR_SHAPE;
+    matrices += m;
+    chunks += c;
+  }
+  if (plan->ws_bytes < 0 ||
+      plan->bytes != matrices * static_cast<int64_t>(sizeof(qn::MuonMatrix)) +
+                         chunks * static_cast<int64_t>(sizeof(qn::MuonChunk)))
+    return QN_ERR_SHAPE;
+  if (chunks > 0 && !table) return QN_ERR_NULL;
+  if (!aligned(table, 16)) return QN_ERR_ALIGN;
+  return QN_OK;
 }
 
 }  // namespace
@@ -1021,6 +1114,105 @@ int lora_adamw_multi_step(const qn_adamw_plan* plan, const void* table, const fl
       adamw_table(table), plan->chunks, plan->state == QN_STATE_8BIT,
       plan->grad_dtype == QN_BF16, grad_scale, lr, beta1, beta2, eps, weight_decay, step,
       as_stream(stream)));
+}
+
+size_t lora_muon_table_bytes(const qn_muon_tensor* t, int32_t count) {
+  qn_muon_plan plan;
+  int64_t runs;
+  if (!t || count < 0 || muon_sizes(t, count, plan, runs) != QN_OK) return 0;
+  return static_cast<size_t>(plan.bytes);
+}
+
+int lora_muon_table(const qn_muon_tensor* t, int32_t count, int32_t grad_dtype, void* table,
+                    size_t bytes, qn_muon_plan* plan) {
+  if (!plan || (count > 0 && !t)) return QN_ERR_NULL;
+  if (grad_dtype != QN_F32 && grad_dtype != QN_BF16) return QN_ERR_UNSUPPORTED;
+  if (count < 0) return QN_ERR_SHAPE;
+  qn_muon_plan made;
+  int64_t total_runs;
+  if (int st = muon_sizes(t, count, made, total_runs); st != QN_OK) return st;
+  made.grad_dtype = grad_dtype;
+  const int64_t grad_size = grad_dtype == QN_BF16 ? 2 : 4;
+  for (int32_t i = 0; i < count; ++i) {
+    const qn_muon_tensor& a = t[i];
+    if (a.rows == 0 || a.cols == 0) continue;
+    if (!a.p || !a.g || !a.m) return QN_ERR_NULL;
+    if (!aligned(a.p, 16) || !aligned(a.g, 16) || !aligned(a.m, 16) || !aligned(a.p_bf16, 16))
+      return QN_ERR_ALIGN;
+  }
+  if (made.bytes > 0 && (!table || bytes < static_cast<size_t>(made.bytes)))
+    return QN_ERR_WORKSPACE;
+  if (!aligned(table, 8)) return QN_ERR_ALIGN;
+  try {
+    std::vector<Range> all;
+    all.reserve(static_cast<size_t>(count) * 4);
+    for (int32_t i = 0; i < count; ++i) {
+      const int64_t n = t[i].rows * t[i].cols;
+      auto add = [&](const void* p, int64_t size, bool written) {
+        const uintptr_t lo = reinterpret_cast<uintptr_t>(p);
+        if (p && n > 0) all.push_back({lo, lo + static_cast<uintptr_t>(size), written});
+      };
+      add(t[i].p, n * 4, true);
+      add(t[i].g, n * grad_size, false);
+      add(t[i].m, n * 4, true);
+      add(t[i].p_bf16, n * 2, true);
+    }
+    if (ranges_overlap(all)) return QN_ERR_SHAPE;
+  } catch (...) {  // no host memory for the ranges
+    return QN_ERR_WORKSPACE;
+  }
+  *plan = made;
+  int64_t matrices = 0;
+  for (int64_t m : made.matrices) matrices += m;
+  qn::MuonMatrix* mats = static_cast<qn::MuonMatrix*>(table);
+  qn::MuonChunk* chunk = reinterpret_cast<qn::MuonChunk*>(mats + matrices);
+  int64_t at = 0;  // in the workspace
+  int32_t index = 0;
+  MuonShape s;
+  for (int cls = 0; cls < qn::kMuonClasses; ++cls)
+    for (int32_t i = 0; i < count; ++i) {
+      muon_shape(t[i], s);
+      if (s.len == 0 || s.cls != cls) continue;
+      const int64_t per = muon_runs_of_chunk(s, total_runs);
+      const int32_t n = static_cast<int32_t>((s.runs + per - 1) / per);
+      const int64_t factor = at + n * muon_sums(s);
+      *mats++ = qn::MuonMatrix{t[i].p, t[i].g, t[i].m, t[i].p_bf16, s.len, per * s.run, at, factor,
+                               static_cast<int32_t>(s.r), t[i].rows > t[i].cols ? 1 : 0, n, 0};
+      for (int32_t c = 0; c < n; ++c) *chunk++ = qn::MuonChunk{index, c};
+      at = factor + 256 * s.tiles * s.tiles;
+      ++index;
+    }
+  return QN_OK;
+}
+
+size_t lora_muon_workspace_bytes(const qn_muon_plan* plan) {
+  return plan && plan->ws_bytes > 0 ? static_cast<size_t>(plan->ws_bytes) : 0;
+}
+
+int lora_muon_multi_step(const qn_muon_plan* plan, const void* table, const qn_muon_step* step,
+                         void* ws, size_t ws_bytes, void* stream) {
+  if (int st = check_muon_plan(plan, table); st != QN_OK) return st;
+  if (!step) return QN_ERR_NULL;
+  if (step->adjust != QN_MUON_ORIGINAL && step->adjust != QN_MUON_MATCH_RMS)
+    return QN_ERR_UNSUPPORTED;
+  if (!(step->lr >= 0.0f) || !(step->momentum >= 0.0f && step->momentum < 1.0f) ||
+      !(step->weight_decay >= 0.0f) || !(step->eps > 0.0f) || step->ns_steps < 1 ||
+      step->ns_steps > 32 || !std::isfinite(step->ns[0]) || !std::isfinite(step->ns[1]) ||
+      !std::isfinite(step->ns[2]) || (step->nesterov != 0 && step->nesterov != 1))
+    return QN_ERR_SHAPE;
+  if (plan->ws_bytes > 0 && (!ws || ws_bytes < static_cast<size_t>(plan->ws_bytes)))
+    return QN_ERR_WORKSPACE;
+  if (!aligned(ws, 16)) return QN_ERR_ALIGN;
+  (void)hipGetLastError();
+  int64_t matrices = 0;
+  for (int64_t m : plan->matrices) matrices += m;
+  const qn::MuonMatrix* mats = static_cast<const qn::MuonMatrix*>(table);
+  const qn::MuonStep h{step->lr,     step->momentum, step->weight_decay, step->eps,
+                       step->ns[0],  step->ns[1],    step->ns[2],        step->ns_steps,
+                       step->nesterov == 1, step->adjust == QN_MUON_MATCH_RMS};
+  return hip_status(qn::launch_muon(mats, reinterpret_cast<const qn::MuonChunk*>(mats + matrices),
+                                    plan->matrices, plan->chunks, plan->grad_dtype == QN_BF16, h,
+                                    ws, as_stream(stream)));
 }
 
 int lora_grads(const qn_bf16* x, const qn_bf16* dy, const qn_bf16* u, const qn_bf16* t,

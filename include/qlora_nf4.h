@@ -778,6 +778,84 @@ QN_API int lora_adamw_multi_step(const qn_adamw_plan* plan, const void* table,
                                  const float* grad_scale, float lr, float beta1, float beta2,
                                  float eps, float weight_decay, int32_t step, void* stream);
 
+/*
+ * One LoRA matrix of lora_muon_multi_step (device pointers, 16-byte aligned):
+ *   p        fp32[rows, cols], updated in place.
+ *   g        the gradient, fp32 or bf16 (one type for all matrices).
+ *   m        fp32[rows, cols], the momentum, updated in place (starts as zeros).
+ *   p_bf16   bf16[rows, cols] out (the new p rounded to bf16), or NULL.
+ *   rows, cols  the smaller of the two at most 128 (QN_ERR_UNSUPPORTED), the
+ *            larger below 2^31; a matrix without elements is skipped, its
+ *            pointers not read.
+ */
+typedef struct qn_muon_tensor {
+  float* p;
+  const void* g;
+  float* m;
+  qn_bf16* p_bf16;
+  int64_t rows;
+  int64_t cols;
+} qn_muon_tensor;
+
+/* What lora_muon_table built; the calls that take a table take its plan. */
+typedef struct qn_muon_plan {
+  int64_t matrices[4];  /* by smaller side: up to 16, 32, 64, 128 */
+  int64_t chunks[4];    /* workgroups of a pass over them */
+  int64_t bytes;        /* bytes of the table */
+  int64_t ws_bytes;     /* and of the workspace */
+  int32_t grad_dtype;   /* QN_F32 or QN_BF16 */
+} qn_muon_plan;
+
+/* factor f of the orthogonal update: sqrt(max(1, rows / cols)), or 0.2
+ * sqrt(max(rows, cols)), which gives it the size of an AdamW update */
+#define QN_MUON_ORIGINAL   0
+#define QN_MUON_MATCH_RMS  1
+
+/* Hyperparameters of a step: lr, weight_decay >= 0, 0 <= momentum < 1, eps >
+ * 0, ns_steps 1 to 32, ns finite, nesterov 0 or 1, else QN_ERR_SHAPE; another
+ * adjust QN_ERR_UNSUPPORTED. */
+typedef struct qn_muon_step {
+  float lr;
+  float momentum;
+  float weight_decay;
+  float eps;
+  double ns[3];
+  int32_t ns_steps;
+  int32_t nesterov;
+  int32_t adjust;
+} qn_muon_step;
+
+/*
+ * lora_muon_table_bytes, lora_muon_table -- HOST functions, as
+ * lora_adamw_table_bytes and lora_adamw_table: check the matrices and write the
+ * table to host memory (8-byte aligned), which the caller copies to the device
+ * (16-byte aligned) once.  Memory that a step writes must not overlap any other
+ * operand of the table (QN_ERR_SHAPE); less than 2^23 chunks in all.
+ */
+QN_API size_t lora_muon_table_bytes(const qn_muon_tensor* t, int32_t count);
+QN_API int lora_muon_table(const qn_muon_tensor* t, int32_t count, int32_t grad_dtype, void* table,
+                           size_t bytes, qn_muon_plan* plan);
+
+/*
+ * lora_muon_multi_step -- one Muon step on every matrix of a table: momentum,
+ * an update made orthogonal by Newton-Schulz steps, decoupled weight decay:
+ *   m <- mu m + (1 - mu) g;   u = mu m + (1 - mu) g (nesterov), or m;
+ *   X = u / (|u| + eps), |u| the root of the sum of squares, transposed where
+ *   rows > cols;  ns_steps times, S = X X^T:  X <- ns[0] X + (ns[1] S + ns[2]
+ *   S^2) X;   p <- p (1 - lr wd) - lr f X.
+ * m and u are fp32, X's products 64-bit; X is rounded to fp32 once, before it
+ * moves p.  Sums are taken in a fixed order: results are bit-reproducible for a
+ * table.  u = 0 gives X = 0.  A NaN or infinite gradient makes its whole matrix
+ * NaN and touches no other.
+ *   ws  device workspace, 16-byte aligned, of at least
+ *       lora_muon_workspace_bytes(plan); not shared by calls that may run at
+ *       the same time.
+ * One launch per pass and class of smaller sides that occurs (three passes).
+ */
+QN_API size_t lora_muon_workspace_bytes(const qn_muon_plan* plan);
+QN_API int lora_muon_multi_step(const qn_muon_plan* plan, const void* table,
+                                const qn_muon_step* step, void* ws, size_t ws_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif
