@@ -88,7 +88,7 @@ class qn_muon_tensor(ctypes.Structure):
 
 class qn_muon_plan(ctypes.Structure):
     _fields_ = [("matrices", ctypes.c_int64 * 4), ("chunks", ctypes.c_int64 * 4),
-                ("bytes", ctypes.c_int64), ("ws_bytes", ctypes.c_int64),
+                ("spans", ctypes.c_int64 * 4), ("bytes", ctypes.c_int64), ("ws_bytes", ctypes.c_int64),
                 ("grad_dtype", ctypes.c_int32)]
 
 

@@ -568,13 +568,13 @@ const qn::AdamChunk* adamw_table(const void* table) {
 // --- Muon over many matrices ----------------------------------------------
 
 constexpr int64_t kMuonMaxChunks = int64_t{1} << 23;  // 256 threads each, under 2^31
-constexpr int64_t kMuonMaxLong = (int64_t{1} << 31) - 1;
+constexpr int64_t kMuonMaxLong = (int64_t{1} << 24) - 1;
 
 // How a matrix is split; -1 for one that is not offered.
 struct MuonShape {
   int64_t r, len;
-  int cls, tiles;     // class, tiles of 16 of the short side
-  int64_t run, runs;  // elements of the long side in a run, runs
+  int cls, tiles;  // class, tiles of 16 of the short side
+  int64_t runs;    // of kMuonRun elements of the long side
 };
 
 int muon_shape(const qn_muon_tensor& t, MuonShape& s) {
@@ -590,16 +590,33 @@ int muon_shape(const qn_muon_tensor& t, MuonShape& s) {
   s.cls = 0;
   while (16 * qn::kMuonTiles[s.cls] < s.r) ++s.cls;
   s.tiles = qn::kMuonTiles[s.cls];
-  s.run = 256 / s.tiles;
-  s.runs = (s.len + s.run - 1) / s.run;
+  s.runs = (s.len + qn::kMuonRun - 1) / qn::kMuonRun;
   return QN_OK;
 }
 
-// Runs of each chunk: one workgroup's, of about 1536 in all where there are
-// that many runs (six a CU; a chunk's sums are as much as half a run), and at
-// most 256 chunks of a matrix, whose sums one workgroup adds.
-int64_t muon_runs_of_chunk(const MuonShape& s, int64_t total_runs) {
-  return std::max({int64_t{1}, (total_runs + 1535) / 1536, (s.runs + 255) / 256});
+// Runs of each chunk or span of a matrix, for about `target` workgroups of a pass
+// in all, at most 256 chunks of a matrix, whose sums one workgroup adds; nearly
+// equal ones.
+int64_t muon_runs_of(const MuonShape& s, int64_t total_runs, int64_t target, bool capped) {
+  const int64_t per = std::max({int64_t{1}, (total_runs + target - 1) / target,
+                                capped ? (s.runs + 255) / 256 : int64_t{1}});
+  const int64_t n = (s.runs + per - 1) / per;
+  return (s.runs + n - 1) / n;
+}
+
+// The first pass leaves tiles (tiles + 1) KB of sums per chunk, which are few
+// for up to 32 rows and short chunks fill the chip more evenly (448 matrices of
+// 16 x 4096: 4096 workgroups 54-59 us, 1536 65; of 64 x 4096: 2048 269-288 and
+// steps of 80, 8192 297 and 100).
+int64_t muon_chunk_runs(const MuonShape& s, int64_t total_runs) {
+  return muon_runs_of(s, total_runs, s.tiles <= 2 ? 4096 : 2048, true);
+}
+
+// The last pass takes the steps' result once per workgroup, which for up to 16
+// rows means to compute it (448 matrices of 16 x 4096: 3072 workgroups 113-125 us,
+// 8192 145; of 64 x 4096: 8192 543-632, 2048 685).
+int64_t muon_span_runs(const MuonShape& s, int64_t total_runs) {
+  return muon_runs_of(s, total_runs, s.tiles == 1 ? 3072 : 8192, false);
 }
 
 int64_t muon_sums(const MuonShape& s) { return s.tiles * (s.tiles + 1) / 2 * 256; }  // doubles
@@ -617,11 +634,13 @@ int muon_sizes(const qn_muon_tensor* t, int32_t count, qn_muon_plan& plan, int64
   for (int32_t i = 0; i < count; ++i) {
     muon_shape(t[i], s);
     if (s.len == 0) continue;
-    const int64_t per = muon_runs_of_chunk(s, total_runs), n = (s.runs + per - 1) / per;
+    const int64_t n = qn::mx_tiles(s.runs, muon_chunk_runs(s, total_runs));
+    const int64_t spans = qn::mx_tiles(s.runs, muon_span_runs(s, total_runs));
     ++plan.matrices[s.cls];
     plan.chunks[s.cls] += n;
+    plan.spans[s.cls] += spans;
     ++matrices;
-    chunks += n;
+    chunks += n + spans;
     doubles += n * muon_sums(s) + 256 * s.tiles * s.tiles;
     if (chunks >= kMuonMaxChunks) return QN_ERR_SHAPE;
   }
@@ -636,10 +655,12 @@ int check_muon_plan(const qn_muon_plan* plan, const void* table) {
   if (plan->grad_dtype != QN_F32 && plan->grad_dtype != QN_BF16) return QN_ERR_UNSUPPORTED;
   int64_t matrices = 0, chunks = 0;
   for (int k = 0; k < qn::kMuonClasses; ++k) {
-    const int64_t m = plan->matrices[k], c = plan->chunks[k];
-    if (m < 0 || c < m || c >= kMuonMaxChunks || (m == 0 && c > 0)) return QN_ERR_SHAPE;
+    const int64_t m = plan->matrices[k], c = plan->chunks[k], s = plan->spans[k];
+    if (m < 0 || c < m || c >= kMuonMaxChunks || s < m || s >= kMuonMaxChunks ||
+        (m == 0 && (c > 0 || s > 0)))
+      return QN_ERR_SHAPE;
     matrices += m;
-    chunks += c;
+    chunks += c + s;
   }
   if (plan->ws_bytes < 0 ||
       plan->bytes != matrices * static_cast<int64_t>(sizeof(qn::MuonMatrix)) +
@@ -1169,19 +1190,25 @@ int lora_muon_table(const qn_muon_tensor* t, int32_t count, int32_t grad_dtype, 
   int64_t at = 0;  // in the workspace
   int32_t index = 0;
   MuonShape s;
-  for (int cls = 0; cls < qn::kMuonClasses; ++cls)
+  for (int cls = 0; cls < qn::kMuonClasses; ++cls) {
+    qn::MuonChunk* span = chunk + made.chunks[cls];
     for (int32_t i = 0; i < count; ++i) {
       muon_shape(t[i], s);
       if (s.len == 0 || s.cls != cls) continue;
-      const int64_t per = muon_runs_of_chunk(s, total_runs);
-      const int32_t n = static_cast<int32_t>((s.runs + per - 1) / per);
+      const int64_t per = muon_chunk_runs(s, total_runs), per2 = muon_span_runs(s, total_runs);
+      const int32_t n = static_cast<int32_t>(qn::mx_tiles(s.runs, per));
+      const int32_t n2 = static_cast<int32_t>(qn::mx_tiles(s.runs, per2));
       const int64_t factor = at + n * muon_sums(s);
-      *mats++ = qn::MuonMatrix{t[i].p, t[i].g, t[i].m, t[i].p_bf16, s.len, per * s.run, at, factor,
-                               static_cast<int32_t>(s.r), t[i].rows > t[i].cols ? 1 : 0, n, 0};
+      *mats++ = qn::MuonMatrix{t[i].p, t[i].g, t[i].m, t[i].p_bf16, s.len, per * qn::kMuonRun,
+                               per2 * qn::kMuonRun, at, factor, static_cast<int32_t>(s.r),
+                               t[i].rows > t[i].cols ? 1 : 0, n, n2};
       for (int32_t c = 0; c < n; ++c) *chunk++ = qn::MuonChunk{index, c};
+      for (int32_t c = 0; c < n2; ++c) *span++ = qn::MuonChunk{index, c};
       at = factor + 256 * s.tiles * s.tiles;
       ++index;
     }
+    chunk = span;
+  }
   return QN_OK;
 }
 
@@ -1204,15 +1231,18 @@ int lora_muon_multi_step(const qn_muon_plan* plan, const void* table, const qn_m
     return QN_ERR_WORKSPACE;
   if (!aligned(ws, 16)) return QN_ERR_ALIGN;
   (void)hipGetLastError();
+  qn::MuonCounts n;
   int64_t matrices = 0;
-  for (int64_t m : plan->matrices) matrices += m;
+  for (int k = 0; k < qn::kMuonClasses; ++k) {
+    n.matrices[k] = plan->matrices[k], n.chunks[k] = plan->chunks[k], n.spans[k] = plan->spans[k];
+    matrices += plan->matrices[k];
+  }
   const qn::MuonMatrix* mats = static_cast<const qn::MuonMatrix*>(table);
   const qn::MuonStep h{step->lr,     step->momentum, step->weight_decay, step->eps,
                        step->ns[0],  step->ns[1],    step->ns[2],        step->ns_steps,
                        step->nesterov == 1, step->adjust == QN_MUON_MATCH_RMS};
   return hip_status(qn::launch_muon(mats, reinterpret_cast<const qn::MuonChunk*>(mats + matrices),
-                                    plan->matrices, plan->chunks, plan->grad_dtype == QN_BF16, h,
-                                    ws, as_stream(stream)));
+                                    n, plan->grad_dtype == QN_BF16, h, ws, as_stream(stream)));
 }
 
 int lora_grads(const qn_bf16* x, const qn_bf16* dy, const qn_bf16* u, const qn_bf16* t,

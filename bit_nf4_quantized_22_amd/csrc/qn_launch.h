@@ -284,8 +284,8 @@ hipError_t launch_grad_norm(const AdamChunk* tab, int64_t chunks, bool bf16_grad
 
 // Muon over many matrices (see lora_muon_multi_step in the C ABI).  The device
 // table holds the matrices, in the order of their classes (short sides up to 16,
-// 32, 64 and 128), then one entry per workgroup of the two passes, in the same
-// order: a chunk of a matrix's long side.
+// 32, 64 and 128), then for each class one entry per workgroup of the first pass,
+// a chunk of a matrix's long side, and one per workgroup of the last, a span.
 struct MuonMatrix {
   float* p;
   const void* g;  // fp32 or bf16
@@ -293,26 +293,29 @@ struct MuonMatrix {
   uint16_t* p_bf16;
   int64_t len;      // the long side; row-major [r, len], or with tall [len, r]
   int64_t chunk;    // elements of the long side in a chunk
+  int64_t span;     // and in a span
   int64_t part;     // in the workspace, in doubles: the chunks' sums
   int64_t factor;   // and the product's left factor
-  int32_t r, tall, chunks, pad;
+  int32_t r, tall, chunks, spans;
 };
 struct MuonChunk {
   int32_t matrix;  // in the table
-  int32_t index;   // among the matrix's chunks
+  int32_t index;   // among the matrix's chunks or spans
 };
 constexpr int kMuonClasses = 4;
 constexpr int kMuonTiles[kMuonClasses] = {1, 2, 4, 8};  // of 16 rows
+constexpr int kMuonRun = 256;  // of the long side, a block of 64 for each wave
 struct MuonStep {
   float lr, momentum, weight_decay, eps;
   double a, b, c;
   int steps;
   bool nesterov, rms;
 };
-hipError_t launch_muon(const MuonMatrix* mats, const MuonChunk* chunks,
-                       const int64_t (&matrices)[kMuonClasses],
-                       const int64_t (&nchunks)[kMuonClasses], bool bf16_grad, const MuonStep& h,
-                       void* ws, hipStream_t st);
+struct MuonCounts {
+  int64_t matrices[kMuonClasses], chunks[kMuonClasses], spans[kMuonClasses];
+};
+hipError_t launch_muon(const MuonMatrix* mats, const MuonChunk* chunks, const MuonCounts& n,
+                       bool bf16_grad, const MuonStep& h, void* ws, hipStream_t st);
 
 // LoRA dropout on the adapter branch (see lora_dropout in the C ABI):
 // threshold = floor(p 2^32) on the 32-bit Philox halves, inv_keep =

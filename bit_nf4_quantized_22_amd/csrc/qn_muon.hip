@@ -18,6 +18,14 @@
 // lane / 16 (register v) of column lane % 16, and an operand's lane element lane
 // % 16 of step lane / 16, so that a tile's registers are what it needs as either
 // operand of its transpose.
+//
+// Bound by HBM: 8 bytes an element in the first pass, 22 in the last.  448
+// matrices of 16 x 4096 (29 M elements): 59 us (4.0 TB/s) and 115 us (5.6 TB/s,
+// part of it from the last-level cache), the steps among them; of 64 x 4096 (117
+// M): 288 us (3.3 TB/s), the steps 80 us, 545-630 us (4.1-4.7 TB/s).  All adapters
+// of a 7B model, r = 64: 1.31 ms, 0.95 at a large copy's rate.  Up to r = 64 the
+// matrix instructions would take a third of these times; at r = 128 (52 M) they
+// are half of them: 250, 230 and 420 us.
 
 #include <cmath>
 
@@ -47,182 +55,178 @@ __device__ __forceinline__ void upper_tile(int q, int& a, int& b) {
 }
 
 struct MuonArgs {
-  float mu, one_minus_mu, decay, lr;
+  float mu, one_minus_mu, decay, lr, eps;
   bool nesterov, rms;
+  double ca, cb, cc;  // of a step
+  int steps;
 };
 
-// 4 consecutive elements in memory, of which n (at most 4) exist.
+// The table's pointers as what they are: from a pointer that it finds in memory
+// the compiler would make flat accesses, which count as LDS accesses too.
 template <typename T>
-__device__ __forceinline__ void load4(const T* p, int64_t n, bool vec, float (&v)[4]) {
-  if (vec && n >= 4) {
-    if constexpr (sizeof(T) == 4) {
-      const float4 w = *reinterpret_cast<const float4*>(p);
-      v[0] = w.x, v[1] = w.y, v[2] = w.z, v[3] = w.w;
-    } else {
-      const uint2 w = *reinterpret_cast<const uint2*>(p);
-      v[0] = bf16_lo(w.x), v[1] = bf16_hi(w.x), v[2] = bf16_lo(w.y), v[3] = bf16_hi(w.y);
-    }
-    return;
-  }
+using Global = __attribute__((address_space(1))) T*;
+
+template <typename T>
+__device__ __forceinline__ Global<T> global(T* p) {
+  return (Global<T>)p;
+}
+
+// Element `lane` behind a wave's address: a scalar and 32 bits, which takes one
+// register for all vectors of a lane (byte offsets below 2^32).
+template <typename T>
+__device__ __forceinline__ Global<T> lane_ptr(Global<T> p, uint32_t lane) {
+  return (Global<T>)((Global<const char>)p + lane * static_cast<uint32_t>(sizeof(T)));
+}
+
+__device__ __forceinline__ float element(float x) { return x; }
+__device__ __forceinline__ float element(uint16_t x) { return bf16_to_f32(x); }
+
+// kN consecutive elements in memory, of which n exist; with kVec all or none of
+// them do, and they are read and written as one vector.
+template <bool kVec, int kN, typename T>
+__device__ __forceinline__ void load_some(Global<const T> p, int n, float (&v)[kN]) {
+  if constexpr (kVec && kN > 1) {
+    typedef T vec_t __attribute__((ext_vector_type(kN)));
+    vec_t w = vec_t(0);
+    if (n > 0) w = *(Global<const vec_t>)p;
 #pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    v[e] = 0.0f;
-    if (e < n) {
-      if constexpr (sizeof(T) == 4)
-        v[e] = p[e];
-      else
-        v[e] = bf16_to_f32(p[e]);
-    }
+    for (int e = 0; e < kN; ++e) v[e] = element(w[e]);
+  } else {
+#pragma unroll
+    for (int e = 0; e < kN; ++e) v[e] = e < n ? element(p[e]) : 0.0f;
   }
 }
 
-template <typename T>
-__device__ __forceinline__ void store4(T* p, int64_t n, bool vec, const float (&v)[4]) {
-  if (vec && n >= 4) {
-    if constexpr (sizeof(T) == 4)
-      *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
-    else
-      *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
-    return;
-  }
+template <bool kVec, int kN>
+__device__ __forceinline__ void store_some(Global<float> p, int n, const float (&v)[kN]) {
+  if constexpr (kVec) {
+    typedef float vec_t __attribute__((ext_vector_type(kN)));
+    vec_t w;
 #pragma unroll
-  for (int e = 0; e < 4; ++e)
-    if (e < n) {
-      if constexpr (sizeof(T) == 4)
-        p[e] = v[e];
-      else
-        p[e] = static_cast<uint16_t>(pack_bf16x2(v[e], 0.0f) & 0xFFFF);
-    }
+    for (int e = 0; e < kN; ++e) w[e] = v[e];
+    if (n > 0) *(Global<vec_t>)p = w;
+  } else {
+#pragma unroll
+    for (int e = 0; e < kN; ++e)
+      if (e < n) p[e] = v[e];
+  }
 }
 
-// How a workgroup's threads take a run of kLen elements of the long side, 4096
-// in all: group j of a thread is 4 elements that lie together in memory, along
-// the long side of a wide matrix and the short one of a tall one.
-template <int kT, int kPitch>
-struct Runs {
-  static constexpr int kLen = 256 / kT, kGroups = 4;
-  static_assert(kT * 16 * kLen == kThreads * kGroups * 4, "16 elements a thread");
-  int64_t first[kGroups];   // the group's first element, of the run at 0
-  int64_t behind[kGroups];  // elements of the run before it in its direction
-  int place[kGroups][4];    // [short][long] in LDS, -1: no element of the matrix
-  int64_t stride;           // of one element of the long side
-  bool vec;                 // all groups can be read as vectors
-
-  __device__ __forceinline__ explicit Runs(const MuonMatrix& mat) {
-    const bool tall = mat.tall != 0;
-    const int r = mat.r;
-    vec = tall || (mat.len & 3) == 0;
-    stride = tall ? r : 1;
+template <bool kVec, int kN>
+__device__ __forceinline__ void store_some(Global<uint16_t> p, int n, const float (&v)[kN]) {
+  typedef uint32_t vec_t __attribute__((ext_vector_type(kN / 2)));
+  vec_t w;
 #pragma unroll
-    for (int j = 0; j < kGroups; ++j) {
-      const int q = j * kThreads + static_cast<int>(threadIdx.x);
-      int i, k;
-      if (tall) {
-        k = q * 4 / r;
-        i = q * 4 - k * r;
-        first[j] = q * 4;
-        behind[j] = q * 4;
-      } else {
-        i = q / (kLen / 4);
-        k = q % (kLen / 4) * 4;
-        first[j] = i * mat.len + k;
-        behind[j] = k;
-      }
-      if (k >= kLen || i >= r) behind[j] = int64_t{1} << 60;
+  for (int e = 0; e < kN / 2; ++e) w[e] = pack_bf16x2(v[2 * e], v[2 * e + 1]);
+  if constexpr (kVec) {
+    if (n > 0) *(Global<vec_t>)p = w;
+  } else {
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        place[j][e] = k < kLen && i < r ? i * kPitch + k : -1;
-        i += tall ? 1 : 0;
-        k += tall ? 0 : 1;
-        if (tall && i == r) i = 0, ++k;
-      }
-    }
+    for (int e = 0; e < kN; ++e)
+      if (e < n) p[e] = static_cast<uint16_t>(w[e / 2] >> (16 * (e & 1)));
   }
-  __device__ __forceinline__ int64_t at(int j, int64_t k0) const { return first[j] + k0 * stride; }
-  // How many elements from group j's first on lie before `end` of the long side
-  // (0 or less: none; more than 4 for whole groups).
-  __device__ __forceinline__ int64_t left(int j, int64_t k0, int64_t end) const {
-    return (end - k0) * stride - behind[j];
-  }
-};
+}
 
-// The momentum and the update of 4 elements.
-__device__ __forceinline__ void momentum4(const MuonArgs& a, const float (&g)[4], float (&m)[4],
-                                          float (&u)[4]) {
+// The momentum and the update of n elements.
+template <int n>
+__device__ __forceinline__ void momentum(const MuonArgs& a, const float (&g)[n], float (&m)[n],
+                                         float (&u)[n]) {
 #pragma unroll
-  for (int e = 0; e < 4; ++e) {
+  for (int e = 0; e < n; ++e) {
     const float gs = g[e] * a.one_minus_mu;
     m[e] = fmaf(m[e], a.mu, gs);
     u[e] = a.nesterov ? fmaf(m[e], a.mu, gs) : m[e];
   }
 }
 
-// u u^T of one chunk of the long side.  Runs of it are staged in LDS [short]
-// [long] as fp32, the next one on its way meanwhile; each wave multiplies a
-// quarter of a run into all tiles, and the waves' sums are added in order.
+// u u^T of a chunk of the long side, its batches dealt to the waves in turn (so
+// that they read the same lines at about the same time: 430 -> 300 us for 448
+// matrices of 64 x 4096).  The products' operands are loaded as they are needed,
+// without LDS, a batch ahead: lane (li, lg) holds row 16 t + li of the short side; a wide matrix gives
+// it 4 consecutive elements of the long side (4 steps, group lg's elements at
+// 4 lg: any order that both operands share will do), a tall one a single one.
+template <int kT, bool kTall, bool kVec, typename G>
+__device__ __forceinline__ void gram_blocks(const MuonMatrix& mat, const MuonArgs& a, int start,
+                                            int end, int wave, f64x4_t (&acc)[upper_tiles(kT)]) {
+  constexpr int kN = kTall ? 1 : kT == 8 ? 2 : 4;  // elements of a load
+  constexpr int kH = kT < 4 ? (kTall ? 16 : 4) / kT : kTall ? 2 : 1;  // loads of a row and batch
+  constexpr int kBatch = 4 * kN * kH;              // of the long side
+  const int lane = threadIdx.x & 63, li = lane & 15, lg = lane >> 4;
+  const int r = mat.r, len = static_cast<int>(mat.len);
+  const Global<const G> g = global(static_cast<const G*>(mat.g));
+  const Global<const float> m = global(static_cast<const float*>(mat.m));
+  const uint32_t place = kTall ? static_cast<uint32_t>(lg * r + li)
+                               : static_cast<uint32_t>(li) * static_cast<uint32_t>(len) + kN * lg;
+  float gv[2][kT][kH][kN], mv[2][kT][kH][kN];
+  auto load = [&](int n, int buf) {
+    const int k0 = start + (wave + n * kWaves) * kBatch;
+    // hidden from the compiler, which would keep and step a pointer for each load
+    int64_t block = kTall ? static_cast<int64_t>(k0) * r : k0;
+    asm volatile("" : "+s"(block));
+#pragma unroll
+    for (int h = 0; h < kH; ++h)
+#pragma unroll
+      for (int t = 0; t < kT; ++t) {
+        const int k = k0 + 4 * kN * h;
+        const int64_t at = block + (kTall ? 4 * kN * h * r + 16 * t
+                                          : static_cast<int64_t>(16 * t) * len + 4 * kN * h);
+        const int n_in = 16 * t + li < r ? end - k - kN * lg : 0;
+        load_some<kVec, kN, G>(lane_ptr(g + at, place), n_in, gv[buf][t][h]);
+        load_some<kVec, kN, float>(lane_ptr(m + at, place), n_in, mv[buf][t][h]);
+      }
+  };
+  auto multiply = [&](int buf) {
+#pragma unroll
+    for (int h = 0; h < kH; ++h) {
+      float u[kT][kN];
+#pragma unroll
+      for (int t = 0; t < kT; ++t) momentum(a, gv[buf][t][h], mv[buf][t][h], u[t]);
+#pragma unroll
+      for (int e = 0; e < kN; ++e) {
+        double f[kT];
+#pragma unroll
+        for (int t = 0; t < kT; ++t) f[t] = static_cast<double>(u[t][e]);
+        int q = 0;
+#pragma unroll
+        for (int x = 0; x < kT; ++x)
+#pragma unroll
+          for (int y = x; y < kT; ++y, ++q) acc[q] = mfma64(f[x], f[y], acc[q]);
+      }
+    }
+  };
+  const int all = (end - start + kBatch - 1) / kBatch;
+  const int batches = all > wave ? (all - wave + kWaves - 1) / kWaves : 0;
+  if (batches > 0) load(0, 0);
+  for (int n = 0; n < batches; n += 2) {
+    if (n + 1 < batches) load(n + 1, 1);
+    multiply(0);
+    if (n + 2 < batches) load(n + 2, 0);
+    if (n + 1 < batches) multiply(1);
+  }
+}
+
 template <int kT, typename G>
 __global__ __launch_bounds__(kThreads) void muon_gram_kernel(const MuonMatrix* __restrict__ mats,
                                                              const MuonChunk* __restrict__ chunks,
                                                              MuonArgs a, double* __restrict__ ws) {
-  constexpr int kLen = 256 / kT, kPitch = kLen + 4, kTiles = upper_tiles(kT);
-  typedef Runs<kT, kPitch> R;
-  constexpr int kFloats = kT * 16 * kPitch;
-  __shared__ __attribute__((aligned(16))) float s_u[2 * kFloats];
+  constexpr int kTiles = upper_tiles(kT);
+  __shared__ f64x4_t s_acc[kWaves * kWaves * 64];  // [tile of the round][wave][lane]
   const MuonChunk c = chunks[blockIdx.x];
   const MuonMatrix mat = mats[c.matrix];
-  const int t = threadIdx.x, lane = t & 63, li = lane & 15, lg = lane >> 4;
+  const int t = threadIdx.x, lane = t & 63;
   const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
-  const int64_t start = c.index * mat.chunk;
-  const int64_t end = start + mat.chunk < mat.len ? start + mat.chunk : mat.len;
-  const R runs(mat);
-  const G* g = static_cast<const G*>(mat.g);
-  for (int i = t; i < 2 * kFloats; i += kThreads) s_u[i] = 0.0f;
-  float gv[R::kGroups][4], mv[R::kGroups][4];
-  auto load = [&](int64_t k0) {
-#pragma unroll
-    for (int j = 0; j < R::kGroups; ++j) {
-      const int64_t at = runs.at(j, k0), left = runs.left(j, k0, end);
-      load4(g + at, left, runs.vec, gv[j]);
-      load4(mat.m + at, left, runs.vec, mv[j]);
-    }
-  };
+  const int start = static_cast<int>(c.index * mat.chunk);
+  const int end = static_cast<int>(start + mat.chunk < mat.len ? start + mat.chunk : mat.len);
   f64x4_t acc[kTiles];
 #pragma unroll
   for (int q = 0; q < kTiles; ++q) acc[q] = f64x4_t{0.0, 0.0, 0.0, 0.0};
-  load(start);
-  __syncthreads();
-  int buf = 0;
-  for (int64_t k0 = start; k0 < end; k0 += kLen, buf ^= 1) {
-    float* su = s_u + buf * kFloats;
-#pragma unroll
-    for (int j = 0; j < R::kGroups; ++j) {
-      float u[4];
-      momentum4(a, gv[j], mv[j], u);
-      const int64_t left = runs.left(j, k0, end);
-#pragma unroll
-      for (int e = 0; e < 4; ++e)  // past the chunk's end zeros, over what the buffer held
-        if (runs.place[j][e] >= 0) su[runs.place[j][e]] = e < left ? u[e] : 0.0f;
-    }
-    __syncthreads();
-    if (k0 + kLen < end) load(k0 + kLen);
-    constexpr int kSteps = kLen / 4 / kWaves;
-#pragma unroll 2
-    for (int s = 0; s < kSteps; ++s) {
-      double f[kT];
-#pragma unroll
-      for (int q = 0; q < kT; ++q)
-        f[q] = static_cast<double>(su[(16 * q + li) * kPitch + 4 * (wave * kSteps + s) + lg]);
-      int q = 0;
-#pragma unroll
-      for (int x = 0; x < kT; ++x)
-#pragma unroll
-        for (int y = x; y < kT; ++y, ++q) acc[q] = mfma64(f[x], f[y], acc[q]);
-    }
-  }
-  // 4 tiles at a time, one per wave
-  __syncthreads();
-  f64x4_t* s_acc = reinterpret_cast<f64x4_t*>(s_u);  // [tile][wave][lane]
-  static_assert(2 * kFloats * 4 >= kWaves * kWaves * 64 * 32, "the sums fit");
+  if (mat.tall)  // of single elements
+    gram_blocks<kT, true, false, G>(mat, a, start, end, wave, acc);
+  else if ((mat.len & 3) == 0)
+    gram_blocks<kT, false, true, G>(mat, a, start, end, wave, acc);
+  else
+    gram_blocks<kT, false, false, G>(mat, a, start, end, wave, acc);
+  // the waves' sums, 4 tiles at a time, one per wave
   f64x4_t* part = reinterpret_cast<f64x4_t*>(ws + mat.part + c.index * (kTiles * 256));
 #pragma unroll
   for (int q0 = 0; q0 < kTiles; q0 += kWaves) {
@@ -273,10 +277,22 @@ __device__ __forceinline__ f64x4_t tile_product(const double* x, const double* y
   return acc;
 }
 
+// Place of T's element (i, j) among the operands of the last pass: step (j / 16,
+// q) of row tile i / 16, 64 lanes each.  Lane (li, lg) multiplies its row with the
+// element of u that it holds there, 4 q + lg of a wide matrix or 4 lg + q of a
+// tall one, and a tall one's rows are turned likewise: result register v of lanes
+// lg is row 4 lg + v.
+template <int kT>
+__device__ __forceinline__ int factor_place(bool tall, int i, int j) {
+  const int a = i & 15, b = j & 15;
+  const int li = tall ? 4 * (a & 3) + (a >> 2) : a;
+  const int lg = tall ? b >> 2 : b & 3, q = tall ? b & 3 : b >> 2;
+  return (((i >> 4) * kT + (j >> 4)) * 4 + q) * 64 + lg * 16 + li;
+}
+
 template <int kT>
 __global__ __launch_bounds__(64 * Steps<kT>::kWavesOf) void muon_steps_kernel(
-    const MuonMatrix* __restrict__ mats, double ca, double cb, double cc, int steps, float eps,
-    double* __restrict__ ws) {
+    const MuonMatrix* __restrict__ mats, MuonArgs a, double* __restrict__ ws) {
   typedef Steps<kT> P;
   __shared__ __attribute__((aligned(16))) double s_x[P::kTiles * P::kTile];
   __shared__ __attribute__((aligned(16))) double s_y[P::kTiles * P::kTile];
@@ -311,7 +327,7 @@ __global__ __launch_bounds__(64 * Steps<kT>::kWavesOf) void muon_steps_kernel(
   double norm2 = 0.0;
 #pragma unroll 8
   for (int i = 0; i < 16 * kT; ++i) norm2 += s_diag[i];
-  const double inv = 1.0 / (sqrt(norm2) + static_cast<double>(eps));
+  const double inv = 1.0 / (sqrt(norm2) + static_cast<double>(a.eps));
 
   auto store = [&](double* to, const f64x4_t (&m)[P::kOwn]) {
 #pragma unroll
@@ -326,7 +342,7 @@ __global__ __launch_bounds__(64 * Steps<kT>::kWavesOf) void muon_steps_kernel(
   };
 #pragma unroll
   for (int d = 0; d < P::kOwn; ++d) s[d] *= inv * inv;
-  for (int n = 0; n < steps; ++n) {
+  for (int n = 0; n < a.steps; ++n) {
     // Q = a I + b S + c S^2
     store(s_x, s);
     __syncthreads();
@@ -335,14 +351,14 @@ __global__ __launch_bounds__(64 * Steps<kT>::kWavesOf) void muon_steps_kernel(
       const f64x4_t s2 = tile_product<kT>(s_x, s_x, ta[d], tb[d], li, lg);
 #pragma unroll
       for (int v = 0; v < 4; ++v)
-        q[d][v] = cc * s2[v] + cb * s[d][v] +
-                  (ta[d] == tb[d] && 4 * v + lg == li ? ca : 0.0);
+        q[d][v] = a.cc * s2[v] + a.cb * s[d][v] +
+                  (ta[d] == tb[d] && 4 * v + lg == li ? a.ca : 0.0);
     }
     store(s_y, q);
     __syncthreads();
     // T Q, and S Q Q unless this was the last step
     f64x4_t r[P::kOwn];
-    if (n + 1 < steps) product(r);
+    if (n + 1 < a.steps) product(r);
     if (n == 0) {
 #pragma unroll
       for (int d = 0; d < P::kOwn; ++d) x[d] = q[d];
@@ -352,7 +368,7 @@ __global__ __launch_bounds__(64 * Steps<kT>::kWavesOf) void muon_steps_kernel(
       __syncthreads();
       product(x);
     }
-    if (n + 1 < steps) {
+    if (n + 1 < a.steps) {
       __syncthreads();
       store(s_x, r);
       __syncthreads();
@@ -360,8 +376,7 @@ __global__ __launch_bounds__(64 * Steps<kT>::kWavesOf) void muon_steps_kernel(
       __syncthreads();
     }
   }
-  // T / (|u| + eps) in the order of the last pass's operands: [16 rows][4 columns]
-  // a lane each
+  // T / (|u| + eps) in the order of the last pass's operands
   double* out = ws + mat.factor;
 #pragma unroll
   for (int d = 0; d < P::kOwn; ++d)
@@ -369,113 +384,208 @@ __global__ __launch_bounds__(64 * Steps<kT>::kWavesOf) void muon_steps_kernel(
     for (int v = 0; v < 4; ++v) {
       const int i = 16 * ta[d] + 4 * v + lg, j = 16 * tb[d] + li;
       const double w = x[d][v] * inv;
-      out[((i >> 4) * (4 * kT) + (j >> 2)) * 64 + (j & 3) * 16 + (i & 15)] = w;
-      out[((j >> 4) * (4 * kT) + (i >> 2)) * 64 + (i & 3) * 16 + (j & 15)] = w;
+      out[factor_place<kT>(mat.tall, i, j)] = w;
+      out[factor_place<kT>(mat.tall, j, i)] = w;
     }
 }
 
-// The update of one chunk: u once more, times T, and into p.
+// The update of blocks of 16 kC of the long side, a wave each: u once more, times
+// T, and into p.  A lane holds 4 kC elements of 16 rows, of a wide matrix as 4
+// vectors along the long side (vector q: row 4 q + lg, columns kC li ..), of a tall
+// one as kC vectors along the short one (vector c: columns 4 lg .. + 3 of row 16 c
+// + li).  Step q and column tile c of the product take element c of vector q, or
+// element q of vector c; rows of T are put in the order in which the results then
+// lie in the same places, so that nothing moves between lanes.
+// (Loads of the next block, and of p before the products, cost the registers of a
+// resident wave: 100 -> 145 us for 448 matrices of 16 x 4096.)
+template <int kT, int kC, int kWavesOf, bool kTall, bool kVec, typename G>
+__device__ __forceinline__ void apply_blocks(const MuonMatrix& mat, const MuonArgs& a, float step,
+                                             int start, int end, int wave, const double* s_w) {
+  constexpr int kN = kTall ? 4 : kC, kX = kTall ? kC : 4;  // elements of a vector, vectors
+  const int lane = threadIdx.x & 63, li = lane & 15, lg = lane >> 4;
+  const int r = mat.r, len = static_cast<int>(mat.len);
+  const Global<const G> g = global(static_cast<const G*>(mat.g));
+  const Global<float> m = global(mat.m), p = global(mat.p);
+  const Global<uint16_t> p_bf16 = global(mat.p_bf16);
+  uint32_t place[kX];  // of the lane's vectors behind a tile's first element
+#pragma unroll
+  for (int x = 0; x < kX; ++x)
+    place[x] = kTall ? static_cast<uint32_t>((16 * x + li) * r + 4 * lg)
+                     : static_cast<uint32_t>(4 * x + lg) * static_cast<uint32_t>(len) + kC * li;
+  // a block's first element in tile t, and how many elements of vector x there are;
+  // the block's place is hidden from the compiler, which would keep a pointer for
+  // each vector and step all of them (128 registers)
+  auto tile_at = [&](int64_t block, int t) {
+    return block + (kTall ? 16 * t : static_cast<int64_t>(16 * t) * len);
+  };
+  auto count = [&](int k0, int t, int x) {
+    if constexpr (kTall) return k0 + 16 * x + li < end ? r - 16 * t - 4 * lg : 0;
+    return 16 * t + 4 * x + lg < r ? end - k0 - kC * li : 0;
+  };
+  float gv[2][kX][kN], mv[2][kX][kN];
+  auto load = [&](int k0, int64_t block, int t) {
+#pragma unroll
+    for (int x = 0; x < kX; ++x) {
+      const int n = count(k0, t, x);
+      load_some<kVec, kN, G>(lane_ptr(g + tile_at(block, t), place[x]), n, gv[t & 1][x]);
+      load_some<kVec, kN, float>(lane_ptr((Global<const float>)m + tile_at(block, t), place[x]), n,
+                                 mv[t & 1][x]);
+    }
+  };
+  for (int k0 = start + wave * 16 * kC; k0 < end; k0 += kWavesOf * 16 * kC) {
+    int64_t block = kTall ? static_cast<int64_t>(k0) * r : k0;
+    asm volatile("" : "+s"(block));
+    f64x4_t acc[kT][kC];
+#pragma unroll
+    for (int h = 0; h < kT; ++h)
+#pragma unroll
+      for (int c = 0; c < kC; ++c) acc[h][c] = f64x4_t{0.0, 0.0, 0.0, 0.0};
+    // T's operands are read in every block anew: held over the loop, as they would
+    // be if the compiler knew where they lie, they take 32 kT^2 registers
+    int from = lane;
+    asm volatile("" : "+v"(from));
+    load(k0, block, 0);
+#pragma unroll
+    for (int t = 0; t < kT; ++t) {
+      if (t + 1 < kT) load(k0, block, t + 1);
+      float u[kX][kN];
+#pragma unroll
+      for (int x = 0; x < kX; ++x) {
+        momentum(a, gv[t & 1][x], mv[t & 1][x], u[x]);
+        store_some<kVec>(lane_ptr(m + tile_at(block, t), place[x]), count(k0, t, x), mv[t & 1][x]);
+      }
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        double b[kC];
+#pragma unroll
+        for (int c = 0; c < kC; ++c) b[c] = static_cast<double>(kTall ? u[c][q] : u[q][c]);
+#pragma unroll
+        for (int h = 0; h < kT; ++h) {
+          const double w = s_w[((h * kT + t) * 4 + q) * 64 + from];
+#pragma unroll
+          for (int c = 0; c < kC; ++c) acc[h][c] = mfma64(w, b[c], acc[h][c]);
+        }
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    }
+#pragma unroll
+    for (int h = 0; h < kT; ++h) {
+      float pv[kX][kN];
+#pragma unroll
+      for (int x = 0; x < kX; ++x)
+        load_some<kVec, kN, float>(lane_ptr((Global<const float>)p + tile_at(block, h), place[x]),
+                                   count(k0, h, x), pv[x]);
+#pragma unroll
+      for (int x = 0; x < kX; ++x) {
+        float (&v)[kN] = pv[x];
+#pragma unroll
+        for (int e = 0; e < kN; ++e) {
+          const double o = kTall ? acc[h][x][e] : acc[h][e][x];
+          v[e] = fmaf(-step, static_cast<float>(o), v[e] * a.decay);
+        }
+        const int n = count(k0, h, x);
+        store_some<kVec>(lane_ptr(p + tile_at(block, h), place[x]), n, v);
+        if (p_bf16) store_some<kVec>(lane_ptr(p_bf16 + tile_at(block, h), place[x]), n, v);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  }
+}
+
+// Product of two symmetric 16 x 16 matrices that commute, in the order of the
+// results: a register is what the instruction takes of either operand.
+__device__ __forceinline__ f64x4_t tile_product(f64x4_t x, f64x4_t y) {
+  f64x4_t acc = f64x4_t{0.0, 0.0, 0.0, 0.0};
+#pragma unroll
+  for (int s = 0; s < 4; ++s) acc = mfma64(x[s], y[s], acc);
+  return acc;
+}
+
+// The steps on one tile, in every workgroup that needs the result and in each of
+// its waves alike, in registers: 17 products of 4 instructions, which costs less
+// than a launch between the passes.  The chunks' sums are added a quarter per
+// wave first.
+__device__ __forceinline__ void one_tile_steps(const MuonMatrix& mat, const MuonArgs& a,
+                                               const double* ws, int wave, double* s_w) {
+  __shared__ f64x4_t s_sum[kWaves][64];
+  const int lane = threadIdx.x & 63, li = lane & 15, lg = lane >> 4;
+  const f64x4_t* part = reinterpret_cast<const f64x4_t*>(ws + mat.part) + lane;
+  f64x4_t s = f64x4_t{0.0, 0.0, 0.0, 0.0};
+#pragma unroll 8
+  for (int i = wave; i < mat.chunks; i += kWaves) s += part[static_cast<int64_t>(i) * 64];
+  s_sum[wave][lane] = s;
+  __syncthreads();
+  s = s_sum[0][lane];
+#pragma unroll
+  for (int w = 1; w < kWaves; ++w) s += s_sum[w][lane];
+  // lane (li, lg) holds the diagonal's li where lg = li % 4
+  double norm2 = 0.0;
+#pragma unroll
+  for (int v = 0; v < 4; ++v)
+    if (4 * v + lg == li) norm2 = s[v];
+#pragma unroll
+  for (int off = 32; off >= 1; off >>= 1) norm2 += __shfl_xor(norm2, off, 64);
+  const double inv = 1.0 / (sqrt(norm2) + static_cast<double>(a.eps));
+  s *= inv * inv;
+  f64x4_t x = s;
+  for (int n = 0; n < a.steps; ++n) {
+    f64x4_t q = a.cc * tile_product(s, s) + a.cb * s;
+#pragma unroll
+    for (int v = 0; v < 4; ++v)
+      if (4 * v + lg == li) q[v] += a.ca;
+    x = n == 0 ? q : tile_product(x, q);
+    s = tile_product(tile_product(s, q), q);
+  }
+#pragma unroll
+  for (int v = 0; v < 4; ++v) s_w[factor_place<1>(mat.tall, 4 * v + lg, li)] = x[v] * inv;
+}
+
+// 8 waves where T takes all of a CU's LDS but for one workgroup.
+template <int kT>
+constexpr int kApplyWaves = kT == 8 ? 8 : kWaves;
+
 template <int kT, typename G>
-__global__ __launch_bounds__(kThreads) void muon_apply_kernel(const MuonMatrix* __restrict__ mats,
+__global__ __launch_bounds__(64 * kApplyWaves<kT>, kT <= 2 ? 4 : kT == 4 ? 3 : 2) void muon_apply_kernel(const MuonMatrix* __restrict__ mats,
                                                               const MuonChunk* __restrict__ chunks,
                                                               MuonArgs a,
                                                               const double* __restrict__ ws) {
-  constexpr int kLen = 256 / kT, kPitch = kLen + 16;  // a step's 4 rows in different banks
-  typedef Runs<kT, kPitch> R;
-  // a wave's row tiles and column tiles of a run, 4 tiles in all
-  constexpr int kRT = kT == 8 ? 2 : 1, kCT = 4 / kRT;
-  constexpr int kRowGroups = kT / kRT, kSteps = 4 * kT;
-  __shared__ __attribute__((aligned(16))) float s_u[kT * 16 * kPitch], s_o[kT * 16 * kPitch];
+  __shared__ __attribute__((aligned(16))) double s_w[256 * kT * kT];
   const MuonChunk c = chunks[blockIdx.x];
   const MuonMatrix mat = mats[c.matrix];
-  const int t = threadIdx.x, lane = t & 63, li = lane & 15, lg = lane >> 4;
-  const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
-  const int row_tile = wave % kRowGroups, col_tile = wave / kRowGroups * kCT;
-  const int64_t start = c.index * mat.chunk;
-  const int64_t end = start + mat.chunk < mat.len ? start + mat.chunk : mat.len;
-  const R runs(mat);
-  const G* g = static_cast<const G*>(mat.g);
-  for (int i = t; i < kT * 16 * kPitch; i += kThreads) s_u[i] = 0.0f;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int start = static_cast<int>(c.index * mat.span);
+  const int end = static_cast<int>(start + mat.span < mat.len ? start + mat.span : mat.len);
   const double rows = static_cast<double>(mat.tall ? mat.len : mat.r);
   const double cols = static_cast<double>(mat.tall ? mat.r : mat.len);
   const double most = rows > cols ? rows : cols;
   const double f = a.rms ? 0.2 * sqrt(most) : rows > cols ? sqrt(rows / cols) : 1.0;
   const float step = static_cast<float>(static_cast<double>(a.lr) * f);
-  double w[kRT][kSteps];
-#pragma unroll
-  for (int h = 0; h < kRT; ++h)
-#pragma unroll
-    for (int s = 0; s < kSteps; ++s)
-      w[h][s] = ws[mat.factor + ((row_tile + h * kRowGroups) * kSteps + s) * 64 + lane];
-  float gv[R::kGroups][4], mv[R::kGroups][4], pv[R::kGroups][4];
-  auto load = [&](int64_t k0) {
-#pragma unroll
-    for (int j = 0; j < R::kGroups; ++j) {
-      const int64_t at = runs.at(j, k0), left = runs.left(j, k0, end);
-      load4(g + at, left, runs.vec, gv[j]);
-      load4(mat.m + at, left, runs.vec, mv[j]);
-    }
-  };
-  load(start);
-  __syncthreads();
-  for (int64_t k0 = start; k0 < end; k0 += kLen) {
-#pragma unroll
-    for (int j = 0; j < R::kGroups; ++j) {
-      const int64_t at = runs.at(j, k0), left = runs.left(j, k0, end);
-      float u[4];
-      momentum4(a, gv[j], mv[j], u);
-      store4(mat.m + at, left, runs.vec, mv[j]);
-      load4(mat.p + at, left, runs.vec, pv[j]);
-#pragma unroll
-      for (int e = 0; e < 4; ++e)
-        if (runs.place[j][e] >= 0) s_u[runs.place[j][e]] = e < left ? u[e] : 0.0f;
-    }
-    __syncthreads();
-    if (k0 + kLen < end) load(k0 + kLen);
-    f64x4_t acc[kRT][kCT];
-#pragma unroll
-    for (int h = 0; h < kRT; ++h)
-#pragma unroll
-      for (int q = 0; q < kCT; ++q) acc[h][q] = f64x4_t{0.0, 0.0, 0.0, 0.0};
-#pragma unroll
-    for (int s = 0; s < kSteps; ++s) {
-      double b[kCT];
-#pragma unroll
-      for (int q = 0; q < kCT; ++q)
-        b[q] = static_cast<double>(s_u[(4 * s + lg) * kPitch + 16 * (col_tile + q) + li]);
-#pragma unroll
-      for (int h = 0; h < kRT; ++h)
-#pragma unroll
-        for (int q = 0; q < kCT; ++q) acc[h][q] = mfma64(w[h][s], b[q], acc[h][q]);
-    }
-#pragma unroll
-    for (int h = 0; h < kRT; ++h)
-#pragma unroll
-      for (int q = 0; q < kCT; ++q)
-#pragma unroll
-        for (int v = 0; v < 4; ++v)
-          s_o[(16 * (row_tile + h * kRowGroups) + 4 * v + lg) * kPitch + 16 * (col_tile + q) + li] =
-              static_cast<float>(acc[h][q][v]);
-    __syncthreads();
-#pragma unroll
-    for (int j = 0; j < R::kGroups; ++j) {
-      const int64_t at = runs.at(j, k0), left = runs.left(j, k0, end);
-#pragma unroll
-      for (int e = 0; e < 4; ++e)
-        if (runs.place[j][e] >= 0)
-          pv[j][e] = fmaf(-step, s_o[runs.place[j][e]], pv[j][e] * a.decay);
-      store4(mat.p + at, left, runs.vec, pv[j]);
-      if (mat.p_bf16) store4(mat.p_bf16 + at, left, runs.vec, pv[j]);
-    }
+  if constexpr (kT == 1) {
+    one_tile_steps(mat, a, ws, wave, s_w);
+  } else {
+    for (int i = threadIdx.x * 2; i < 256 * kT * kT; i += 128 * kApplyWaves<kT>)
+      *reinterpret_cast<double2*>(s_w + i) =
+          *reinterpret_cast<const double2*>(ws + mat.factor + i);
   }
+  __syncthreads();
+  constexpr int kC = kT == 1 ? 4 : 2, kW = kApplyWaves<kT>;
+  if (mat.tall && (mat.r & 3) == 0)
+    apply_blocks<kT, kC, kW, true, true, G>(mat, a, step, start, end, wave, s_w);
+  else if (mat.tall)
+    apply_blocks<kT, kC, kW, true, false, G>(mat, a, step, start, end, wave, s_w);
+  else if ((mat.len & 3) == 0)
+    apply_blocks<kT, kC, kW, false, true, G>(mat, a, step, start, end, wave, s_w);
+  else
+    apply_blocks<kT, kC, kW, false, false, G>(mat, a, step, start, end, wave, s_w);
 }
 
 template <int kT>
 hipError_t launch_class(const MuonMatrix* mats, const MuonMatrix* of, int64_t matrices,
-                        const MuonChunk* chunks, int64_t n, bool bf16_grad, const MuonStep& h, const MuonArgs& a, double* ws,
+                        const MuonChunk* chunks, int64_t nchunks, int64_t nspans, bool bf16_grad, const MuonArgs& a, double* ws,
                         hipStream_t st) {
-  if (n == 0) return hipSuccess;
-  const dim3 grid(static_cast<uint32_t>(n));
+  if (matrices == 0) return hipSuccess;
+  const dim3 grid(static_cast<uint32_t>(nchunks)), grid2(static_cast<uint32_t>(nspans));
+  const MuonChunk* spans = chunks + nchunks;
   if (bf16_grad)
     hipLaunchKernelGGL((muon_gram_kernel<kT, uint16_t>), grid, dim3(kThreads), 0, st, mats, chunks,
                        a, ws);
@@ -483,42 +593,45 @@ hipError_t launch_class(const MuonMatrix* mats, const MuonMatrix* of, int64_t ma
     hipLaunchKernelGGL((muon_gram_kernel<kT, float>), grid, dim3(kThreads), 0, st, mats, chunks, a,
                        ws);
   if (hipError_t e = hipGetLastError(); e != hipSuccess) return e;
-  hipLaunchKernelGGL(muon_steps_kernel<kT>, dim3(static_cast<uint32_t>(matrices)),
-                     dim3(64 * Steps<kT>::kWavesOf), 0, st, of, h.a, h.b, h.c, h.steps, h.eps, ws);
-  if (hipError_t e = hipGetLastError(); e != hipSuccess) return e;
+  if constexpr (kT > 1) {
+    hipLaunchKernelGGL(muon_steps_kernel<kT>, dim3(static_cast<uint32_t>(matrices)),
+                       dim3(64 * Steps<kT>::kWavesOf), 0, st, of, a, ws);
+    if (hipError_t e = hipGetLastError(); e != hipSuccess) return e;
+  }
   if (bf16_grad)
-    hipLaunchKernelGGL((muon_apply_kernel<kT, uint16_t>), grid, dim3(kThreads), 0, st, mats,
-                       chunks, a, ws);
+    hipLaunchKernelGGL((muon_apply_kernel<kT, uint16_t>), grid2, dim3(64 * kApplyWaves<kT>), 0, st,
+                       mats, spans, a, ws);
   else
-    hipLaunchKernelGGL((muon_apply_kernel<kT, float>), grid, dim3(kThreads), 0, st, mats, chunks, a,
-                       ws);
+    hipLaunchKernelGGL((muon_apply_kernel<kT, float>), grid2, dim3(64 * kApplyWaves<kT>), 0, st,
+                       mats, spans, a, ws);
   return hipGetLastError();
 }
 
 }  // namespace
 
-hipError_t launch_muon(const MuonMatrix* mats, const MuonChunk* chunks,
-                       const int64_t (&matrices)[kMuonClasses], const int64_t (&nchunks)[kMuonClasses],
+hipError_t launch_muon(const MuonMatrix* mats, const MuonChunk* chunks, const MuonCounts& n,
                        bool bf16_grad, const MuonStep& h, void* ws, hipStream_t st) {
   MuonArgs a;
   a.mu = h.momentum;
   a.one_minus_mu = static_cast<float>(1.0 - static_cast<double>(h.momentum));
   a.decay = static_cast<float>(1.0 - static_cast<double>(h.lr) * static_cast<double>(h.weight_decay));
   a.lr = h.lr;
+  a.eps = h.eps;
+  a.ca = h.a, a.cb = h.b, a.cc = h.c;
+  a.steps = h.steps;
   a.nesterov = h.nesterov;
   a.rms = h.rms;
   double* w = static_cast<double*>(ws);
-  int64_t m = 0, c = 0;
+  const MuonMatrix* of = mats;  // a chunk names its matrix from the table's start
   hipError_t e = hipSuccess;
   for (int k = 0; k < kMuonClasses && e == hipSuccess; ++k) {
-    // a chunk names its matrix from the table's start, the steps from the class's
-    const MuonMatrix* of = mats + m;
-    const int64_t n = matrices[k], nc = nchunks[k];
-    e = k == 0   ? launch_class<1>(mats, of, n, chunks + c, nc, bf16_grad, h, a, w, st)
-        : k == 1 ? launch_class<2>(mats, of, n, chunks + c, nc, bf16_grad, h, a, w, st)
-        : k == 2 ? launch_class<4>(mats, of, n, chunks + c, nc, bf16_grad, h, a, w, st)
-                 : launch_class<8>(mats, of, n, chunks + c, nc, bf16_grad, h, a, w, st);
-    m += n, c += nc;
+    const int64_t m = n.matrices[k], c = n.chunks[k], s = n.spans[k];
+    e = k == 0   ? launch_class<1>(mats, of, m, chunks, c, s, bf16_grad, a, w, st)
+        : k == 1 ? launch_class<2>(mats, of, m, chunks, c, s, bf16_grad, a, w, st)
+        : k == 2 ? launch_class<4>(mats, of, m, chunks, c, s, bf16_grad, a, w, st)
+                 : launch_class<8>(mats, of, m, chunks, c, s, bf16_grad, a, w, st);
+    of += m;
+    chunks += c + s;
   }
   return e;
 }

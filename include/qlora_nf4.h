@@ -785,7 +785,7 @@ QN_API int lora_adamw_multi_step(const qn_adamw_plan* plan, const void* table,
  *   m        fp32[rows, cols], the momentum, updated in place (starts as zeros).
  *   p_bf16   bf16[rows, cols] out (the new p rounded to bf16), or NULL.
  *   rows, cols  the smaller of the two at most 128 (QN_ERR_UNSUPPORTED), the
- *            larger below 2^31; a matrix without elements is skipped, its
+ *            larger below 2^24; a matrix without elements is skipped, its
  *            pointers not read.
  */
 typedef struct qn_muon_tensor {
@@ -800,7 +800,8 @@ typedef struct qn_muon_tensor {
 /* What lora_muon_table built; the calls that take a table take its plan. */
 typedef struct qn_muon_plan {
   int64_t matrices[4];  /* by smaller side: up to 16, 32, 64, 128 */
-  int64_t chunks[4];    /* workgroups of a pass over them */
+  int64_t chunks[4];    /* workgroups of the first pass over them */
+  int64_t spans[4];     /* and of the last */
   int64_t bytes;        /* bytes of the table */
   int64_t ws_bytes;     /* and of the workspace */
   int32_t grad_dtype;   /* QN_F32 or QN_BF16 */

@@ -39,35 +39,58 @@ def hyper(lr=1e-3, momentum=0.95, weight_decay=0.1, eps=1e-7, ns=(3.4445, -4.775
                            nesterov, adjust)
 
 
+def parse(plan, host, size):
+    """Matrices as (64-bit fields, 32-bit fields), entries as [matrix, index]."""
+    n = sum(plan.matrices)
+    wide = host[:n * 88].view(np.int64).reshape(n, 11)
+    small = host[:n * 88].view(np.int32).reshape(n, 22)[:, 18:]
+    return wide, small, host[n * 88:size].view(np.int32).reshape(-1, 2)
+
+
+LEN, CHUNK, SPAN, PART, FACTOR = range(4, 9)
+
+
 def test_table_counts_and_order(lib):  # noqa: F811
     shapes = [(128, 300), (16, 16), (5000, 17), (1, 9), (0, 7), (64, 64), (33, 40), (7, 0)]
     st, plan, host, size = build(tensors(*shapes))
     assert st == qn.QN_OK and plan.bytes == size
     assert list(plan.matrices) == [2, 1, 2, 1]
-    assert list(plan.chunks) == [2, 40, 2, 10]
-    assert size == 6 * 80 + 54 * 8
+    # few matrices: a chunk and a span for each run of 256
+    assert list(plan.chunks) == list(plan.spans) == [2, 20, 2, 2]
+    assert size == 6 * 88 + 2 * 26 * 8
     # doubles: a chunk's sums, and the factor of each matrix
     want = sum(c * t * (t + 1) // 2 * 256 + m * 256 * t * t
                for c, m, t in zip(plan.chunks, plan.matrices, (1, 2, 4, 8)))
     assert lib.lora_muon_workspace_bytes(ctypes.byref(plan)) == plan.ws_bytes == 8 * want
     # the entries lie by class, each with its own room
-    ints = host[:6 * 80].view(np.int64).reshape(6, 10)
-    assert ints[:, 4].tolist() == [16, 9, 5000, 64, 40, 300]
-    r = host[:6 * 80].view(np.int32).reshape(6, 20)[:, 16:]
-    assert r[:, 0].tolist() == [16, 1, 17, 64, 33, 128]
-    assert r[:, 1].tolist() == [0, 0, 1, 0, 0, 0]
-    ends = ints[:, 7] + 256 * np.array([1, 1, 4, 16, 16, 64])
-    assert (ints[1:, 6] == ends[:-1]).all() and ends[-1] == want
-    chunks = host[6 * 80:size].view(np.int32).reshape(-1, 2)
-    assert (np.bincount(chunks[:, 0]) == r[:, 2]).all()
+    wide, small, entries = parse(plan, host, size)
+    assert wide[:, LEN].tolist() == [16, 9, 5000, 64, 40, 300]
+    assert small[:, 0].tolist() == [16, 1, 17, 64, 33, 128]
+    assert small[:, 1].tolist() == [0, 0, 1, 0, 0, 0]
+    ends = wide[:, FACTOR] + 256 * np.array([1, 1, 4, 16, 16, 64])
+    assert (wide[1:, PART] == ends[:-1]).all() and ends[-1] == want
+    at, first = 0, 0
+    for m, c, s in zip(plan.matrices, plan.chunks, plan.spans):
+        for n, col in ((c, 2), (s, 3)):
+            part = entries[at:at + n]
+            assert (np.bincount(part[:, 0] - first, minlength=m) == small[first:first + m, col]).all()
+            at += n
+        first += m
+    assert at == len(entries)
 
 
 def test_long_matrices_and_many(lib):  # noqa: F811
-    st, plan, host, _ = build(tensors((16, 10_000_000), (2 ** 31 - 1, 1)))
-    assert st == qn.QN_OK and max(plan.chunks) <= 512
-    st, plan, _, _ = build(tensors(*[(16, 4096)] * 448))
-    # 7168 runs over 1536 workgroups: 5 runs each
-    assert st == qn.QN_OK and list(plan.chunks) == [448 * 4, 0, 0, 0]
+    st, plan, host, size = build(tensors((16, 10_000_000), (2 ** 24 - 1, 1)))
+    assert st == qn.QN_OK and sum(plan.chunks) <= 512 and sum(plan.spans) >= 2048
+    for shape in ((16, 4096), (64, 4096)):
+        st, plan, host, size = build(tensors(*[shape] * 448))
+        wide, small, _ = parse(plan, host, size)
+        # nearly equal parts of the 16 runs, for either pass
+        for length, count in ((CHUNK, 2), (SPAN, 3)):
+            assert st == qn.QN_OK and (wide[:, length] % 256 == 0).all()
+            assert (small[:, count] * wide[:, length] >= 4096).all()
+            assert ((small[:, count] - 1) * wide[:, length] < 4096).all()
+    assert sum(plan.chunks) < sum(plan.spans)
 
 
 def test_table_refusals(lib):  # noqa: F811
@@ -91,7 +114,7 @@ def test_table_refusals(lib):  # noqa: F811
     assert build(tensors(good, good))[0] == qn.QN_ERR_SHAPE
     other = (2 * A, good[1], 3 * A, None, 4, 64)
     assert build(tensors(good, other))[0] == qn.QN_OK
-    for shape in ((-1, 4), (4, -1), (2 ** 31, 1), (1, 2 ** 40)):
+    for shape in ((-1, 4), (4, -1), (2 ** 24, 1), (1, 2 ** 40)):
         assert build(tensors(shape))[0] == qn.QN_ERR_SHAPE
         assert lib.lora_muon_table_bytes(tensors(shape), 1) == 0
     assert build(tensors((129, 130)))[0] == qn.QN_ERR_UNSUPPORTED
@@ -145,7 +168,8 @@ def test_step_refusals(lib):  # noqa: F811
 @pytest.mark.parametrize("shape", [(1, 1), (16, 257), (17, 129), (129, 33), (100, 100)])
 def test_chunks_cover_the_long_side(lib, shape):  # noqa: F811
     _, plan, host, size = build(tensors(shape))
-    m = host[:80].view(np.int64)
-    assert m[4] == max(shape)
-    n, chunk = host[:80].view(np.int32)[18], m[5]
-    assert sum(plan.chunks) == n and (n - 1) * chunk < max(shape) <= n * chunk
+    wide, small, _ = parse(plan, host, size)
+    assert wide[0, LEN] == max(shape)
+    for length, count, total in ((CHUNK, 2, plan.chunks), (SPAN, 3, plan.spans)):
+        n, part = small[0, count], wide[0, length]
+        assert sum(total) == n and (n - 1) * part < max(shape) <= n * part
