@@ -574,7 +574,8 @@ constexpr int64_t kMuonMaxLong = (int64_t{1} << 24) - 1;
 struct MuonShape {
   int64_t r, len;
   int cls, tiles;  // class, tiles of 16 of the short side
-  int64_t runs;    // of kMuonRun elements of the long side
+  int64_t run;     // kMuonRun of the class
+  int64_t runs;    // of the long side
 };
 
 int muon_shape(const qn_muon_tensor& t, MuonShape& s) {
@@ -590,7 +591,8 @@ int muon_shape(const qn_muon_tensor& t, MuonShape& s) {
   s.cls = 0;
   while (16 * qn::kMuonTiles[s.cls] < s.r) ++s.cls;
   s.tiles = qn::kMuonTiles[s.cls];
-  s.runs = (s.len + qn::kMuonRun - 1) / qn::kMuonRun;
+  s.run = qn::kMuonRun[s.cls];
+  s.runs = qn::mx_tiles(s.len, s.run);
   return QN_OK;
 }
 
@@ -1199,8 +1201,8 @@ int lora_muon_table(const qn_muon_tensor* t, int32_t count, int32_t grad_dtype, 
       const int32_t n = static_cast<int32_t>(qn::mx_tiles(s.runs, per));
       const int32_t n2 = static_cast<int32_t>(qn::mx_tiles(s.runs, per2));
       const int64_t factor = at + n * muon_sums(s);
-      *mats++ = qn::MuonMatrix{t[i].p, t[i].g, t[i].m, t[i].p_bf16, s.len, per * qn::kMuonRun,
-                               per2 * qn::kMuonRun, at, factor, static_cast<int32_t>(s.r),
+      *mats++ = qn::MuonMatrix{t[i].p, t[i].g, t[i].m, t[i].p_bf16, s.len, per * s.run,
+                               per2 * s.run, at, factor, static_cast<int32_t>(s.r),
                                t[i].rows > t[i].cols ? 1 : 0, n, n2};
       for (int32_t c = 0; c < n; ++c) *chunk++ = qn::MuonChunk{index, c};
       for (int32_t c = 0; c < n2; ++c) *span++ = qn::MuonChunk{index, c};

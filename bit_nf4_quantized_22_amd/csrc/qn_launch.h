@@ -304,7 +304,9 @@ struct MuonChunk {
 };
 constexpr int kMuonClasses = 4;
 constexpr int kMuonTiles[kMuonClasses] = {1, 2, 4, 8};  // of 16 rows
-constexpr int kMuonRun = 256;  // of the long side, a block of 64 for each wave
+// What a workgroup of the passes takes at a time of the long side: 64 (or 32) for
+// each of its waves.
+constexpr int kMuonRun[kMuonClasses] = {256, 128, 128, 256};
 struct MuonStep {
   float lr, momentum, weight_decay, eps;
   double a, b, c;

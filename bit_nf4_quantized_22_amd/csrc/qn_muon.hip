@@ -46,11 +46,14 @@ __device__ __forceinline__ f64x4_t mfma64(double a, double b, f64x4_t c) {
 
 constexpr int upper_tiles(int t) { return t * (t + 1) / 2; }
 
-// Tile (row, column) number q of those on and above the diagonal.
-template <int kT>
-__device__ __forceinline__ void upper_tile(int q, int& a, int& b) {
+// Number of tile (a, b), a <= b, of t x t, and the q-th tile.
+__host__ __device__ constexpr int upper_index(int t, int a, int b) {
+  return a * t - a * (a - 1) / 2 + (b - a);
+}
+
+__device__ __forceinline__ void upper_tile(int t, int q, int& a, int& b) {
   a = 0;
-  while (q >= kT - a) q -= kT - a++;
+  while (q >= t - a) q -= t - a++;
   b = a + q;
 }
 
@@ -186,11 +189,12 @@ __device__ __forceinline__ void gram_blocks(const MuonMatrix& mat, const MuonArg
         double f[kT];
 #pragma unroll
         for (int t = 0; t < kT; ++t) f[t] = static_cast<double>(u[t][e]);
-        int q = 0;
 #pragma unroll
-        for (int x = 0; x < kT; ++x)
+        for (int y = 0; y < kT; ++y)
+          if (kT < 4 || 16 * y < r)
 #pragma unroll
-          for (int y = x; y < kT; ++y, ++q) acc[q] = mfma64(f[x], f[y], acc[q]);
+            for (int x = 0; x <= y; ++x)
+              acc[upper_index(kT, x, y)] = mfma64(f[x], f[y], acc[upper_index(kT, x, y)]);
       }
     }
   };
@@ -243,34 +247,23 @@ __global__ __launch_bounds__(kThreads) void muon_gram_kernel(const MuonMatrix* _
 }
 
 // The steps on one matrix's S, a workgroup each: wave w holds the tiles w, w + W,
-// ... of S, Q and T in registers, and products read their operands, two at a
-// time, from LDS.
-template <int kT>
-struct Steps {
-  static constexpr int kTiles = upper_tiles(kT);
-  static constexpr int kOwn = kT == 8 ? 3 : 1, kWavesOf = kTiles / kOwn;
-  static constexpr int kPitch = 17, kTile = 16 * kPitch;  // doubles
-  static_assert(kOwn * kWavesOf == kTiles, "tiles of a wave");
-};
+// ... of S, Q and T in registers (of the kN x kN that r reaches: 5 x 5 for r =
+// 74), and products read their operands, two at a time, from LDS.
+constexpr int kStepPitch = 17, kStepTile = 16 * kStepPitch;  // doubles
 
-__device__ __forceinline__ int upper_index(int t, int a, int b) {
-  return a * t - a * (a - 1) / 2 + (b - a);
-}
-
-template <int kT>
+template <int kN>
 __device__ __forceinline__ f64x4_t tile_product(const double* x, const double* y, int a, int b,
                                                 int li, int lg) {
-  typedef Steps<kT> P;
   f64x4_t acc = f64x4_t{0.0, 0.0, 0.0, 0.0};
-#pragma unroll(kT == 8 ? 2 : kT)
-  for (int c = 0; c < kT; ++c) {
+#pragma unroll(kN > 5 ? 2 : kN)
+  for (int c = 0; c < kN; ++c) {
     // X(a, c)[li][4 s + lg] and Y(c, b)[4 s + lg][li], or the other half's
     const bool xu = a <= c, yu = c <= b;
-    const double* px = x + upper_index(kT, xu ? a : c, xu ? c : a) * P::kTile +
-                       (xu ? li * P::kPitch + lg : lg * P::kPitch + li);
-    const double* py = y + upper_index(kT, yu ? c : b, yu ? b : c) * P::kTile +
-                       (yu ? lg * P::kPitch + li : li * P::kPitch + lg);
-    const int dx = xu ? 4 : 4 * P::kPitch, dy = yu ? 4 * P::kPitch : 4;
+    const double* px = x + upper_index(kN, xu ? a : c, xu ? c : a) * kStepTile +
+                       (xu ? li * kStepPitch + lg : lg * kStepPitch + li);
+    const double* py = y + upper_index(kN, yu ? c : b, yu ? b : c) * kStepTile +
+                       (yu ? lg * kStepPitch + li : li * kStepPitch + lg);
+    const int dx = xu ? 4 : 4 * kStepPitch, dy = yu ? 4 * kStepPitch : 4;
 #pragma unroll
     for (int s = 0; s < 4; ++s) acc = mfma64(px[s * dx], py[s * dy], acc);
   }
@@ -290,65 +283,71 @@ __device__ __forceinline__ int factor_place(bool tall, int i, int j) {
   return (((i >> 4) * kT + (j >> 4)) * 4 + q) * 64 + lg * 16 + li;
 }
 
-template <int kT>
-__global__ __launch_bounds__(64 * Steps<kT>::kWavesOf) void muon_steps_kernel(
-    const MuonMatrix* __restrict__ mats, MuonArgs a, double* __restrict__ ws) {
-  typedef Steps<kT> P;
-  __shared__ __attribute__((aligned(16))) double s_x[P::kTiles * P::kTile];
-  __shared__ __attribute__((aligned(16))) double s_y[P::kTiles * P::kTile];
-  __shared__ double s_diag[16 * kT];
-  const MuonMatrix mat = mats[blockIdx.x];
+template <int kT, int kN, int kWavesOf>
+__device__ __forceinline__ void tile_steps(const MuonMatrix& mat, const MuonArgs& a, double* ws,
+                                           double* s_x, double* s_y, double* s_diag) {
+  constexpr int kTiles = upper_tiles(kN), kOwn = (kTiles + kWavesOf - 1) / kWavesOf;
   const int t = threadIdx.x, lane = t & 63, li = lane & 15, lg = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
-  int ta[P::kOwn], tb[P::kOwn];
-  f64x4_t s[P::kOwn], q[P::kOwn], x[P::kOwn];
+  int ta[kOwn], tb[kOwn];
+  bool have[kOwn];
+  f64x4_t s[kOwn], q[kOwn], x[kOwn];
   // the chunks' sums, in their order
 #pragma unroll
-  for (int d = 0; d < P::kOwn; ++d) {
-    const int n = wave + P::kWavesOf * d;
-    upper_tile<kT>(n, ta[d], tb[d]);
-    const f64x4_t* part = reinterpret_cast<const f64x4_t*>(ws + mat.part) + n * 64 + lane;
+  for (int d = 0; d < kOwn; ++d) {
+    const int n = wave + kWavesOf * d;
+    have[d] = n < kTiles;
+    upper_tile(kN, have[d] ? n : 0, ta[d], tb[d]);
+    const f64x4_t* part = reinterpret_cast<const f64x4_t*>(ws + mat.part) +
+                          upper_index(kT, ta[d], tb[d]) * 64 + lane;
+    constexpr int kStride = upper_tiles(kT) * 64;
     f64x4_t sum = f64x4_t{0.0, 0.0, 0.0, 0.0};
     int i = 0;
     for (; i + 8 <= mat.chunks; i += 8) {
       f64x4_t v[8];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] = part[static_cast<int64_t>(i + e) * (P::kTiles * 64)];
+      for (int e = 0; e < 8; ++e) v[e] = part[static_cast<int64_t>(i + e) * kStride];
 #pragma unroll
       for (int e = 0; e < 8; ++e) sum += v[e];
     }
-    for (; i < mat.chunks; ++i) sum += part[static_cast<int64_t>(i) * (P::kTiles * 64)];
+    for (; i < mat.chunks; ++i) sum += part[static_cast<int64_t>(i) * kStride];
     s[d] = sum;
 #pragma unroll
     for (int v = 0; v < 4; ++v)
-      if (ta[d] == tb[d] && 4 * v + lg == li) s_diag[16 * ta[d] + li] = sum[v];
+      if (have[d] && ta[d] == tb[d] && 4 * v + lg == li) s_diag[16 * ta[d] + li] = sum[v];
   }
   __syncthreads();
   double norm2 = 0.0;
 #pragma unroll 8
-  for (int i = 0; i < 16 * kT; ++i) norm2 += s_diag[i];
+  for (int i = 0; i < 16 * kN; ++i) norm2 += s_diag[i];
   const double inv = 1.0 / (sqrt(norm2) + static_cast<double>(a.eps));
 
-  auto store = [&](double* to, const f64x4_t (&m)[P::kOwn]) {
+  auto store = [&](double* to, const f64x4_t (&m)[kOwn]) {
 #pragma unroll
-    for (int d = 0; d < P::kOwn; ++d)
+    for (int d = 0; d < kOwn; ++d)
+      if (have[d])
 #pragma unroll
-      for (int v = 0; v < 4; ++v)
-        to[(wave + P::kWavesOf * d) * P::kTile + (4 * v + lg) * P::kPitch + li] = m[d][v];
+        for (int v = 0; v < 4; ++v)
+          to[(wave + kWavesOf * d) * kStepTile + (4 * v + lg) * kStepPitch + li] = m[d][v];
   };
-  auto product = [&](f64x4_t (&to)[P::kOwn]) {
+  auto product = [&](f64x4_t (&to)[kOwn]) {
 #pragma unroll
-    for (int d = 0; d < P::kOwn; ++d) to[d] = tile_product<kT>(s_x, s_y, ta[d], tb[d], li, lg);
+    for (int d = 0; d < kOwn; ++d)
+      if (have[d]) to[d] = tile_product<kN>(s_x, s_y, ta[d], tb[d], li, lg);
   };
 #pragma unroll
-  for (int d = 0; d < P::kOwn; ++d) s[d] *= inv * inv;
+  for (int d = 0; d < kOwn; ++d) {
+    s[d] *= inv * inv;
+    x[d] = q[d] = s[d];
+  }
   for (int n = 0; n < a.steps; ++n) {
     // Q = a I + b S + c S^2
     store(s_x, s);
     __syncthreads();
 #pragma unroll
-    for (int d = 0; d < P::kOwn; ++d) {
-      const f64x4_t s2 = tile_product<kT>(s_x, s_x, ta[d], tb[d], li, lg);
+    for (int d = 0; d < kOwn; ++d) {
+      if (!have[d]) continue;
+      const f64x4_t s2 = tile_product<kN>(s_x, s_x, ta[d], tb[d], li, lg);
 #pragma unroll
       for (int v = 0; v < 4; ++v)
         q[d][v] = a.cc * s2[v] + a.cb * s[d][v] +
@@ -357,11 +356,11 @@ __global__ __launch_bounds__(64 * Steps<kT>::kWavesOf) void muon_steps_kernel(
     store(s_y, q);
     __syncthreads();
     // T Q, and S Q Q unless this was the last step
-    f64x4_t r[P::kOwn];
+    f64x4_t r[kOwn];
     if (n + 1 < a.steps) product(r);
     if (n == 0) {
 #pragma unroll
-      for (int d = 0; d < P::kOwn; ++d) x[d] = q[d];
+      for (int d = 0; d < kOwn; ++d) x[d] = q[d];
     } else {
       __syncthreads();
       store(s_x, x);
@@ -379,14 +378,39 @@ __global__ __launch_bounds__(64 * Steps<kT>::kWavesOf) void muon_steps_kernel(
   // T / (|u| + eps) in the order of the last pass's operands
   double* out = ws + mat.factor;
 #pragma unroll
-  for (int d = 0; d < P::kOwn; ++d)
+  for (int d = 0; d < kOwn; ++d)
 #pragma unroll
     for (int v = 0; v < 4; ++v) {
       const int i = 16 * ta[d] + 4 * v + lg, j = 16 * tb[d] + li;
       const double w = x[d][v] * inv;
-      out[factor_place<kT>(mat.tall, i, j)] = w;
-      out[factor_place<kT>(mat.tall, j, i)] = w;
+      if (have[d]) {
+        out[factor_place<kT>(mat.tall, i, j)] = w;
+        out[factor_place<kT>(mat.tall, j, i)] = w;
+      }
     }
+}
+
+// Waves of a workgroup: one a tile, or of 8 x 8 a third as many.
+template <int kT>
+constexpr int kStepWaves = kT == 8 ? 12 : upper_tiles(kT);
+
+template <int kT>
+__global__ __launch_bounds__(64 * kStepWaves<kT>) void muon_steps_kernel(
+    const MuonMatrix* __restrict__ mats, MuonArgs a, double* __restrict__ ws) {
+  __shared__ __attribute__((aligned(16))) double s_x[upper_tiles(kT) * kStepTile];
+  __shared__ __attribute__((aligned(16))) double s_y[upper_tiles(kT) * kStepTile];
+  __shared__ double s_diag[16 * kT];
+  const MuonMatrix mat = mats[blockIdx.x];
+  constexpr int kW = kStepWaves<kT>;
+  const int tiles = (mat.r + 15) / 16;  // more than kT / 2
+  if constexpr (kT == 8) {
+    if (tiles == 5) return tile_steps<kT, 5, kW>(mat, a, ws, s_x, s_y, s_diag);
+    if (tiles == 6) return tile_steps<kT, 6, kW>(mat, a, ws, s_x, s_y, s_diag);
+    if (tiles == 7) return tile_steps<kT, 7, kW>(mat, a, ws, s_x, s_y, s_diag);
+  }
+  if constexpr (kT == 4)
+    if (tiles == 3) return tile_steps<kT, 3, kW>(mat, a, ws, s_x, s_y, s_diag);
+  tile_steps<kT, kT, kW>(mat, a, ws, s_x, s_y, s_diag);
 }
 
 // The update of blocks of 16 kC of the long side, a wave each: u once more, times
@@ -447,6 +471,7 @@ __device__ __forceinline__ void apply_blocks(const MuonMatrix& mat, const MuonAr
     load(k0, block, 0);
 #pragma unroll
     for (int t = 0; t < kT; ++t) {
+      if (kT >= 4 && 16 * t >= r) continue;
       if (t + 1 < kT) load(k0, block, t + 1);
       float u[kX][kN];
 #pragma unroll
@@ -461,6 +486,7 @@ __device__ __forceinline__ void apply_blocks(const MuonMatrix& mat, const MuonAr
         for (int c = 0; c < kC; ++c) b[c] = static_cast<double>(kTall ? u[c][q] : u[q][c]);
 #pragma unroll
         for (int h = 0; h < kT; ++h) {
+          if (kT >= 4 && 16 * h >= r) continue;
           const double w = s_w[((h * kT + t) * 4 + q) * 64 + from];
 #pragma unroll
           for (int c = 0; c < kC; ++c) acc[h][c] = mfma64(w, b[c], acc[h][c]);
@@ -470,6 +496,7 @@ __device__ __forceinline__ void apply_blocks(const MuonMatrix& mat, const MuonAr
     }
 #pragma unroll
     for (int h = 0; h < kT; ++h) {
+      if (kT >= 4 && 16 * h >= r) continue;
       float pv[kX][kN];
 #pragma unroll
       for (int x = 0; x < kX; ++x)
@@ -595,7 +622,7 @@ hipError_t launch_class(const MuonMatrix* mats, const MuonMatrix* of, int64_t ma
   if (hipError_t e = hipGetLastError(); e != hipSuccess) return e;
   if constexpr (kT > 1) {
     hipLaunchKernelGGL(muon_steps_kernel<kT>, dim3(static_cast<uint32_t>(matrices)),
-                       dim3(64 * Steps<kT>::kWavesOf), 0, st, of, a, ws);
+                       dim3(64 * kStepWaves<kT>), 0, st, of, a, ws);
     if (hipError_t e = hipGetLastError(); e != hipSuccess) return e;
   }
   if (bf16_grad)
