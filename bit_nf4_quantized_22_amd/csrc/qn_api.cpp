@@ -457,11 +457,15 @@ int mx_linear(bool bwd, const qn_mxfp4_weight* w, const qn_bf16* in, int64_t M, 
   }
   const bool decode = !bwd && M <= qn::kFp8DecodeM, few = !bwd && qn::mx_few(M, v.N, v.K);
   const int m32 = static_cast<int>(few ? M : 0);
+  uint8_t* turned = codes + f.turned;
+  uint8_t* tscale = codes + f.tscale;
   hipError_t e = r == 0   ? qn::launch_mx_rows(in, M, L, bwd, codes, scale, s)
                  : decode ? qn::launch_mx_decode_project(in, m32, L, A, r, codes, scale, part, s)
-                          : qn::launch_mx_rows_project(in, M, L, bwd ? B : A, r, bwd, codes, scale,
-                                                       part, s);
+                 : bwd    ? qn::launch_mx_backward(v, in, M, B, r, codes, scale, part, turned,
+                                                   tscale, s)
+                          : qn::launch_mx_rows_project(in, M, L, A, r, codes, scale, part, s);
   if (e != hipSuccess) return QN_ERR_HIP;
+  if (bwd && r == 0 && qn::launch_mx_turn(v, turned, tscale, s) != hipSuccess) return QN_ERR_HIP;
   if (r > 0 && !decode &&
       qn::launch_fp8_project_sum(part, qn::fp8_project_slices(M, L), M, r, ls, act, low, s) !=
           hipSuccess)
@@ -469,16 +473,9 @@ int mx_linear(bool bwd, const qn_mxfp4_weight* w, const qn_bf16* in, int64_t M, 
   if (few)
     return hip_status(qn::launch_mx_decode(v, codes, scale, m32, part, qn::fp8_decode_slices(L),
                                            act, B, r, ls, out, low, s));
-  const uint8_t* wc = v.codes;
-  const uint8_t* wsc = v.scale;
-  if (bwd) {
-    if (qn::launch_mx_turn(v, codes + f.turned, codes + f.tscale, s) != hipSuccess)
-      return QN_ERR_HIP;
-    wc = codes + f.turned;
-    wsc = codes + f.tscale;
-  }
-  return hip_status(qn::launch_mx_gemm(wc, wsc, v.N, v.K, f.bytes, codes, scale, M, act,
-                                       bwd ? A : B, r, bwd, out, split, s));
+  return hip_status(qn::launch_mx_gemm(bwd ? turned : v.codes, bwd ? tscale : v.scale, v.N, v.K,
+                                       f.bytes, codes, scale, M, act, bwd ? A : B, r, bwd, out,
+                                       split, s));
 }
 
 bool adamw_hyper_ok(float lr, float beta1, float beta2, float eps, float weight_decay) {

@@ -210,20 +210,23 @@ hipError_t launch_mx_scales(bool pack, const uint8_t* in, int64_t R, int64_t K, 
                             hipStream_t st);
 // A batch x [M, L] in codes: forward E2M1 [M, L / 2] with tiles as a weight's,
 // backward E4M3 [M, mx_tiles(L, 128) * 128] with tiles of 64 rows x 128 columns.
-// The second form also gives fp8_project_slices(M, L) partial sums
-// part[slices][M][r] of the LoRA projection x P^T (P = A [r, L] forward, B [L, r]
-// backward; r >= 1).
+// The second form, forward, also gives fp8_project_slices(M, L) partial sums
+// part[slices][M][r] of the LoRA projection x A^T (A [r, L], r >= 1).
 hipError_t launch_mx_rows(const uint16_t* x, int64_t M, int64_t L, bool bwd, uint8_t* codes,
                           uint8_t* scale, hipStream_t st);
-hipError_t launch_mx_rows_project(const uint16_t* x, int64_t M, int64_t L, const uint16_t* P, int r,
-                                  bool bwd, uint8_t* codes, uint8_t* scale, float* part,
-                                  hipStream_t st);
+hipError_t launch_mx_rows_project(const uint16_t* x, int64_t M, int64_t L, const uint16_t* A, int r,
+                                  uint8_t* codes, uint8_t* scale, float* part, hipStream_t st);
 // The same of M <= kFp8DecodeM tokens, forward, in fp8_decode_slices(L) slices.
 hipError_t launch_mx_decode_project(const uint16_t* x, int M, int64_t L, const uint16_t* A, int r,
                                     uint8_t* codes, uint8_t* scale, float* part, hipStream_t st);
 // W^T in E5M2 codes wt [K, mx_tiles(N, 128) * 128] with tiles ts of 64 rows x
 // 128 columns, for the backward's product.
 hipError_t launch_mx_turn(const MxView& w, uint8_t* wt, uint8_t* ts, hipStream_t st);
+// launch_mx_rows of dy [M, N] with fp8_project_slices(M, N) partial sums of dy B (B
+// [N, r], r >= 1), and launch_mx_turn, in one launch.
+hipError_t launch_mx_backward(const MxView& w, const uint16_t* dy, int64_t M, const uint16_t* B,
+                              int r, uint8_t* codes, uint8_t* scale, float* part, uint8_t* wt,
+                              uint8_t* ts, hipStream_t st);
 // y [M, N] = x W^T + (lora_scale u) B^T for mx_few(..) tokens in codes, u given as
 // to launch_fp8_decode.
 bool mx_few(int64_t M, int64_t N, int64_t K);

@@ -152,7 +152,7 @@ struct Mx4Rows {
 struct Mx8Rows {
   typedef uint2 Codes;
   static constexpr int kBytes = 128;
-  static constexpr bool kForward = false, kBackward = true;
+  static constexpr bool kForward = false, kBackward = false;  // mx_backward_kernel
   uint8_t* codes;
   int64_t pitch;
   uint8_t* scale;
@@ -226,14 +226,12 @@ typedef int i32x2_t __attribute__((ext_vector_type(2)));
 typedef __attribute__((address_space(3))) i32x2_t lds_i32x2_t;
 typedef __attribute__((address_space(3))) uint8_t lds_u8_t;
 
-__global__ __launch_bounds__(kT) void mx_turn_kernel(const uint8_t* __restrict__ codes,
-                                                     const uint8_t* __restrict__ scale, int64_t N,
-                                                     int64_t K, int64_t Np,
-                                                     uint8_t* __restrict__ wt,
-                                                     uint8_t* __restrict__ ts) {
-  __shared__ __attribute__((aligned(16))) uint8_t s_w[128 * 128];
+__device__ __forceinline__ void turn_tile(const uint8_t* __restrict__ codes,
+                                          const uint8_t* __restrict__ scale, int64_t N, int64_t K,
+                                          int64_t Np, uint8_t* __restrict__ wt,
+                                          uint8_t* __restrict__ ts, int64_t tile, uint8_t* s_w) {
   const int64_t nbn = Np / 128;
-  const int64_t n0 = static_cast<int64_t>(blockIdx.x % nbn) * 128, k0 = blockIdx.x / nbn * 128;
+  const int64_t n0 = tile % nbn * 128, k0 = tile / nbn * 128;
   const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
   const int64_t rt = (N + 31) / 32, kt = (K + 63) / 64;
   // row n0 + 32 wave + lane % 32, groups lane / 32 and 2 + lane / 32 of the
@@ -314,6 +312,35 @@ __global__ __launch_bounds__(kT) void mx_turn_kernel(const uint8_t* __restrict__
   }
 }
 
+__global__ __launch_bounds__(kT) void mx_turn_kernel(const uint8_t* __restrict__ codes,
+                                                     const uint8_t* __restrict__ scale, int64_t N,
+                                                     int64_t K, int64_t Np,
+                                                     uint8_t* __restrict__ wt,
+                                                     uint8_t* __restrict__ ts) {
+  __shared__ __attribute__((aligned(16))) uint8_t s_w[128 * 128];
+  turn_tile(codes, scale, N, K, Np, wt, ts, blockIdx.x, s_w);
+}
+
+// Both in one launch: the first workgroups quantise and project the batch, which
+// waits on memory more than it reads, the others turn the weight meanwhile.
+template <int kRT>
+__global__ __launch_bounds__(kT) void mx_backward_kernel(
+    const uint16_t* __restrict__ x, int64_t M, int64_t L, const uint16_t* __restrict__ P, int r,
+    bool vec_p, int per_slice, Mx8Rows out_q, float* __restrict__ part, int slices, int projecting,
+    const uint8_t* __restrict__ codes, const uint8_t* __restrict__ scale, int64_t K,
+    uint8_t* __restrict__ wt, uint8_t* __restrict__ ts) {
+  typedef ProjectLds<Mx8Rows, kRT, 4> Lds;
+  constexpr int kBytes = sizeof(Lds) > 128 * 128 ? sizeof(Lds) : 128 * 128;
+  __shared__ __attribute__((aligned(16))) uint8_t lds[kBytes];
+  const int bid = blockIdx.x;
+  if (bid < projecting)
+    quantize_project<Mx8Rows, true, kRT, 4>(x, M, L, P, r, vec_p, per_slice, out_q, part,
+                                            bid / slices, bid % slices,
+                                            *reinterpret_cast<Lds*>(lds));
+  else
+    turn_tile(codes, scale, L, K, out_q.pitch, wt, ts, bid - projecting, lds);
+}
+
 }  // namespace
 
 hipError_t launch_mx_quantize(const void* x, bool bf16, int64_t R, int64_t K, uint8_t* codes,
@@ -374,15 +401,31 @@ hipError_t launch_mx_rows(const uint16_t* x, int64_t M, int64_t L, bool bwd, uin
   return hipGetLastError();
 }
 
-hipError_t launch_mx_rows_project(const uint16_t* x, int64_t M, int64_t L, const uint16_t* P, int r,
-                                  bool bwd, uint8_t* codes, uint8_t* scale, float* part,
-                                  hipStream_t st) {
-  const int slices = fp8_project_slices(M, L);
-  if (bwd)
-    return go_quantize_project(x, M, L, P, r, true,
-                               Mx8Rows{codes, mx_tiles(L, 128) * 128, scale, mx_tiles(M, 64)},
-                               slices, part, st);
-  return go_quantize_project(x, M, L, P, r, false, rows4(codes, scale, M, L), slices, part, st);
+hipError_t launch_mx_rows_project(const uint16_t* x, int64_t M, int64_t L, const uint16_t* A, int r,
+                                  uint8_t* codes, uint8_t* scale, float* part, hipStream_t st) {
+  return go_quantize_project(x, M, L, A, r, false, rows4(codes, scale, M, L),
+                             fp8_project_slices(M, L), part, st);
+}
+
+hipError_t launch_mx_backward(const MxView& w, const uint16_t* dy, int64_t M, const uint16_t* B,
+                              int r, uint8_t* codes, uint8_t* scale, float* part, uint8_t* wt,
+                              uint8_t* ts, hipStream_t st) {
+  if (M == 0) return hipSuccess;
+  const int slices = fp8_project_slices(M, w.N), per = project_blocks_per_slice(M, w.N);
+  const int64_t projecting = mx_tiles(M, 64) * slices;
+  const int64_t turning = mx_tiles(w.N, 128) * mx_tiles(w.K, 128);
+  const bool vec = (reinterpret_cast<uintptr_t>(B) & 15) == 0 && (r & 7) == 0;
+  auto go = [&](auto k) {
+    hipLaunchKernelGGL(k, dim3(static_cast<uint32_t>(projecting + turning)), dim3(kT), 0, st, dy, M,
+                       w.N, B, r, vec, per,
+                       Mx8Rows{codes, mx_tiles(w.N, 128) * 128, scale, mx_tiles(M, 64)}, part,
+                       slices, static_cast<int>(projecting), w.codes, w.scale, w.K, wt, ts);
+    return hipGetLastError();
+  };
+  return r <= 16   ? go(mx_backward_kernel<1>)
+         : r <= 32 ? go(mx_backward_kernel<2>)
+         : r <= 64 ? go(mx_backward_kernel<4>)
+                   : go(mx_backward_kernel<8>);
 }
 
 hipError_t launch_mx_decode_project(const uint16_t* x, int M, int64_t L, const uint16_t* A, int r,

@@ -80,21 +80,28 @@ __device__ __forceinline__ int p_place(int row, int chunk) {
   return row * (16 * kRT) + (((chunk >> 1) ^ sw) << 4) + (chunk & 1) * 8;
 }
 
+// LDS of a workgroup: two tiles of P, and each wave's codes of a block.
+template <typename Q, int kRT, int kWaves>
+struct ProjectLds {
+  __attribute__((aligned(16))) uint16_t p[2][kRT * 16 * 128];
+  __attribute__((aligned(16))) uint8_t q[kWaves][16 * (Q::kBytes + 16)];
+};
+
 template <typename Q, bool kRowsL, int kRT, int kWaves>
-__global__ __launch_bounds__(64 * kWaves) void quantize_project_kernel(
-    const uint16_t* __restrict__ x, int64_t M, int64_t L, const uint16_t* __restrict__ P, int r,
-    bool vec_p, int per_slice, Q out_q, float* __restrict__ part) {
+__device__ __forceinline__ void quantize_project(const uint16_t* __restrict__ x, int64_t M,
+                                                 int64_t L, const uint16_t* __restrict__ P, int r,
+                                                 bool vec_p, int per_slice, const Q& out_q,
+                                                 float* __restrict__ part, int group, int slice,
+                                                 ProjectLds<Q, kRT, kWaves>& lds) {
   constexpr int kThreads = 64 * kWaves;
   constexpr int kLoads = kRT * 256 / kThreads;  // 16-byte chunks of P per thread and block
   static_assert(kLoads * kThreads == kRT * 256, "P tile split");
   constexpr int kQPitch = Q::kBytes + 16, kQChunks = Q::kBytes / 16;
-  __shared__ __attribute__((aligned(16))) uint16_t sP[2][kRT * 16 * 128];
-  __shared__ __attribute__((aligned(16))) uint8_t sQ[kWaves][16 * kQPitch];
   const int t = threadIdx.x, lane = t & 63, li = lane & 15, lg = lane >> 4;
-  const int64_t row = (static_cast<int64_t>(blockIdx.x) * kWaves + (t >> 6)) * 16 + li;
+  const int64_t row = (static_cast<int64_t>(group) * kWaves + (t >> 6)) * 16 + li;
   const int64_t m = row < M ? row : M - 1;
   const int64_t blocks = (L + 127) / 128;
-  const int64_t b0 = static_cast<int64_t>(blockIdx.y) * per_slice;
+  const int64_t b0 = static_cast<int64_t>(slice) * per_slice;
   const int64_t b1 = b0 + per_slice < blocks ? b0 + per_slice : blocks;
   uint4 w[4], p[kLoads];
   auto load_x = [&](int64_t b) {
@@ -125,7 +132,7 @@ __global__ __launch_bounds__(64 * kWaves) void quantize_project_kernel(
   load_x(b0);
   load_p(b0);
   for (int64_t b = b0; b < b1; ++b) {
-    uint16_t* sp = sP[(b - b0) & 1];
+    uint16_t* sp = lds.p[(b - b0) & 1];
     uint4 cur[4];
 #pragma unroll
     for (int c = 0; c < 4; ++c) cur[c] = w[c];
@@ -144,9 +151,9 @@ __global__ __launch_bounds__(64 * kWaves) void quantize_project_kernel(
     const typename Q::Block q = Q::quantize(cur);
     if (row < M) out_q.store_scale(q, b, row, lg);
     // the codes leave as whole rows of the block, 8 or 16 of them per store (8
-    // bytes of 16 rows per store took 40% longer for the whole kernel); sQ is
+    // bytes of 16 rows per store took 40% longer for the whole kernel); sq is
     // the wave's own, so the order of its LDS accesses keeps the turns apart
-    uint8_t* sq = sQ[t >> 6];
+    uint8_t* sq = lds.q[t >> 6];
     __builtin_amdgcn_wave_barrier();
 #pragma unroll
     for (int c = 0; c < 4; ++c)
@@ -186,7 +193,7 @@ __global__ __launch_bounds__(64 * kWaves) void quantize_project_kernel(
   }
   if (row >= M) return;
   // lane (li, lg): ranks 16 i + 4 lg .. + 3 of token li
-  float* out = part + (static_cast<int64_t>(blockIdx.y) * M + row) * r;
+  float* out = part + (static_cast<int64_t>(slice) * M + row) * r;
 #pragma unroll
   for (int i = 0; i < kRT; ++i) {
     const int j = 16 * i + 4 * lg;
@@ -198,6 +205,15 @@ __global__ __launch_bounds__(64 * kWaves) void quantize_project_kernel(
         if (j + e < r) out[j + e] = acc[i][e];
     }
   }
+}
+
+template <typename Q, bool kRowsL, int kRT, int kWaves>
+__global__ __launch_bounds__(64 * kWaves) void quantize_project_kernel(
+    const uint16_t* __restrict__ x, int64_t M, int64_t L, const uint16_t* __restrict__ P, int r,
+    bool vec_p, int per_slice, Q out_q, float* __restrict__ part) {
+  __shared__ ProjectLds<Q, kRT, kWaves> lds;
+  quantize_project<Q, kRowsL, kRT, kWaves>(x, M, L, P, r, vec_p, per_slice, out_q, part, blockIdx.x,
+                                           blockIdx.y, lds);
 }
 
 // The same for the decode path (up to 16 tokens, P = A): a wave takes one
@@ -279,13 +295,14 @@ hipError_t go_quantize_project(const uint16_t* x, int64_t M, int64_t L, const ui
     hipLaunchKernelGGL(k, grid, dim3(64 * waves), 0, st, x, M, L, P, r, vec_p, per, q, part);
     return hipGetLastError();
   };
-  if (!rows_l) {
-    if constexpr (Q::kForward)
+  if constexpr (Q::kForward) {
+    if (!rows_l)
       return r <= 16   ? go(quantize_project_kernel<Q, false, 1, 4>)
              : r <= 32 ? go(quantize_project_kernel<Q, false, 2, 4>)
              : r <= 64 ? go(quantize_project_kernel<Q, false, 4, 4>)
                        : go(quantize_project_kernel<Q, false, 8, 4>);
-  } else if constexpr (Q::kBackward) {
+  }
+  if constexpr (Q::kBackward) {
     if (waves == 1)
       return r <= 16   ? go(quantize_project_kernel<Q, true, 1, 1>)
              : r <= 32 ? go(quantize_project_kernel<Q, true, 2, 1>)
