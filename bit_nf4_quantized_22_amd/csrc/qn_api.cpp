@@ -406,7 +406,7 @@ MxWs mx_ws(bool bwd, int64_t M, int64_t N, int64_t K, int32_t r) {
   if (r > 0 && (bwd || M > qn::kFp8DecodeM))
     f.split += round_up(m * static_cast<size_t>(qn::fp8_lora_pitch(r)) * 2, 256);
   f.total = f.split;
-  const int splits = bwd || !qn::mx_few(M, N, K) ? qn::mx_gemm_splits(M, cols, f.bytes) : 1;
+  const int splits = bwd || !qn::mx_few(M, N, K) ? qn::mx_gemm_splits(M, cols, f.bytes, bwd) : 1;
   if (splits > 1)
     f.total += m * static_cast<size_t>(cols) * 4 * static_cast<size_t>(splits);
   return f;

@@ -243,9 +243,9 @@ hipError_t launch_mx_token(const MxView& w, const uint16_t* x, const uint16_t* A
 // out [M, N] = x w^T + act B^T (w, x E2M1 codes, bytes = K / 2), or with bwd
 // out [M, K] = x w^T + act A (w the turned weight, x E4M3 codes, bytes a multiple
 // of 128); act as launch_fp8_project_sum gives it (r == 0: no LoRA term).  The
-// contraction is split over mx_gemm_splits(M, ncols, bytes) workgroups where the
+// contraction is split over mx_gemm_splits(M, ncols, bytes, bwd) workgroups where the
 // tiles are few and part, fp32 [splits][M][ncols], is given.
-int mx_gemm_splits(int64_t M, int64_t ncols, int64_t bytes);
+int mx_gemm_splits(int64_t M, int64_t ncols, int64_t bytes, bool bwd);
 hipError_t launch_mx_gemm(const uint8_t* w, const uint8_t* ws, int64_t N, int64_t K, int64_t bytes,
                           const uint8_t* x, const uint8_t* xs, int64_t M, const uint16_t* act,
                           const uint16_t* lw, int r, bool bwd, uint16_t* out, float* part,

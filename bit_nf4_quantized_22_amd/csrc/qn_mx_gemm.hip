@@ -339,21 +339,28 @@ int64_t small_tiles(int64_t M, int64_t ncols) {
 }
 
 // Large tiles where the small ones would take more than one round of the CUs.
+// Small and large, calls on 4096 x 4096: 1024 tokens (256 small tiles) 26.6 and 32.4
+// us, backward 40 and 45; 1152 tokens 37.5 and 32.4; 2048 38.5 and 35.8, backward 55
+// and 49; 11008 x 4096, 256 tokens 24 and 32, 512 39 and 33.
 bool large(int64_t M, int64_t ncols) { return small_tiles(M, ncols) > 256; }
 
 }  // namespace
 
-int mx_gemm_splits(int64_t M, int64_t ncols, int64_t bytes) {
+int mx_gemm_splits(int64_t M, int64_t ncols, int64_t bytes, bool bwd) {
   if (M <= 0 || large(M, ncols)) return 1;
-  // up to one workgroup per CU; the parts cost a launch and their way out and
-  // back
+  // Up to one workgroup per CU.  A step costs 0.45 us forward and 0.55 us backward,
+  // the launch that adds the parts 3.5, a part 4 bytes an output at 5.5 TB/s out and
+  // back, half of it hidden: fitted to calls such as 4096 x 11008, 128 tokens in 1, 2, 4
+  // and 8 parts (44.5, 36, 30, 29 us), 4096 x 4096, 256 tokens in 1, 2, 4 (21.9, 25.6,
+  // 28.9) and backward (38, 34, 29).
   const int64_t steps = mx_tiles(bytes, 128), most = 256 / small_tiles(M, ncols);
-  const double out = static_cast<double>(M) * static_cast<double>(ncols) * 8 / 5.5e6;
-  double best = 0.42 * static_cast<double>(steps);
+  const double out = static_cast<double>(M) * static_cast<double>(ncols) * 4 / 5.5e6;
+  const double step = bwd ? 0.55 : 0.45;
+  double best = step * static_cast<double>(steps);
   int splits = 1;
   for (int64_t s = 2; s <= most && s <= steps; ++s) {
     const int64_t per = (steps + s - 1) / s, n = (steps + per - 1) / per;
-    const double t = 0.42 * static_cast<double>(per) + 2.4 + (out + 0.1) * static_cast<double>(n);
+    const double t = step * static_cast<double>(per) + 3.5 + (out + 0.1) * static_cast<double>(n);
     if (t < best) best = t, splits = static_cast<int>(n);
   }
   return splits;
@@ -381,7 +388,7 @@ hipError_t launch_mx_gemm(const uint8_t* w, const uint8_t* ws, int64_t N, int64_
       hipLaunchKernelGGL(mx_gemm_kernel<false>, grid, dim3(512), 0, st, g, static_cast<int>(nbig));
     return hipGetLastError();
   }
-  const int splits = part ? mx_gemm_splits(M, ncols, bytes) : 1;
+  const int splits = part ? mx_gemm_splits(M, ncols, bytes, bwd) : 1;
   const int per = static_cast<int>((mx_tiles(bytes, 128) + splits - 1) / splits);
   if (splits > 1) g.part = part;
   const dim3 grid(static_cast<uint32_t>(small_tiles(M, ncols)), static_cast<uint32_t>(splits));

@@ -15,6 +15,14 @@
 // One token: the same launch quantises x, each wave for its own runs, and,
 // where the adapter is small, computes u = x A^T.  More tokens: x's codes and
 // u's partial sums come from a launch before.
+//
+// Times of calls in a graph, the weight not in the caches, r = 16: one token on
+// 4096 x 4096 8.3 us (without an adapter 4.6, the bytes at a large copy's rate
+// 1.8), on 22016 x 8192 25.6 (22.1, 18.9); 16 tokens on 4096 x 4096 10.8, on 4096 x
+// 11008 15.4 (4.9), on 22016 x 8192 38.0.  Small calls are a chain of latencies:
+// launch, load, sum over the waves, LoRA term; with many tokens it is x's codes,
+// which every workgroup reads from the L2 caches.  16 waves a workgroup: one token
+// the same within 10%, 16 tokens 10.8 -> 13.6 us and 15.4 -> 18.2.
 
 #include "qn_decode.h"
 #include "qn_launch.h"
@@ -59,7 +67,11 @@ __global__ __launch_bounds__(64 * kWaves) void mx_token_kernel(
   __shared__ __attribute__((aligned(16))) uint2 s_x[kU == kOwnU ? kWaves : 1][kAhead][64];
   __shared__ __attribute__((aligned(16))) uint16_t s_q[kWaves][kAhead][64];  // 4 codes a lane
   const int t = threadIdx.x, lane = t & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
+  // the wave's part is turned by the workgroup, so that the CUs of an XCD do not
+  // ask its L2 for the same lines of A at the same time (4096 x 4096, r = 8 7.3 -> 7.0
+  // us)
+  const int wave = __builtin_amdgcn_readfirstlane(((t >> 6) + (blockIdx.x >> 3)) & (kWaves - 1));
+  static_assert((kWaves & (kWaves - 1)) == 0, "the turn is a bijection");
   const int li = lane & 15, lg = lane >> 4;
   const int64_t n0 = static_cast<int64_t>(blockIdx.x) * 16;  // N is a multiple of 16
   const int64_t groups = K / 32, runs = (K + 255) / 256, rt = (N + 31) / 32;
@@ -279,16 +291,23 @@ __global__ __launch_bounds__(64 * kWaves) void mx_decode_kernel(
 
 }  // namespace
 
+// Past 16 tokens x's codes, which every workgroup reads, are what counts; past 64
+// MiB of them in all the tiles of the large batches cost less.  17 to 32 tokens, this
+// kernel and the tiles: 4096 x 4096 13.6 and 18.1 us, 4096 x 11008 22.8 and 24.5, 8192
+// x 8192 22.3 and 23.8, but 22016 x 8192 44 and 36; 33 to 64: 4096 x 4096 15.8 and
+// 20.2, but 4096 x 11008 28.8 and 27.0, 8192 x 8192 35.6 and 25.6.
 bool mx_few(int64_t M, int64_t N, int64_t K) {
-  // x's codes go to every workgroup; see fp8_few, with half the bytes
   const int64_t cols = N > 4096 ? N : 4096;
   return M <= kFp8DecodeM ||
-         (M <= kFp8FewM && (M + 15) / 16 * cols * K / 2 < (int64_t{64} << 20));
+         (M <= kFp8FewM && (M + 15) / 16 * cols * K / 2 <= (int64_t{64} << 20));
 }
 
+// Every workgroup reads A, from the caches: past 32 MiB in all, or 128 KB each, a
+// projection launch of its own costs less.  In this launch and in two: r = 8 on 1024
+// x 4096 6.4 and 7.0 us, on 4096 x 4096 7.0 and 8.1; r = 16 on 1088 x 2112 5.2 and 6.5,
+// on 4096 x 4096 8.3 and 8.1 (the host has one launch less); but r = 8 on 11008 x 4096 17 and 10.8, on 4096 x 11008 13
+// and 11.8.
 bool mx_token_self_u(const MxView& w, int r) {
-  // A is read by every workgroup, from the caches: past 32 MiB in all, or 128
-  // KB each, a projection launch of its own costs less
   const int64_t a = int64_t{2} * r * w.K;
   return r <= 16 && a <= (int64_t{128} << 10) && w.N / 16 * a <= (int64_t{32} << 20);
 }
@@ -323,8 +342,10 @@ hipError_t launch_mx_decode(const MxView& w, const uint8_t* x, const uint8_t* xs
                        fp8_lora_pitch(r), B, r, vec_b, lora_scale, y, u_out);
     return hipGetLastError();
   };
-  const int64_t pairs = (w.N + 31) / 32;
-  const bool two = pairs > 128 && pairs <= 256 && w.K > 2048;
+  // two rows of columns a workgroup halve the reads of x, where half the workgroups
+  // still keep the chip busy; 16 tokens, one row and two: 4096 x 4096 10.8 and 11.8 us,
+  // 6144 x 4096 15.2 and 12.1, 8192 x 2048 13.6 and 10.8, 22016 x 8192 46 and 38
+  const bool two = (w.N + 31) / 32 > 128;
   if (M <= 16)
     return two ? go(mx_decode_kernel<8, 1, 2>, 8, 2) : go(mx_decode_kernel<8, 1, 1>, 8, 1);
   if (M <= 32)
