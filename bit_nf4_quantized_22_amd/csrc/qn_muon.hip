@@ -22,10 +22,13 @@
 // Bound by HBM: 8 bytes an element in the first pass, 22 in the last.  448
 // matrices of 16 x 4096 (29 M elements): 59 us (4.0 TB/s) and 115 us (5.6 TB/s,
 // part of it from the last-level cache), the steps among them; of 64 x 4096 (117
-// M): 288 us (3.3 TB/s), the steps 80 us, 545-630 us (4.1-4.7 TB/s).  All adapters
-// of a 7B model, r = 64: 1.31 ms, 0.95 at a large copy's rate.  Up to r = 64 the
-// matrix instructions would take a third of these times; at r = 128 (52 M) they
-// are half of them: 250, 230 and 420 us.
+// M): 299 us (3.1 TB/s), the steps 86 us, 542 us (4.8 TB/s).  All adapters of a 7B
+// model: r = 16 256 us, r = 64 1.30 ms, 0.95 at a large copy's rate.  Up to r = 64 the
+// matrix instructions would take a third of these times; at r = 128 (100 matrices
+// of 128 x 4096, 52 M) they are half of them: 288, 236 and 429 us.  The steps of a
+// matrix are one CU's work, and above 32 rows its 64-bit rate bounds them (15
+// matrices: 64 rows 34 us, 74 rows 62, 128 rows 214, for 17 products each).
+// Few matrices are a chain of latencies: one layer's 14 of r = 16 19 us.
 
 #include <cmath>
 
@@ -145,9 +148,10 @@ __device__ __forceinline__ void momentum(const MuonArgs& a, const float (&g)[n],
 // u u^T of a chunk of the long side, its batches dealt to the waves in turn (so
 // that they read the same lines at about the same time: 430 -> 300 us for 448
 // matrices of 64 x 4096).  The products' operands are loaded as they are needed,
-// without LDS, a batch ahead: lane (li, lg) holds row 16 t + li of the short side; a wide matrix gives
-// it 4 consecutive elements of the long side (4 steps, group lg's elements at
-// 4 lg: any order that both operands share will do), a tall one a single one.
+// without LDS, a batch ahead: lane (li, lg) holds row 16 t + li of the short side;
+// a wide matrix gives it 4 consecutive elements of the long side (4 steps, group
+// lg's elements at 4 lg: any order that both operands share will do), a tall one a
+// single one.
 template <int kT, bool kTall, bool kVec, typename G>
 __device__ __forceinline__ void gram_blocks(const MuonMatrix& mat, const MuonArgs& a, int start,
                                             int end, int wave, f64x4_t (&acc)[upper_tiles(kT)]) {
@@ -572,10 +576,9 @@ template <int kT>
 constexpr int kApplyWaves = kT == 8 ? 8 : kWaves;
 
 template <int kT, typename G>
-__global__ __launch_bounds__(64 * kApplyWaves<kT>, kT <= 2 ? 4 : kT == 4 ? 3 : 2) void muon_apply_kernel(const MuonMatrix* __restrict__ mats,
-                                                              const MuonChunk* __restrict__ chunks,
-                                                              MuonArgs a,
-                                                              const double* __restrict__ ws) {
+__global__ __launch_bounds__(64 * kApplyWaves<kT>, kT <= 2 ? 4 : kT == 4 ? 3 : 2) void
+muon_apply_kernel(const MuonMatrix* __restrict__ mats, const MuonChunk* __restrict__ chunks,
+                  MuonArgs a, const double* __restrict__ ws) {
   __shared__ __attribute__((aligned(16))) double s_w[256 * kT * kT];
   const MuonChunk c = chunks[blockIdx.x];
   const MuonMatrix mat = mats[c.matrix];
@@ -608,8 +611,8 @@ __global__ __launch_bounds__(64 * kApplyWaves<kT>, kT <= 2 ? 4 : kT == 4 ? 3 : 2
 
 template <int kT>
 hipError_t launch_class(const MuonMatrix* mats, const MuonMatrix* of, int64_t matrices,
-                        const MuonChunk* chunks, int64_t nchunks, int64_t nspans, bool bf16_grad, const MuonArgs& a, double* ws,
-                        hipStream_t st) {
+                        const MuonChunk* chunks, int64_t nchunks, int64_t nspans, bool bf16_grad,
+                        const MuonArgs& a, double* ws, hipStream_t st) {
   if (matrices == 0) return hipSuccess;
   const dim3 grid(static_cast<uint32_t>(nchunks)), grid2(static_cast<uint32_t>(nspans));
   const MuonChunk* spans = chunks + nchunks;

@@ -18,6 +18,15 @@
 // 8-bit one.  The chunks of a row are XOR-swizzled by the choice of each lane's
 // source address.  A last step that the rows fill only in part reads its last
 // chunk again: the scales there are 2^-127 on both sides.
+//
+// Launches: forward 2048 x 11008 x 4096 59-64 us (2.9-3.1 PFLOP/s), 4096 x 22016 x
+// 8192 384-400 us (3.7-3.85; the vendor's 4-bit product of 8192^3 3.15), 2048 x 4096 x
+// 11008 56 us (3.3); backward 2048 x 11008 x 4096 83-89 us (2.0-2.2; the vendor's
+// 8-bit product of 8192^3 2.68), 4096 x 22016 x 8192 577 us (2.56).  A large tile's
+// step is LDS reads (192 KB a CU, 0.64 us at 128 bytes a clock), DMA and MFMA (0.43 us
+// of 4-bit products, 0.86 of 8-bit ones) of nearly equal length, and its LDS holds
+// one workgroup; a half tile reads LDS a third more often per product.  The first
+// MXFP4 step read the chunks of a row behind a uniform branch: it spilled, 1513 us.
 
 #include "qn_launch.h"
 #include "qn_mx.h"

@@ -305,8 +305,8 @@ bool mx_few(int64_t M, int64_t N, int64_t K) {
 // Every workgroup reads A, from the caches: past 32 MiB in all, or 128 KB each, a
 // projection launch of its own costs less.  In this launch and in two: r = 8 on 1024
 // x 4096 6.4 and 7.0 us, on 4096 x 4096 7.0 and 8.1; r = 16 on 1088 x 2112 5.2 and 6.5,
-// on 4096 x 4096 8.3 and 8.1 (the host has one launch less); but r = 8 on 11008 x 4096 17 and 10.8, on 4096 x 11008 13
-// and 11.8.
+// on 4096 x 4096 8.3 and 8.1 (the host has one launch less); but r = 8 on 11008 x 4096
+// 17 and 10.8, on 4096 x 11008 13 and 11.8.
 bool mx_token_self_u(const MxView& w, int r) {
   const int64_t a = int64_t{2} * r * w.K;
   return r <= 16 && a <= (int64_t{128} << 10) && w.N / 16 * a <= (int64_t{32} << 20);

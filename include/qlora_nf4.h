@@ -851,7 +851,8 @@ QN_API int lora_muon_table(const qn_muon_tensor* t, int32_t count, int32_t grad_
  *   ws  device workspace, 16-byte aligned, of at least
  *       lora_muon_workspace_bytes(plan); not shared by calls that may run at
  *       the same time.
- * One launch per pass and class of smaller sides that occurs (three passes).
+ * Three launches per class of smaller sides that occurs (up to 16, 32, 64, 128),
+ * two for up to 16.
  */
 QN_API size_t lora_muon_workspace_bytes(const qn_muon_plan* plan);
 QN_API int lora_muon_multi_step(const qn_muon_plan* plan, const void* table,
