@@ -64,24 +64,8 @@ __global__ __launch_bounds__(64 * kWaves) void fp8_token_kernel(
   const float* wsr = ws + (n0 / 128) * kb;
 
   uint4 bf[kFrags];
-  if (kU != kNoAdapter && wave == 0) {
-#pragma unroll
-    for (int q = 0; q < kFrags; ++q) {
-      bf[q] = make_uint4(0, 0, 0, 0);
-      if (32 * q < r)
-        bf[q] = load_bf16x8(B + (n0 + li) * r + 32 * q + 8 * lg, r - 32 * q - 8 * lg, vec_b);
-    }
-  }
-  if constexpr (kU == kGivenU) {
-    // thread (q0, j) adds the slices q0, q0 + par, ... of rank j
-    const int par = kThreads / r, j = t % r, q0 = t / r;
-    float s = 0.0f;
-    if (q0 < par) {
-#pragma unroll 4
-      for (int q = q0; q < slices; q += par) s += part[static_cast<int64_t>(q) * r + j];
-    }
-    s_u[t] = s;
-  }
+  if (kU != kNoAdapter && wave == 0) load_up<kFrags>(bf, B, n0, r, li, lg, vec_b);
+  if constexpr (kU == kGivenU) s_u[t] = add_slices<kThreads>(part, slices, r, t);
   f32x4_t acc = f32x4_t{0.f, 0.f, 0.f, 0.f}, ua = acc;
   for (int64_t bw = wave; bw < kb; bw += kAhead * kWaves) {
     // everything that these blocks need is asked for first
@@ -148,18 +132,8 @@ __global__ __launch_bounds__(64 * kWaves) void fp8_token_kernel(
     const int sums = kU == kOwnU          ? kWaves
                      : kThreads / r < slices ? kThreads / r
                                              : slices;
-    for (int j = lane; j < 32 * kFrags && j < ((r + 31) & ~31); j += 64) {
-      float s = 0.0f;
-      if (j < r) {
-#pragma unroll 8
-        for (int q = 0; q < sums; ++q) s += s_u[q * pitch + j];
-      }
-      if (u_out && blockIdx.x == 0 && j < r)
-        u_out[j] = static_cast<uint16_t>(pack_bf16x2(s, 0.f) & 0xFFFF);
-      store_us(s_us, j, s * lora_scale);
-    }
-    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-    acc = lora_up(acc, bf, s_us, 0, r, li, lg);
+    acc = token_up<kFrags>(acc, bf, s_u, pitch, sums, s_us, r, lora_scale,
+                           blockIdx.x == 0 ? u_out : nullptr, lane);
   }
   if (li == 0) store_columns(y + n0 + 4 * lg, acc);
 }
@@ -237,14 +211,7 @@ __global__ __launch_bounds__(64 * kWaves) void fp8_decode_kernel(
   const int64_t nw = n0 + 16 * (wave / kMT);
   const bool finish = wave < kTiles && nw < N;
   uint4 bf[kDecodeMaxRank / 32];
-  if (finish) {
-#pragma unroll
-    for (int q = 0; q < kDecodeMaxRank / 32; ++q) {
-      bf[q] = make_uint4(0, 0, 0, 0);
-      if (32 * q < r)
-        bf[q] = load_bf16x8(B + (nw + li) * r + 32 * q + 8 * lg, r - 32 * q - 8 * lg, vec_b);
-    }
-  }
+  if (finish) load_up<kDecodeMaxRank / 32>(bf, B, nw, r, li, lg, vec_b);
   if (kMT == 1 && r > 0) {
     const int q0 = t / mr;
     float s = 0.0f;
@@ -286,17 +253,8 @@ __global__ __launch_bounds__(64 * kWaves) void fp8_decode_kernel(
         s_u[i] = s;
       }
       __syncthreads();
-      const int rp = (r + 31) & ~31;
-      for (int i = t; i < 16 * rp; i += kThreads) {
-        const int row = i / rp, j = i % rp;
-        float s = 0.0f;
-        if (row < M && j < r) {
-          for (int q = 0; q < par && q < slices; ++q) s += s_u[q * mr + row * r + j];
-          if (u_out && blockIdx.x == 0)
-            u_out[row * r + j] = static_cast<uint16_t>(pack_bf16x2(s, 0.f) & 0xFFFF);
-        }
-        store_us(s_us + row * 2 * rp, j, s * lora_scale);
-      }
+      spread_u<kThreads>(s_u, par, slices, mr, M, r, lora_scale, s_us,
+                         blockIdx.x == 0 ? u_out : nullptr, t);
     }
   }
   __syncthreads();

@@ -19,7 +19,7 @@
 // Times of calls in a graph, the weight not in the caches, r = 16: one token on
 // 4096 x 4096 8.3 us (without an adapter 4.6, the bytes at a large copy's rate
 // 1.8), on 22016 x 8192 25.6 (22.1, 18.9); 16 tokens on 4096 x 4096 10.8, on 4096 x
-// 11008 15.4 (4.9), on 22016 x 8192 38.0.  Small calls are a chain of latencies:
+// 11008 15.4 (4.9), on 22016 x 8192 32.8.  Small calls are a chain of latencies:
 // launch, load, sum over the waves, LoRA term; with many tokens it is x's codes,
 // which every workgroup reads from the L2 caches.  16 waves a workgroup: one token
 // the same within 10%, 16 tokens 10.8 -> 13.6 us and 15.4 -> 18.2.
@@ -342,14 +342,21 @@ hipError_t launch_mx_decode(const MxView& w, const uint8_t* x, const uint8_t* xs
                        fp8_lora_pitch(r), B, r, vec_b, lora_scale, y, u_out);
     return hipGetLastError();
   };
-  // two rows of columns a workgroup halve the reads of x, where half the workgroups
+  // Two rows of columns a workgroup halve the reads of x, where half the workgroups
   // still keep the chip busy; 16 tokens, one row and two: 4096 x 4096 10.8 and 11.8 us,
-  // 6144 x 4096 15.2 and 12.1, 8192 x 2048 13.6 and 10.8, 22016 x 8192 46 and 38
-  const bool two = (w.N + 31) / 32 > 128;
+  // 6144 x 4096 15.2 and 12.1, 8192 x 2048 13.6 and 10.8, 22016 x 8192 46 and 38.
+  // Where these are more than the CUs, 4 waves each let more of them reside than 8:
+  // 8 waves and 4, 11008 x 4096 18.3 and 15.7 us, 22016 x 8192 38 and 33, 28672 x 1024
+  // 21.7 and 15.6, 32 tokens on 11008 x 4096 20.9 and 19.3; but 8192 x 8192 17.2 and 17.9.
+  const int64_t pairs = (w.N + 31) / 32;
   if (M <= 16)
-    return two ? go(mx_decode_kernel<8, 1, 2>, 8, 2) : go(mx_decode_kernel<8, 1, 1>, 8, 1);
+    return pairs > 256   ? go(mx_decode_kernel<4, 1, 2>, 4, 2)
+           : pairs > 128 ? go(mx_decode_kernel<8, 1, 2>, 8, 2)
+                         : go(mx_decode_kernel<8, 1, 1>, 8, 1);
   if (M <= 32)
-    return two ? go(mx_decode_kernel<8, 2, 2>, 8, 2) : go(mx_decode_kernel<8, 2, 1>, 8, 1);
+    return pairs > 256   ? go(mx_decode_kernel<4, 2, 2>, 4, 2)
+           : pairs > 128 ? go(mx_decode_kernel<8, 2, 2>, 8, 2)
+                         : go(mx_decode_kernel<8, 2, 1>, 8, 1);
   return go(mx_decode_kernel<8, 4, 1>, 8, 1);
 }
 

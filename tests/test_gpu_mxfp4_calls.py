@@ -397,7 +397,11 @@ def test_batches_at_the_border_between_few_and_tiles(M, N, K):
                                      (32, 5008, 2112, 128), (17, 8192, 2080, 0),
                                      (1, 4112, 4128, 16), (1, 8192, 1056, 128),
                                      (1, 4112, 544, 17), (1, 4096, 1056, 33), (1, 144, 4096, 16),
-                                     (1, 144, 4128, 16), (1, 144, 8192, 8), (1, 5008, 416, 0)])
+                                     (1, 144, 4128, 16), (1, 144, 8192, 8), (1, 5008, 416, 0),
+                                     # more pairs of row tiles than CUs
+                                     (16, 8208, 2080, 64), (2, 8224, 416, 0), (9, 11008, 544, 128),
+                                     (3, 8208, 1312, 7), (32, 8208, 2080, 24), (17, 11008, 32, 0),
+                                     (31, 8224, 288, 128)])
 def test_few_tokens_with_many_columns(M, N, K, r):
     w = weights(N, K, M)
     xb = acts(M, K, 3)
@@ -423,6 +427,18 @@ def test_few_tokens_with_many_columns(M, N, K, r):
         assert rel_to_bound(to_np(u), xf @ Af.T, bu + 1e-30) <= 1
     bound = layer_bound(ref, xv, wc.T, xf, Af, Bf, s, K, False)
     assert rel_to_bound(got[:, c], ref, bound) <= 1
+
+
+def test_a_row_does_not_depend_on_its_batch_with_many_columns():
+    """As above for 16 tokens and fewer, where a workgroup has two row tiles and 4
+    waves."""
+    N, K, r = 8208, 1312, 24
+    mw = qn.mxfp4_quantize_weight(torch.from_numpy(weights(N, K, 2)).to(DEV))
+    A, B = adapters(N, K, r, 2)
+    x = bf16_dev(acts(16, K, 2))
+    y = qn.mxfp4_linear_fwd(mw, x, A, B, r, 16.0)
+    for M in (2, 7, 15):
+        assert torch.equal(qn.mxfp4_linear_fwd(mw, x[:M].contiguous(), A, B, r, 16.0), y[:M])
 
 
 def test_long_contraction_of_a_few_tokens():
