@@ -18,8 +18,8 @@
 //
 // Times of calls in a graph, the weight not in the caches, r = 16: one token on
 // 4096 x 4096 8.3 us (without an adapter 4.6, the bytes at a large copy's rate
-// 1.8), on 22016 x 8192 25.6 (22.1, 18.9); 16 tokens on 4096 x 4096 10.8, on 4096 x
-// 11008 15.4 (4.9), on 22016 x 8192 32.8.  Small calls are a chain of latencies:
+// 1.8), on 22016 x 8192 25.6 (22.1, 18.9); 16 tokens on 4096 x 4096 10.6, on 4096 x
+// 11008 15.3 (4.9), on 22016 x 8192 31.1.  Small calls are a chain of latencies:
 // launch, load, sum over the waves, LoRA term; with many tokens it is x's codes,
 // which every workgroup reads from the L2 caches.  16 waves a workgroup: one token
 // the same within 10%, 16 tokens 10.8 -> 13.6 us and 15.4 -> 18.2.
@@ -166,7 +166,10 @@ __global__ __launch_bounds__(64 * kWaves) void mx_decode_kernel(
     const uint16_t* __restrict__ B, int r, bool vec_b, float lora_scale, uint16_t* __restrict__ y,
     uint16_t* __restrict__ u_out) {
   constexpr int kThreads = 64 * kWaves;
-  constexpr int kAhead = kMT <= 2 ? 2 : 1;  // runs in flight besides the one multiplied
+  // runs in flight besides the one multiplied; with two more registers hold a
+  // workgroup less (2 tokens on 22016 x 8192 27.8 -> 31.6 us, 16 on 11008 x 4096 14.7 ->
+  // 15.7)
+  constexpr int kAhead = 1;
   constexpr int kTiles = kMT * kRows, kXS = (kMT + 1) / 2;
   static_assert(kTiles <= kWaves, "a wave finishes 16 columns of 16 tokens");
   __shared__ f32x4_t s_acc[kWaves][kTiles][64];
