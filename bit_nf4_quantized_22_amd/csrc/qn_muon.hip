@@ -25,7 +25,7 @@
 // M): 299 us (3.1 TB/s), the steps 86 us, 542 us (4.8 TB/s).  All adapters of a 7B
 // model: r = 16 256 us, r = 64 1.30 ms, 0.95 at a large copy's rate.  Up to r = 64 the
 // matrix instructions would take a third of these times; at r = 128 (100 matrices
-// of 128 x 4096, 52 M) they are half of them: 288, 236 and 429 us.  The steps of a
+// of 128 x 4096, 52 M) they are half of them: 290, 224 and 426 us.  The steps of a
 // matrix are one CU's work, and above 32 rows its 64-bit rate bounds them (15
 // matrices: 64 rows 34 us, 74 rows 62, 128 rows 214, for 17 products each).
 // Few matrices are a chain of latencies: one layer's 14 of r = 16 19 us.
@@ -49,15 +49,14 @@ __device__ __forceinline__ f64x4_t mfma64(double a, double b, f64x4_t c) {
 
 constexpr int upper_tiles(int t) { return t * (t + 1) / 2; }
 
-// Number of tile (a, b), a <= b, of t x t, and the q-th tile.
-__host__ __device__ constexpr int upper_index(int t, int a, int b) {
-  return a * t - a * (a - 1) / 2 + (b - a);
-}
+// Number of tile (a, b), a <= b: column by column, so that the tiles of a smaller
+// matrix are the first ones of a larger.
+__host__ __device__ constexpr int upper_index(int a, int b) { return b * (b + 1) / 2 + a; }
 
-__device__ __forceinline__ void upper_tile(int t, int q, int& a, int& b) {
-  a = 0;
-  while (q >= t - a) q -= t - a++;
-  b = a + q;
+__device__ __forceinline__ void upper_tile(int q, int& a, int& b) {
+  b = 0;
+  while (q > b) q -= ++b;
+  a = q;
 }
 
 struct MuonArgs {
@@ -198,7 +197,7 @@ __device__ __forceinline__ void gram_blocks(const MuonMatrix& mat, const MuonArg
           if (kT < 4 || 16 * y < r)
 #pragma unroll
             for (int x = 0; x <= y; ++x)
-              acc[upper_index(kT, x, y)] = mfma64(f[x], f[y], acc[upper_index(kT, x, y)]);
+              acc[upper_index(x, y)] = mfma64(f[x], f[y], acc[upper_index(x, y)]);
       }
     }
   };
@@ -234,10 +233,12 @@ __global__ __launch_bounds__(kThreads) void muon_gram_kernel(const MuonMatrix* _
     gram_blocks<kT, false, true, G>(mat, a, start, end, wave, acc);
   else
     gram_blocks<kT, false, false, G>(mat, a, start, end, wave, acc);
-  // the waves' sums, 4 tiles at a time, one per wave
+  // the waves' sums, 4 tiles at a time, one per wave; those that r reaches
+  const int rows = (mat.r + 15) / 16, tiles = rows * (rows + 1) / 2;
   f64x4_t* part = reinterpret_cast<f64x4_t*>(ws + mat.part + c.index * (kTiles * 256));
 #pragma unroll
   for (int q0 = 0; q0 < kTiles; q0 += kWaves) {
+    if (kT >= 4 && q0 >= tiles) break;
     if (q0 > 0) __syncthreads();
 #pragma unroll
     for (int q = q0; q < q0 + kWaves && q < kTiles; ++q)
@@ -263,9 +264,9 @@ __device__ __forceinline__ f64x4_t tile_product(const double* x, const double* y
   for (int c = 0; c < kN; ++c) {
     // X(a, c)[li][4 s + lg] and Y(c, b)[4 s + lg][li], or the other half's
     const bool xu = a <= c, yu = c <= b;
-    const double* px = x + upper_index(kN, xu ? a : c, xu ? c : a) * kStepTile +
+    const double* px = x + upper_index(xu ? a : c, xu ? c : a) * kStepTile +
                        (xu ? li * kStepPitch + lg : lg * kStepPitch + li);
-    const double* py = y + upper_index(kN, yu ? c : b, yu ? b : c) * kStepTile +
+    const double* py = y + upper_index(yu ? c : b, yu ? b : c) * kStepTile +
                        (yu ? lg * kStepPitch + li : li * kStepPitch + lg);
     const int dx = xu ? 4 : 4 * kStepPitch, dy = yu ? 4 * kStepPitch : 4;
 #pragma unroll
@@ -301,9 +302,9 @@ __device__ __forceinline__ void tile_steps(const MuonMatrix& mat, const MuonArgs
   for (int d = 0; d < kOwn; ++d) {
     const int n = wave + kWavesOf * d;
     have[d] = n < kTiles;
-    upper_tile(kN, have[d] ? n : 0, ta[d], tb[d]);
+    upper_tile(have[d] ? n : 0, ta[d], tb[d]);
     const f64x4_t* part = reinterpret_cast<const f64x4_t*>(ws + mat.part) +
-                          upper_index(kT, ta[d], tb[d]) * 64 + lane;
+                          upper_index(ta[d], tb[d]) * 64 + lane;
     constexpr int kStride = upper_tiles(kT) * 64;
     f64x4_t sum = f64x4_t{0.0, 0.0, 0.0, 0.0};
     int i = 0;
