@@ -612,10 +612,10 @@ int64_t muon_chunk_runs(const MuonShape& s, int64_t total_runs) {
 }
 
 // The last pass takes the steps' result once per workgroup, which for up to 16
-// rows means to compute it (448 matrices of 16 x 4096: 3072 workgroups 113-125 us,
+// rows means to compute it (448 matrices of 16 x 4096: 3200 workgroups 113-125 us,
 // 8192 145; of 64 x 4096: 8192 543-632, 2048 685).
 int64_t muon_span_runs(const MuonShape& s, int64_t total_runs) {
-  return muon_runs_of(s, total_runs, s.tiles == 1 ? 3072 : 8192, false);
+  return muon_runs_of(s, total_runs, s.tiles == 1 ? 3200 : 8192, false);
 }
 
 int64_t muon_sums(const MuonShape& s) { return s.tiles * (s.tiles + 1) / 2 * 256; }  // doubles
