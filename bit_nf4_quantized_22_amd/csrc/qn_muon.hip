@@ -253,7 +253,11 @@ __global__ __launch_bounds__(kThreads) void muon_gram_kernel(const MuonMatrix* _
 
 // The steps on one matrix's S, a workgroup each: wave w holds the tiles w, w + W,
 // ... of S, Q and T in registers (of the kN x kN that r reaches: 5 x 5 for r =
-// 74), and products read their operands, two at a time, from LDS.
+// 74), and products read their operands, two at a time, from LDS.  A diagonal tile
+// goes there by its upper half, as the whole matrix does by its upper tiles: with
+// the products' own lower halves, which rounding makes others, T mixed directions
+// that u has with those that it has not (r = 64, u of rank one, 12 steps: X off by
+// 1.2 instead of 6e-6, 8 steps 2e-6 instead of 3e-11).
 constexpr int kStepPitch = 17, kStepTile = 16 * kStepPitch;  // doubles
 
 template <int kN>
@@ -329,11 +333,17 @@ __device__ __forceinline__ void tile_steps(const MuonMatrix& mat, const MuonArgs
 
   auto store = [&](double* to, const f64x4_t (&m)[kOwn]) {
 #pragma unroll
-    for (int d = 0; d < kOwn; ++d)
-      if (have[d])
+    for (int d = 0; d < kOwn; ++d) {
+      if (!have[d]) continue;
+      double* tile = to + (wave + kWavesOf * d) * kStepTile;
+      const bool diagonal = ta[d] == tb[d];
 #pragma unroll
-        for (int v = 0; v < 4; ++v)
-          to[(wave + kWavesOf * d) * kStepTile + (4 * v + lg) * kStepPitch + li] = m[d][v];
+      for (int v = 0; v < 4; ++v) {
+        const int i = 4 * v + lg;
+        if (!diagonal || i <= li) tile[i * kStepPitch + li] = m[d][v];
+        if (diagonal && i < li) tile[li * kStepPitch + i] = m[d][v];
+      }
+    }
   };
   auto product = [&](f64x4_t (&to)[kOwn]) {
 #pragma unroll
@@ -388,7 +398,7 @@ __device__ __forceinline__ void tile_steps(const MuonMatrix& mat, const MuonArgs
     for (int v = 0; v < 4; ++v) {
       const int i = 16 * ta[d] + 4 * v + lg, j = 16 * tb[d] + li;
       const double w = x[d][v] * inv;
-      if (have[d]) {
+      if (have[d] && i <= j) {
         out[factor_place<kT>(mat.tall, i, j)] = w;
         out[factor_place<kT>(mat.tall, j, i)] = w;
       }

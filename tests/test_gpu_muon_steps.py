@@ -1,0 +1,44 @@
+"""The Muon step at the largest counts of Newton-Schulz steps that it takes, on
+updates that have no part in most directions, or parts over 10 decades (GPU)."""
+
+import numpy as np
+import pytest
+import torch
+
+import bit_nf4_quantized_22_amd as qn
+from oracle import muon
+from tests.gpu_helpers import to_np
+from tests.muon_bounds import LARGEST, steps_bound
+from tests.test_gpu_muon import Case, U
+
+pytestmark = pytest.mark.gpu
+
+# every class of smaller sides, wide and tall
+SHAPES = [(16, 700), (700, 16), (5, 300), (31, 500), (64, 1500), (1000, 48), (128, 300), (333, 97)]
+
+
+@pytest.mark.parametrize("kind", ["rank one", "steep", "zero", "falling"])
+@pytest.mark.parametrize("ns,most", LARGEST)
+def test_largest_counts(ns, most, kind):
+    """The fp32 bounds of the step, and on X what 64 bits leave of S0: a sum has at
+    most 64 elements of a chunk's 256 in a wave, 4 waves and 12 chunks."""
+    f = np.float32
+    lr, mu, eps = np.float64(f(2e-3)), np.float64(f(0.95)), np.float64(f(1e-7))
+    om = np.float64(f(1 - mu))
+    for steps in (5, most // 2, most):
+        c = Case(SHAPES, 21, kinds=(kind,), momentum=kind != "rank one")
+        qn.lora_muon_multi_step(c.table, lr=2e-3, weight_decay=0.0, ns_coefficients=ns,
+                                ns_steps=steps)
+        torch.cuda.synchronize()
+        for i, (rows, cols) in enumerate(SHAPES):
+            m1, p1 = (to_np(t).astype(np.float64) for t in (c.m[i], c.p[i]))
+            p0 = c.p0[i].astype(np.float64)
+            gs = (c.g[i].astype(f) * f(om)).astype(np.float64)
+            u = (m1 * mu + gs).astype(f).astype(np.float64)
+            x = muon.orthogonalised(u, eps, ns, steps)
+            size = lr * muon.factor("original", rows, cols)
+            want = p0 - size * x
+            bound = np.linalg.norm(U * (2 * np.abs(p0) + np.abs(want) + 2 * size * np.abs(x)))
+            bound += size * steps_bound(u, ns, steps, chain=64 + 4 + 12, eps=eps)
+            assert np.linalg.norm(p1 - want) <= bound, (rows, cols, steps)
+
