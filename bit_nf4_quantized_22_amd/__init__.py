@@ -1162,7 +1162,8 @@ def lora_muon_multi_step(table, lr=1e-3, momentum=0.95, nesterov=True, weight_de
                          ws=None, stream=None):
     """One in-place Muon step on every matrix of a table.  adjust: "original"
     multiplies the orthogonal update by sqrt(max(1, rows / cols)),
-    "match_rms_adamw" by 0.2 sqrt(max(rows, cols))."""
+    "match_rms_adamw" by 0.2 sqrt(max(rows, cols)).  abs(ns_coefficients[0]) ** (2 *
+    ns_steps) may reach 2**43: 12 steps of the default."""
     torch = _torch()
     dev = table.device
     kinds = {"original": QN_MUON_ORIGINAL, "match_rms_adamw": QN_MUON_MATCH_RMS}

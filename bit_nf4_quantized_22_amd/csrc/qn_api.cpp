@@ -566,6 +566,11 @@ const qn::AdamChunk* adamw_table(const void* table) {
 
 constexpr int64_t kMuonMaxChunks = int64_t{1} << 23;  // 256 threads each, under 2^31
 constexpr int64_t kMuonMaxLong = (int64_t{1} << 24) - 1;
+// Bits by which the steps may raise what rounding leaves of S0's null directions,
+// eigenvalues of 2^-53 or a little more of either sign: ns[0]^2 a step.  A negative
+// one near 1 runs away (12 steps of 3.4445, 42.8 bits: X off by 1e-4 on singular
+// values over 10 decades; 14 steps 2e-2, 16 steps 1e1, 20 steps NaN).
+constexpr double kMuonMaxGrowth = 43.0;
 
 // How a matrix is split; -1 for one that is not offered.
 struct MuonShape {
@@ -1226,6 +1231,8 @@ int lora_muon_multi_step(const qn_muon_plan* plan, const void* table, const qn_m
       step->ns_steps > 32 || !std::isfinite(step->ns[0]) || !std::isfinite(step->ns[1]) ||
       !std::isfinite(step->ns[2]) || (step->nesterov != 0 && step->nesterov != 1))
     return QN_ERR_SHAPE;
+  if (2.0 * step->ns_steps * std::log2(std::fabs(step->ns[0])) > kMuonMaxGrowth)
+    return QN_ERR_UNSUPPORTED;
   if (plan->ws_bytes > 0 && (!ws || ws_bytes < static_cast<size_t>(plan->ws_bytes)))
     return QN_ERR_WORKSPACE;
   if (!aligned(ws, 16)) return QN_ERR_ALIGN;

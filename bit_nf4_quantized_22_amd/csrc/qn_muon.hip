@@ -11,7 +11,8 @@
 // S0 squares the singular values, and the steps raise the least of them by up to
 // a factor of a^2 each, so u u^T, the steps and the last product are in 64
 // bits, on the 64-bit matrix instruction: in 32 bits the least directions would
-// be noise.
+// be noise.  For the same reason the host refuses counts of steps that would raise
+// 64 bits' own noise to the size of X (kMuonMaxGrowth).
 //
 // Rows of r are padded to kT tiles of 16 (1, 2, 4 or 8); a symmetric matrix is
 // its tiles on and above the diagonal.  A wave's 16 x 16 result holds rows 4 v +

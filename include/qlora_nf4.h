@@ -814,7 +814,8 @@ typedef struct qn_muon_plan {
 
 /* Hyperparameters of a step: lr, weight_decay >= 0, 0 <= momentum < 1, eps >
  * 0, ns_steps 1 to 32, ns finite, nesterov 0 or 1, else QN_ERR_SHAPE; another
- * adjust QN_ERR_UNSUPPORTED. */
+ * adjust, and |ns[0]|^(2 ns_steps) past 2^43 (more than 12 steps of 3.4445, 21 of
+ * 2), QN_ERR_UNSUPPORTED. */
 typedef struct qn_muon_step {
   float lr;
   float momentum;
@@ -845,7 +846,9 @@ QN_API int lora_muon_table(const qn_muon_tensor* t, int32_t count, int32_t grad_
  *   rows > cols;  ns_steps times, S = X X^T:  X <- ns[0] X + (ns[1] S + ns[2]
  *   S^2) X;   p <- p (1 - lr wd) - lr f X.
  * m and u are fp32, X's products 64-bit; X is rounded to fp32 once, before it
- * moves p.  Sums are taken in a fixed order: results are bit-reproducible for a
+ * moves p.  The steps run on X X^T, which holds a direction of u as the square of
+ * its part of |u|: up to |ns[0]|^(2 ns_steps) = 2^30 this costs X less than its
+ * rounding, at 2^43 the directions of about 2^-21 |u| are off by up to 1e-4.  Sums are taken in a fixed order: results are bit-reproducible for a
  * table.  u = 0 gives X = 0.  A NaN or infinite gradient makes its whole matrix
  * NaN and touches no other.
  *   ws  device workspace, 16-byte aligned, of at least

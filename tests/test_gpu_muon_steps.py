@@ -42,3 +42,13 @@ def test_largest_counts(ns, most, kind):
             bound += size * steps_bound(u, ns, steps, chain=64 + 4 + 12, eps=eps)
             assert np.linalg.norm(p1 - want) <= bound, (rows, cols, steps)
 
+
+def test_more_steps_are_refused_and_change_nothing():
+    c = Case([(16, 700)], 22, kinds=("rank one",))
+    for kw in ({"ns_steps": 13}, {"ns_steps": 32},
+               {"ns_steps": 24, "ns_coefficients": (1.875, -1.25, 0.375)}):
+        with pytest.raises(qn.QnError) as e:
+            qn.lora_muon_multi_step(c.table, **kw)
+        assert e.value.status == qn.QN_ERR_UNSUPPORTED
+    torch.cuda.synchronize()
+    assert np.array_equal(to_np(c.p[0]), c.p0[0]) and np.array_equal(to_np(c.m[0]), c.m0[0])
