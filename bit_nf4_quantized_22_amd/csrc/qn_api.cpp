@@ -564,7 +564,10 @@ const qn::AdamChunk* adamw_table(const void* table) {
 
 // --- Muon over many matrices ----------------------------------------------
 
-constexpr int64_t kMuonMaxChunks = int64_t{1} << 23;  // 256 threads each, under 2^31
+// Chunks and spans of a table, at least one of each for a matrix: the first pass
+// has 256 threads a chunk, the last up to 512 a span, the steps up to 768 a matrix,
+// each launch less than 2^32.
+constexpr int64_t kMuonMaxChunks = int64_t{1} << 23;
 constexpr int64_t kMuonMaxLong = (int64_t{1} << 24) - 1;
 // Bits by which the steps may raise what rounding leaves of S0's null directions,
 // eigenvalues of 2^-53 or a little more of either sign: ns[0]^2 a step.  A negative
@@ -623,7 +626,9 @@ int64_t muon_span_runs(const MuonShape& s, int64_t total_runs) {
   return muon_runs_of(s, total_runs, s.tiles == 1 ? 3200 : 8192, false);
 }
 
-int64_t muon_sums(const MuonShape& s) { return s.tiles * (s.tiles + 1) / 2 * 256; }  // doubles
+// Doubles of a chunk's sums and of a matrix's left factor, of `tiles` tiles of rows.
+int64_t muon_sums(int64_t tiles) { return tiles * (tiles + 1) / 2 * 256; }
+int64_t muon_factor(int64_t tiles) { return tiles * tiles * 256; }
 
 // Matrices and chunks by class, table and workspace of `count` matrices.
 int muon_sizes(const qn_muon_tensor* t, int32_t count, qn_muon_plan& plan, int64_t& total_runs) {
@@ -645,7 +650,7 @@ int muon_sizes(const qn_muon_tensor* t, int32_t count, qn_muon_plan& plan, int64
     plan.spans[s.cls] += spans;
     ++matrices;
     chunks += n + spans;
-    doubles += n * muon_sums(s) + 256 * s.tiles * s.tiles;
+    doubles += n * muon_sums(s.tiles) + muon_factor(s.tiles);
     if (chunks >= kMuonMaxChunks) return QN_ERR_SHAPE;
   }
   plan.bytes = matrices * static_cast<int64_t>(sizeof(qn::MuonMatrix)) +
@@ -657,7 +662,7 @@ int muon_sizes(const qn_muon_tensor* t, int32_t count, qn_muon_plan& plan, int64
 int check_muon_plan(const qn_muon_plan* plan, const void* table) {
   if (!plan) return QN_ERR_NULL;
   if (plan->grad_dtype != QN_F32 && plan->grad_dtype != QN_BF16) return QN_ERR_UNSUPPORTED;
-  int64_t matrices = 0, chunks = 0;
+  int64_t matrices = 0, chunks = 0, doubles = 0;
   for (int k = 0; k < qn::kMuonClasses; ++k) {
     const int64_t m = plan->matrices[k], c = plan->chunks[k], s = plan->spans[k];
     if (m < 0 || c < m || c >= kMuonMaxChunks || s < m || s >= kMuonMaxChunks ||
@@ -665,8 +670,9 @@ int check_muon_plan(const qn_muon_plan* plan, const void* table) {
       return QN_ERR_SHAPE;
     matrices += m;
     chunks += c + s;
+    doubles += c * muon_sums(qn::kMuonTiles[k]) + m * muon_factor(qn::kMuonTiles[k]);
   }
-  if (plan->ws_bytes < 0 ||
+  if (chunks >= kMuonMaxChunks || plan->ws_bytes != doubles * 8 ||
       plan->bytes != matrices * static_cast<int64_t>(sizeof(qn::MuonMatrix)) +
                          chunks * static_cast<int64_t>(sizeof(qn::MuonChunk)))
     return QN_ERR_SHAPE;
@@ -1202,13 +1208,13 @@ int lora_muon_table(const qn_muon_tensor* t, int32_t count, int32_t grad_dtype, 
       const int64_t per = muon_chunk_runs(s, total_runs), per2 = muon_span_runs(s, total_runs);
       const int32_t n = static_cast<int32_t>(qn::mx_tiles(s.runs, per));
       const int32_t n2 = static_cast<int32_t>(qn::mx_tiles(s.runs, per2));
-      const int64_t factor = at + n * muon_sums(s);
+      const int64_t factor = at + n * muon_sums(s.tiles);
       *mats++ = qn::MuonMatrix{t[i].p, t[i].g, t[i].m, t[i].p_bf16, s.len, per * s.run,
                                per2 * s.run, at, factor, static_cast<int32_t>(s.r),
                                t[i].rows > t[i].cols ? 1 : 0, n, n2};
       for (int32_t c = 0; c < n; ++c) *chunk++ = qn::MuonChunk{index, c};
       for (int32_t c = 0; c < n2; ++c) *span++ = qn::MuonChunk{index, c};
-      at = factor + 256 * s.tiles * s.tiles;
+      at = factor + muon_factor(s.tiles);
       ++index;
     }
     chunk = span;

@@ -832,7 +832,8 @@ typedef struct qn_muon_step {
  * lora_adamw_table_bytes and lora_adamw_table: check the matrices and write the
  * table to host memory (8-byte aligned), which the caller copies to the device
  * (16-byte aligned) once.  Memory that a step writes must not overlap any other
- * operand of the table (QN_ERR_SHAPE); less than 2^23 chunks in all.
+ * operand of the table (QN_ERR_SHAPE); less than 2^23 chunks and spans
+ * in all.
  */
 QN_API size_t lora_muon_table_bytes(const qn_muon_tensor* t, int32_t count);
 QN_API int lora_muon_table(const qn_muon_tensor* t, int32_t count, int32_t grad_dtype, void* table,
