@@ -254,11 +254,12 @@ __global__ __launch_bounds__(kThreads) void muon_gram_kernel(const MuonMatrix* _
 
 // The steps on one matrix's S, a workgroup each: wave w holds the tiles w, w + W,
 // ... of S, Q and T in registers (of the kN x kN that r reaches: 5 x 5 for r =
-// 74), and products read their operands, two at a time, from LDS.  A diagonal tile
-// goes there by its upper half, as the whole matrix does by its upper tiles: with
-// the products' own lower halves, which rounding makes others, T mixed directions
-// that u has with those that it has not (r = 64, u of rank one, 12 steps: X off by
-// 1.2 instead of 6e-6, 8 steps 2e-6 instead of 3e-11).
+// 74), and products read their operands, two at a time, from LDS.  The diagonal
+// tiles of S and Q go there by their upper halves, as the whole matrix does by its
+// upper tiles: with the products' own lower halves, which rounding makes others, T
+// mixed directions that u has with those that it has not (r = 64, u of rank one, 12
+// steps: X off by 1.2 instead of 6e-6, 8 steps 2e-6 instead of 3e-11; T's and S Q's
+// lower halves may stay).
 constexpr int kStepPitch = 17, kStepTile = 16 * kStepPitch;  // doubles
 
 template <int kN>
@@ -332,12 +333,13 @@ __device__ __forceinline__ void tile_steps(const MuonMatrix& mat, const MuonArgs
   for (int i = 0; i < 16 * kN; ++i) norm2 += s_diag[i];
   const double inv = 1.0 / (sqrt(norm2) + static_cast<double>(a.eps));
 
-  auto store = [&](double* to, const f64x4_t (&m)[kOwn]) {
+  // (by_upper: of a diagonal tile the upper half, to both places)
+  auto store = [&](double* to, const f64x4_t (&m)[kOwn], bool by_upper) {
 #pragma unroll
     for (int d = 0; d < kOwn; ++d) {
       if (!have[d]) continue;
       double* tile = to + (wave + kWavesOf * d) * kStepTile;
-      const bool diagonal = ta[d] == tb[d];
+      const bool diagonal = by_upper && ta[d] == tb[d];
 #pragma unroll
       for (int v = 0; v < 4; ++v) {
         const int i = 4 * v + lg;
@@ -358,7 +360,7 @@ __device__ __forceinline__ void tile_steps(const MuonMatrix& mat, const MuonArgs
   }
   for (int n = 0; n < a.steps; ++n) {
     // Q = a I + b S + c S^2
-    store(s_x, s);
+    store(s_x, s, true);
     __syncthreads();
 #pragma unroll
     for (int d = 0; d < kOwn; ++d) {
@@ -369,7 +371,7 @@ __device__ __forceinline__ void tile_steps(const MuonMatrix& mat, const MuonArgs
         q[d][v] = a.cc * s2[v] + a.cb * s[d][v] +
                   (ta[d] == tb[d] && 4 * v + lg == li ? a.ca : 0.0);
     }
-    store(s_y, q);
+    store(s_y, q, true);
     __syncthreads();
     // T Q, and S Q Q unless this was the last step
     f64x4_t r[kOwn];
@@ -379,13 +381,13 @@ __device__ __forceinline__ void tile_steps(const MuonMatrix& mat, const MuonArgs
       for (int d = 0; d < kOwn; ++d) x[d] = q[d];
     } else {
       __syncthreads();
-      store(s_x, x);
+      store(s_x, x, false);
       __syncthreads();
       product(x);
     }
     if (n + 1 < a.steps) {
       __syncthreads();
-      store(s_x, r);
+      store(s_x, r, false);
       __syncthreads();
       product(s);
       __syncthreads();
