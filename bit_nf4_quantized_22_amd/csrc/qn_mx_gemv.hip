@@ -295,14 +295,17 @@ __global__ __launch_bounds__(64 * kWaves) void mx_decode_kernel(
 }  // namespace
 
 // Past 16 tokens x's codes, which every workgroup reads, are what counts; past 64
-// MiB of them in all the tiles of the large batches cost less.  17 to 32 tokens, this
-// kernel and the tiles: 4096 x 4096 13.6 and 18.1 us, 4096 x 11008 22.8 and 24.5, 8192
-// x 8192 22.3 and 23.8, but 22016 x 8192 44 and 36; 33 to 64: 4096 x 4096 15.8 and
-// 20.2, but 4096 x 11008 28.8 and 27.0, 8192 x 8192 35.6 and 25.6.
+// MiB of them in all the tiles of the large batches cost less, and from 33 tokens,
+// with 16 rows of columns a workgroup, past two rounds of the CUs.  This kernel and
+// the tiles, us: 17 to 32 tokens 4096 x 4096 12.5-13.2 and 17-18, 4096 x 11008 21-23 and
+// 23-25, 8192 x 8192 21-22 and 24, 16384 x 4096 18-19 and 22, but 22016 x 8192 37-40 and
+// 36; 33 to 64 tokens 4096 x 4096 14-16 and 19-20, 4096 x 8192 20-23 and 22-26, 8192 x
+// 4096 19-23 and 20-23, but 4096 x 11008 25-29 and 25-27, 8192 x 8192 30-36 and 25-27,
+// 11008 x 1024 18-19 and 14-15, 28672 x 1024 33-35 and 15-16.
 bool mx_few(int64_t M, int64_t N, int64_t K) {
   const int64_t cols = N > 4096 ? N : 4096;
-  return M <= kFp8DecodeM ||
-         (M <= kFp8FewM && (M + 15) / 16 * cols * K / 2 <= (int64_t{64} << 20));
+  return M <= kFp8DecodeM || (M <= kFp8FewM && (M <= 32 || N <= 8192) &&
+                              (M + 15) / 16 * cols * K / 2 <= (int64_t{64} << 20));
 }
 
 // Every workgroup reads A, from the caches: past 32 MiB in all, or 128 KB each, a
@@ -346,11 +349,11 @@ hipError_t launch_mx_decode(const MxView& w, const uint8_t* x, const uint8_t* xs
     return hipGetLastError();
   };
   // Two rows of columns a workgroup halve the reads of x, where half the workgroups
-  // still keep the chip busy; 16 tokens, one row and two: 4096 x 4096 10.8 and 11.8 us,
-  // 6144 x 4096 15.2 and 12.1, 8192 x 2048 13.6 and 10.8, 22016 x 8192 46 and 38.
+  // still keep the chip busy; 16 tokens, one row and two, 8 waves: 4096 x 4096 10.5 and
+  // 11.2 us, 6144 x 4096 12.7 and 11.5, 8192 x 8192 17.6 and 16.1, 32 tokens 26.6 and 22.1.
   // Where these are more than the CUs, 4 waves each let more of them reside than 8:
-  // 8 waves and 4, 11008 x 4096 18.3 and 15.7 us, 22016 x 8192 38 and 33, 28672 x 1024
-  // 21.7 and 15.6, 32 tokens on 11008 x 4096 20.9 and 19.3; but 8192 x 8192 17.2 and 17.9.
+  // 8 waves and 4, 11008 x 4096 16.8 and 14.7 us, 22016 x 8192 34.7 and 30.8, 28672 x 1024
+  // 18.5 and 13.9, 32 tokens on 11008 x 4096 19.8 and 18.9; but 8192 x 8192 16.1 and 18.2.
   const int64_t pairs = (w.N + 31) / 32;
   if (M <= 16)
     return pairs > 256   ? go(mx_decode_kernel<4, 1, 2>, 4, 2)
