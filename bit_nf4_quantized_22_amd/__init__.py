@@ -1169,6 +1169,8 @@ def lora_muon_multi_step(table, lr=1e-3, momentum=0.95, nesterov=True, weight_de
     kinds = {"original": QN_MUON_ORIGINAL, "match_rms_adamw": QN_MUON_MATCH_RMS}
     if adjust not in kinds:
         raise ValueError(f"adjust: one of {sorted(kinds)}")
+    if len(ns_coefficients) != 3:
+        raise ValueError("ns_coefficients: need three")
     step = qn_muon_step(lr, momentum, weight_decay, eps,
                         (ctypes.c_double * 3)(*ns_coefficients), ns_steps, int(bool(nesterov)),
                         kinds[adjust])
