@@ -830,13 +830,13 @@ def fp8_matmul(fw, codes, scale, transposed=False, out=None, ws=None, stream=Non
 def fp8_linear_fwd(fw, x, A, B, r, alpha, y=None, u_out=None, ws=None, stream=None):
     """y = Q(x) W^T + (alpha/r) (x A^T) B^T on an Fp8Weight (bf16 in/out)."""
     return _scaled_linear("fp8_linear_fwd", QN_OP_FP8_FWD, fw, x, fw.K, fw.N, A, B, r, alpha, y,
-                       u_out, ws, stream)
+                          u_out, ws, stream)
 
 
 def fp8_linear_bwd_dx(fw, dy, A, B, r, alpha, dx=None, t_out=None, ws=None, stream=None):
     """dx = Q(dy) W + (alpha/r) (dy B) A on an Fp8Weight (bf16 in/out)."""
     return _scaled_linear("fp8_linear_bwd_dx", QN_OP_FP8_BWD_DX, fw, dy, fw.N, fw.K, A, B, r, alpha,
-                       dx, t_out, ws, stream)
+                          dx, t_out, ws, stream)
 
 
 def _scaled_linear(fn, op, fw, x, L, n, A, B, r, alpha, out, low, ws, stream):
@@ -992,13 +992,13 @@ def mxfp4_matmul(mw, codes, scale, out=None, ws=None, stream=None):
 def mxfp4_linear_fwd(mw, x, A, B, r, alpha, y=None, u_out=None, ws=None, stream=None):
     """y = Q(x) W^T + (alpha/r) (x A^T) B^T on an Mxfp4Weight (bf16 in/out)."""
     return _scaled_linear("mxfp4_linear_fwd", QN_OP_MXFP4_FWD, mw, x, mw.K, mw.N, A, B, r, alpha, y,
-                       u_out, ws, stream)
+                          u_out, ws, stream)
 
 
 def mxfp4_linear_bwd_dx(mw, dy, A, B, r, alpha, dx=None, t_out=None, ws=None, stream=None):
     """dx = Q8(dy) W + (alpha/r) (dy B) A on an Mxfp4Weight (bf16 in/out)."""
     return _scaled_linear("mxfp4_linear_bwd_dx", QN_OP_MXFP4_BWD_DX, mw, dy, mw.N, mw.K, A, B, r,
-                       alpha, dx, t_out, ws, stream)
+                          alpha, dx, t_out, ws, stream)
 
 
 # --- AdamW over many matrices ----------------------------------------------

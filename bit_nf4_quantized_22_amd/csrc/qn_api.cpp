@@ -612,16 +612,19 @@ int64_t muon_runs_of(const MuonShape& s, int64_t total_runs, int64_t target, boo
 }
 
 // The first pass leaves tiles (tiles + 1) KB of sums per chunk, which are few
-// for up to 32 rows and short chunks fill the chip more evenly (448 matrices of
-// 16 x 4096: 4096 workgroups 54-59 us, 1536 65; of 64 x 4096: 2048 269-288 and
-// steps of 80, 8192 297 and 100).
+// for up to 32 rows.  Targets, the chunks that they give, and times: a step on all
+// adapters of a 7B model, r = 32, 2048 (2272) 596-601 us, 4096 (4192) 585-589, 8192
+// (6656) 587-588, r = 16 the same within 1%; 448 matrices of 64 x 4096, 2048 (2240)
+// first pass 287-297 us and steps 80-86, 8192 (7168) 296-301 and 104.
 int64_t muon_chunk_runs(const MuonShape& s, int64_t total_runs) {
   return muon_runs_of(s, total_runs, s.tiles <= 2 ? 4096 : 2048, true);
 }
 
 // The last pass takes the steps' result once per workgroup, which for up to 16
-// rows means to compute it (448 matrices of 16 x 4096: 3200 workgroups 113-125 us,
-// 8192 145; of 64 x 4096: 8192 543-632, 2048 685).
+// rows means to compute it.  Targets, the spans that they give, and times: a step on
+// all adapters of a 7B model, r = 4, 3200 (2464) 114-118 us, 4096 (3552) 128, 8192
+// (4928) 139, r = 16 261, 260 and 257; the pass on 448 matrices of 64 x 4096, 8192
+// (7168) 541-643 us, 4096 (3584) 567-671, 2048 (2240) 616-714.
 int64_t muon_span_runs(const MuonShape& s, int64_t total_runs) {
   return muon_runs_of(s, total_runs, s.tiles == 1 ? 3200 : 8192, false);
 }

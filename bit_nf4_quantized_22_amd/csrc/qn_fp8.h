@@ -75,6 +75,8 @@ __device__ __forceinline__ uint32_t lanes_max(uint32_t x) {
   return x;
 }
 
+typedef short i16x4_t __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) i16x4_t lds_i16x4_t;
 typedef int i32x8_t __attribute__((ext_vector_type(8)));
 
 // c + a b^T of 16 x 128 E4M3 fragments: lane l gives row l % 16 of a and of

@@ -299,7 +299,8 @@ struct MuonMatrix {
   int64_t span;     // and in a span
   int64_t part;     // in the workspace, in doubles: the chunks' sums
   int64_t factor;   // and the product's left factor
-  int32_t r, tall, chunks, spans;
+  int32_t r, tall, chunks;
+  int32_t spans;    // for readers of the table on the host: a span names itself
 };
 struct MuonChunk {
   int32_t matrix;  // in the table

@@ -21,14 +21,14 @@
 // operand of its transpose.
 //
 // Bound by HBM: 8 bytes an element in the first pass, 22 in the last.  448
-// matrices of 16 x 4096 (29 M elements): 59 us (4.0 TB/s) and 115 us (5.6 TB/s,
-// part of it from the last-level cache), the steps among them; of 64 x 4096 (117
-// M): 299 us (3.1 TB/s), the steps 86 us, 542 us (4.8 TB/s).  All adapters of a 7B
-// model: r = 16 256 us, r = 64 1.30 ms, 0.95 at a large copy's rate.  Up to r = 64 the
-// matrix instructions would take a third of these times; at r = 128 (100 matrices
-// of 128 x 4096, 52 M) they are half of them: 290, 224 and 426 us.  The steps of a
-// matrix are one CU's work, and above 32 rows its 64-bit rate bounds them (15
-// matrices: 64 rows 34 us, 74 rows 62, 128 rows 214, for 17 products each).
+// matrices of 16 x 4096 (29 M elements): 58 us (4.0 TB/s) and 116-122 us (5.3-5.6
+// TB/s, part of it from the last-level cache), the steps among them; of 64 x 4096 (117
+// M): 297 us (3.2 TB/s), the steps 86 us, 540 us (4.8 TB/s), of 4096 x 64 643 us.  All
+// adapters of a 7B model: r = 16 256 us, r = 64 1.30 ms, 0.95 at a large copy's rate.  Up
+// to r = 64 the matrix instructions would take a third of these times; at r = 128 (100
+// matrices of 128 x 4096, 52 M) they are half of them: 300, 234 and 442 us.  The steps
+// of a matrix are one CU's work, and above 32 rows its 64-bit rate bounds them (15
+// matrices: 64 rows 36 us, 74 rows 63, 100 rows 190, 128 rows 209, for 17 products each).
 // Few matrices are a chain of latencies: one layer's 14 of r = 16 19 us.
 
 #include <cmath>

@@ -9,9 +9,6 @@
 
 namespace qn {
 
-typedef short i16x4_t __attribute__((ext_vector_type(4)));
-typedef __attribute__((address_space(3))) i16x4_t lds_i16x4_t;
-
 // 8 values as they lie in memory; the bits of their largest magnitude; the
 // values as fp32.
 template <typename T>

@@ -9,8 +9,6 @@
 
 namespace qn {
 
-typedef short i16x4_t __attribute__((ext_vector_type(4)));
-typedef __attribute__((address_space(3))) i16x4_t lds_i16x4_t;
 typedef __attribute__((address_space(3))) uint8_t lds_u8_t;
 
 // Slot of 16-byte chunk c in a 128-byte row is c ^ row_swz(row).  A 16-byte
