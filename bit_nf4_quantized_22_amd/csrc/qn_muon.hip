@@ -549,7 +549,10 @@ __device__ __forceinline__ f64x4_t tile_product(f64x4_t x, f64x4_t y) {
 // The steps on one tile, in every workgroup that needs the result and in each of
 // its waves alike, in registers: 17 products of 4 instructions, which costs less
 // than a launch between the passes.  The chunks' sums are added a quarter per
-// wave first.
+// wave first.  T is multiplied from the left: what rounding mixes of u's directions
+// into one that u has not grows like T there, ns[0]^n.  From the right, step n adds
+// Q's rounding, grown by as much, times T's factor there (u of rank one, 12 steps: X
+// off by 3e-4 instead of 1e-9).
 __device__ __forceinline__ void one_tile_steps(const MuonMatrix& mat, const MuonArgs& a,
                                                const double* ws, int wave, double* s_w) {
   __shared__ f64x4_t s_sum[kWaves][64];
@@ -578,7 +581,7 @@ __device__ __forceinline__ void one_tile_steps(const MuonMatrix& mat, const Muon
 #pragma unroll
     for (int v = 0; v < 4; ++v)
       if (4 * v + lg == li) q[v] += a.ca;
-    x = n == 0 ? q : tile_product(x, q);
+    x = n == 0 ? q : tile_product(q, x);
     s = tile_product(tile_product(s, q), q);
   }
 #pragma unroll

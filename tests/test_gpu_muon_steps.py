@@ -43,6 +43,31 @@ def test_largest_counts(ns, most, kind):
             assert np.linalg.norm(p1 - want) <= bound, (rows, cols, steps)
 
 
+@pytest.mark.parametrize("ns,most", LARGEST)
+def test_updates_of_exactly_rank_one(ns, most):
+    """Products of integers: u is its own fp32 number, and X = f(1) u / |u| has no
+    part in any other direction, whatever T makes of these."""
+    rng = np.random.default_rng(23)
+    eps = np.float64(np.float32(1e-7))
+    for shape in SHAPES + [(1, 40), (2, 4096), (16, 4096), (4096, 16), (100, 16), (17, 900)]:
+        g = np.outer(rng.integers(1, 2 ** 11, shape[0]), rng.integers(1, 2 ** 12, shape[1]))
+        g = (g * 2.0 ** -30).astype(np.float32)
+        p = torch.zeros(shape, device="cuda:0")
+        table = qn.lora_muon_table([p], [torch.from_numpy(g).to(p.device)], [torch.zeros_like(p)])
+        u = g.astype(np.float64)
+        for steps in (5, 8, most):
+            p.zero_()
+            table.tensors[2][0].zero_()
+            qn.lora_muon_multi_step(table, lr=1.0, momentum=0.0, weight_decay=0.0,
+                                    ns_coefficients=ns, ns_steps=steps)
+            torch.cuda.synchronize()
+            size = muon.factor("original", *shape)
+            want = -size * muon.orthogonalised(u, eps, ns, steps)
+            bound = 3 * U * np.linalg.norm(want)
+            bound += size * steps_bound(u, ns, steps, chain=64 + 4 + 32, eps=eps)
+            assert np.linalg.norm(to_np(p) - want) <= bound, (shape, steps)
+
+
 def test_more_steps_are_refused_and_change_nothing():
     c = Case([(16, 700)], 22, kinds=("rank one",))
     for kw in ({"ns_steps": 13}, {"ns_steps": 32},
